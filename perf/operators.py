@@ -66,6 +66,11 @@ def _mult(rng, lo, hi, m):
     return max(m, _log_int(rng, lo, hi) // m * m)
 
 
+def _width(rng, act, fp8, most):
+    """Output features; FP8 SwiGLU has whole scale blocks of gate and of up rows."""
+    return _mult(rng, 128, most, 128) if fp8 and act == "swiglu" else _log_int(rng, 16, most)
+
+
 def draw(rng):
     op = rng.choice(["route", "route_grad", "linear", "linear_grad", "grouped", "grouped", "packed", "grouped_grad"])
     if op == "route" or op == "route_grad":
@@ -83,7 +88,7 @@ def draw(rng):
     if op == "linear":
         fp8 = rng.random() < 0.25
         return dict(op=op, T=_log_int(rng, 1, 4096), I=_mult(rng, 128, 7168, 128 if fp8 else 8),
-                    O=_log_int(rng, 16, 4096), act=act, bias=rng.random() < 0.5, residual=rng.random() < 0.5,
+                    O=_width(rng, act, fp8, 4096), act=act, bias=rng.random() < 0.5, residual=rng.random() < 0.5,
                     out="bf16" if fp8 else rng.choice(["bf16", "f32"]), fp8=fp8)
     if op == "linear_grad":
         return dict(op=op, T=_log_int(rng, 1, 4096), I=_mult(rng, 64, 4096, 8), O=_log_int(rng, 16, 2048), act=act,
@@ -92,7 +97,7 @@ def draw(rng):
         return dict(op=op, G=_log_int(rng, 1, 32), rows=_log_int(rng, 1, 8192), skew=rng.uniform(0, 1),
                     I=_mult(rng, 64, 2048, 8), O=_log_int(rng, 16, 2048), act=act, bias=rng.random() < 0.5)
     fp8 = rng.random() < 0.5
-    c = dict(op=op, G=_log_int(rng, 1, 48), I=_mult(rng, 128, 4096, 128 if fp8 else 8), O=_log_int(rng, 16, 2048),
+    c = dict(op=op, G=_log_int(rng, 1, 48), I=_mult(rng, 128, 4096, 128 if fp8 else 8), O=_width(rng, act, fp8, 2048),
              act=act, bias=rng.random() < 0.5, fp8=fp8)
     if op == "packed":
         c.update(cap=_log_int(rng, 1, 256), fill=rng.uniform(0.05, 1.0))
