@@ -26,7 +26,9 @@ Rank-granular path (normal mode, one row per (token, flagged rank)):
 FP8 payload: per_token_cast_to_fp8 / per_token_cast_back; every dispatch
 accepts and returns (codes, scales) tuples, and dispatch(..., cast_fp8=fmt)
 casts on the way. Fixed-capacity packed layout (low-latency dispatch):
-low_latency_dispatch / low_latency_combine. copy_(dst, src) is libcgd's plain
+low_latency_dispatch / low_latency_combine. The router and the experts'
+products around these calls (route, grouped_linear, linear and their
+gradients) are in experts.py. copy_(dst, src) is libcgd's plain
 16-byte copy, the measured copy ceiling the bandwidths are compared with.
 
 The calls follow the DeepEP-style Buffer API described by the DeepEP Python
@@ -50,7 +52,8 @@ __all__ = ["get_dispatch_layout", "dispatch", "dispatch_plan", "dispatch_apply",
            "PackedHandle", "low_latency_dispatch", "layout_and_low_latency_dispatch", "low_latency_combine", "layout_and_dispatch_plan", "copy_",
            "layout_and_normal_dispatch_plan", "layout_and_dispatch", "normal_workspace_bytes",
            "layout_and_normal_workspace_bytes", "empty_", "layout_and_dispatch_noalloc", "init",
-           "layout_and_normal_dispatch"]
+           "layout_and_normal_dispatch", "route", "route_backward", "linear", "linear_backward", "grouped_linear",
+           "grouped_linear_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _BUILT_LIB = os.path.join(_PKG, "libcgd.so")
@@ -87,7 +90,7 @@ def load():
             raise FileNotFoundError(f"CGD_LIBRARY names {_LIB_PATH}, which does not exist")
         from . import build as _build
         _build.build()
-    _lib = configure(ctypes.CDLL(_LIB_PATH))
+    _lib = _configure_experts(configure(ctypes.CDLL(_LIB_PATH)))
     return _lib
 
 
@@ -1318,3 +1321,8 @@ def low_latency_combine(expert_out: torch.Tensor, topk_weights: torch.Tensor, ha
                lib.cgd_combine(_ptr(expert_out), E * cap, H, _ptr(handle.dst_row), _ptr(topk_weights), T, K,
                                _ptr(out), _stream(dev)))
     return out
+
+
+# The operators that compute around these moves (they use the helpers above).
+from .experts import (configure as _configure_experts, grouped_linear, grouped_linear_backward, linear,  # noqa: E402
+                      linear_backward, route, route_backward)

@@ -8,6 +8,7 @@
 #include <mutex>
 #include <string>
 
+#include "cgd_experts_launch.h"
 #include "cgd_launch.h"
 
 namespace {
@@ -80,6 +81,9 @@ int check_scales(const void* scales, int64_t st, int64_t sb, int fmt, bool neede
 }
 
 }  // namespace
+
+// The message of a call checked in another file.
+int cgd::report(int code, const char* message) { return fail(code, "%s", message); }
 
 extern "C" {
 
@@ -1041,6 +1045,11 @@ extern "C" int cgd_init(void) {
     if (err == hipSuccess) err = cgd::preload_fp8();
     if (err == hipSuccess) err = cgd::preload_normal();
     if (err == hipSuccess) err = cgd::preload_layout();
+    if (err == hipSuccess) err = cgd::preload_route();
+    if (err == hipSuccess) err = cgd::preload_gemm();
+    if (err == hipSuccess) err = cgd::preload_gemm_fp8();
+    if (err == hipSuccess) err = cgd::preload_gemm_grad();
+    if (err == hipSuccess) err = cgd::preload_act_grad();
     if (err != hipSuccess) return hip_fail(err, "loading the GPU code");
     return CGD_OK;
 }

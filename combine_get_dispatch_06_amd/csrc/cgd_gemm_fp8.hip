@@ -1,0 +1,21 @@
+// Forward products of the FP8 payload: e4m3 codes with one scale for 128
+// values of a row (fp32, or a UE8M0 byte) against e4m3 weights with one fp32
+// scale for a block of 128 x 128. A step of the reduction is one such block:
+// its 16x16x128 products start from zero and are added in fp32, times both scales.
+#include "cgd_gemm_launch.h"
+
+namespace cgd {
+
+hipError_t launch_forward_fp8(const GemmArgs& a, const GemmPlan& p, bool grouped, hipStream_t stream) {
+    if (p.tile == 0) return launch_gemm<256, 256, 2, 4, 2, false, false, true>(a, grouped, stream);
+    if (p.tile == 1) return launch_gemm<128, 128, 2, 2, 2, false, false, true>(a, grouped, stream);
+    if (p.tile == 2) return launch_gemm<64, 128, 1, 4, 3, false, false, true>(a, grouped, stream);
+    return launch_gemm<32, 128, 1, 4, 3, false, false, true>(a, grouped, stream);
+}
+
+hipError_t preload_gemm_fp8() {
+    hipFuncAttributes at;
+    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&gemm_kernel<128, 128, 2, 2, 2, false, false, true>));
+}
+
+}  // namespace cgd

@@ -1,0 +1,44 @@
+// Gradients of the products.
+//   grad_x[m, i]    = sum_o d[m, o] * W[o, i]   (W read transposed)
+//   grad_W[e][o, i] = sum over e's rows m of d[m, o] * x[m, i]   (both read transposed)
+// A group without rows has zero gradients, which are written.
+#include "cgd_gemm_launch.h"
+
+namespace cgd {
+
+// 256 x 256 tiles once they give most CUs one, smaller ones below that.
+static int input_tile(const Groups& g, bool grouped, int64_t k) {
+    const int64_t per = grouped ? (g.total + g.groups - 1) / g.groups : g.total;
+    if (per > 128 && worst_pieces(g, 256, grouped) * ((k + 255) / 256) >= 200) return 0;
+    return per > 64 ? 1 : 2;
+}
+static int weight_tile(const Groups& g, int64_t width, int64_t k) {
+    return (int64_t)g.groups * ((width + 255) / 256) * ((k + 255) / 256) >= 200 ? 0 : 1;
+}
+
+int64_t grad_blocks(const Groups& g, bool grouped, int64_t width, int64_t k) {
+    const int ti = input_tile(g, grouped, k), tw = weight_tile(g, width, k);
+    const int bm = ti == 0 ? 256 : ti == 1 ? 128 : 64, bn = ti == 0 ? 256 : 128, bw = tw == 0 ? 256 : 128;
+    const int64_t bi = worst_pieces(g, bm, grouped) * ((k + bn - 1) / bn);
+    const int64_t w = (int64_t)g.groups * ((width + bw - 1) / bw) * ((k + bw - 1) / bw);
+    return (bi > w ? bi : w) + 8;
+}
+
+hipError_t launch_input_grad(const GemmArgs& a, bool grouped, hipStream_t stream) {
+    const int tile = input_tile(a.g, grouped, a.n);
+    if (tile == 0) return launch_gemm<256, 256, 2, 4, 2, false, true, false>(a, grouped, stream);
+    if (tile == 1) return launch_gemm<128, 128, 2, 2, 2, false, true, false>(a, grouped, stream);
+    return launch_gemm<64, 128, 1, 4, 3, false, true, false>(a, grouped, stream);
+}
+
+hipError_t launch_weight_grad(const GemmArgs& a, hipStream_t stream) {
+    if (weight_tile(a.g, a.m, a.n) == 0) return launch_gemm<256, 256, 2, 4, 2, true, true, false>(a, true, stream);
+    return launch_gemm<128, 128, 2, 2, 2, true, true, false>(a, true, stream);
+}
+
+hipError_t preload_gemm_grad() {
+    hipFuncAttributes at;
+    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&gemm_kernel<128, 128, 2, 2, 2, true, true, false>));
+}
+
+}  // namespace cgd

@@ -1,0 +1,314 @@
+"""The dense and the grouped products and their gradients against a plain
+computation in 64 bits.
+
+Tolerances, derived before the first run (S = sum of |terms| of a value):
+  - a bf16 result is off by half a step, 2^-8 of the value (fp32: 2^-24);
+  - an fp32 sum of n terms, in any order, by n * 2^-24 * S; an FP8 step of 128
+    products is aligned to its largest product and keeps 23 bits below it,
+    hence 128 * 2^-23 of that product at most, 2^-16 * S over all steps;
+  - bias and residual: one fp32 rounding each, within the same n (n + 3);
+  - activations have slopes within [-0.13, 1.13] and cost some fp32 steps of
+    their own (2^-20 of the value covers exp, erf, the division and products);
+  - a gradient's operand d is rounded to bf16: 2^-8 of each term, 2^-8 * S;
+    its activation slope is good to 2^-20 of (1 + |preact|) * |grad|.
+"""
+import math
+
+import pytest
+import torch
+
+import combine_get_dispatch_06_amd as cgd
+from gpu_util import DEV, say
+
+pytestmark = pytest.mark.gpu
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def _gen(seed):
+    g = torch.Generator().manual_seed(seed)
+    return g
+
+
+def _bf(g, *shape, scale=1.0):
+    return (torch.randn(shape, generator=g, dtype=F32) * scale).to(BF16)
+
+
+def _act64(v, act, O):
+    if act == "relu":
+        return v.clamp_min(0)
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    if act == "gelu":
+        return 0.5 * v * (1 + torch.erf(v / math.sqrt(2)))
+    if act == "swiglu":
+        return v[..., :O] * torch.sigmoid(v[..., :O]) * v[..., O:]
+    return v
+
+
+def _ref(x, w, b, act, O, res=None, steps=2.0 ** -24, extra=3):
+    """-> (value, preact, tolerance before the last rounding, the preact's)."""
+    x, w = x.to(F64), w.to(F64)
+    pre = x @ w.mT
+    S = x.abs() @ w.abs().mT
+    if b is not None:
+        pre = pre + b.to(F64)
+        S = S + b.to(F64).abs()
+    n = x.shape[-1] + extra
+    tpre = (n * steps if steps < 2.0 ** -20 else steps) * S
+    y = _act64(pre, act, O)
+    if act == "swiglu":
+        g, u = pre[..., :O], pre[..., O:]
+        t = 1.13 * tpre[..., :O] * (u.abs() + tpre[..., O:]) + (g * torch.sigmoid(g)).abs() * tpre[..., O:]
+    else:
+        t = (1.13 if act else 1.0) * tpre
+    t = t + y.abs() * 2.0 ** -20
+    if res is not None:
+        y = y + res.to(F64)
+        t = t + (y.abs() + res.to(F64).abs()) * 2.0 ** -23
+    return y, pre, t, tpre
+
+
+def _near(got, want, tol, dtype, what):
+    got = got.to(F64).cpu()
+    bad = ~((got - want).abs() <= tol + HALF[dtype] * (want.abs() + tol) + 2.0 ** -120)
+    if bad.any():
+        i = bad.nonzero()[0].tolist()
+        raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} values off, first at {i}: "
+                             f"{got[tuple(i)]} for {want[tuple(i)]} +- {tol[tuple(i)]}")
+
+
+def _fp8_x(g, *shape, fmt=cgd.SCALE_F32):
+    q = (torch.randn(shape, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+    s = shape[:-1] + (shape[-1] // 128,)
+    if fmt == cgd.SCALE_UE8M0:
+        sc = torch.randint(118, 124, s, generator=g, dtype=torch.uint8)
+        f = torch.exp2(sc.to(F64) - 127)
+    else:
+        sc = torch.rand(s, generator=g) * 0.02 + 0.005
+        f = sc.to(F64)
+    return (q, sc), q.to(F32).to(F64) * f.repeat_interleave(128, -1)
+
+
+def _fp8_w(g, lead, O, K):
+    q = (torch.randn(*lead, O, K, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn)
+    sc = torch.rand(*lead, (O + 127) // 128, K // 128, generator=g) * 0.001 + 0.0002
+    full = sc.to(F64).repeat_interleave(128, -2)[..., :O, :].repeat_interleave(128, -1)
+    return (q, sc), q.to(F32).to(F64) * full
+
+
+def _dev(v):
+    if v is None:
+        return None
+    if isinstance(v, tuple):
+        return tuple(t.to(DEV) for t in v)
+    return v.to(DEV)
+
+
+# one row, odd rows, tile edges; reductions of one piece, of a ragged last piece,
+# long ones; few and odd columns
+@pytest.mark.parametrize("T,K,O", [(1, 8, 1), (1, 7168, 256), (3, 64, 16), (32, 72, 130), (33, 128, 64),
+                                   (64, 1032, 129), (100, 520, 257), (128, 7168, 256), (129, 200, 1003),
+                                   (257, 2048, 384), (777, 136, 515), (2100, 264, 4100), (4096, 320, 4096)])
+@pytest.mark.parametrize("act,bias,res,f32", [(None, False, False, True), (None, True, True, False),
+                                              ("gelu", True, True, False), ("relu", False, False, False),
+                                              ("silu", True, False, True), ("swiglu", True, True, False)])
+def test_linear(T, K, O, act, bias, res, f32):
+    say(f"linear T={T} K={K} O={O} act={act} bias={bias} res={res} f32={f32}")
+    g = _gen(T * 7 + K + O)
+    W = 2 * O if act == "swiglu" else O
+    x, w = _bf(g, T, K), _bf(g, W, K, scale=1 / math.sqrt(K))
+    b = _bf(g, W) if bias else None
+    r = _bf(g, T, O) if res else None
+    dt = F32 if f32 else BF16
+    out, pre = cgd.linear(_dev(x), _dev(w), bias=_dev(b), activation=act, residual=_dev(r), out_dtype=dt,
+                          return_preact=True)
+    alone = cgd.linear(_dev(x), _dev(w), bias=_dev(b), activation=act, residual=_dev(r), out_dtype=dt)
+    torch.cuda.synchronize()
+    y, p, t, tp = _ref(x, w, b, act, O, r)
+    assert out.dtype == dt and out.shape == (T, O) and pre.shape == (T, W)
+    _near(out, y, t, dt, "out")
+    _near(pre, p, tp, BF16, "preact")
+    assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("T,K,O", [(1, 128, 128), (5, 256, 17), (64, 7168, 256), (130, 640, 300), (1000, 2048, 384),
+                                   (2048, 256, 5120)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("fmt,colmajor", [(cgd.SCALE_F32, False), (cgd.SCALE_F32, True), (cgd.SCALE_UE8M0, False),
+                                          (cgd.SCALE_UE8M0, True)])
+def test_linear_fp8(T, K, O, act, fmt, colmajor):
+    say(f"linear fp8 T={T} K={K} O={O} act={act} fmt={fmt} colmajor={colmajor}")
+    g = _gen(T + K + O)
+    if act == "swiglu":
+        O = max(128, O // 128 * 128)
+    W = 2 * O if act == "swiglu" else O
+    x, xd = _fp8_x(g, T, K, fmt=fmt)
+    w, wd = _fp8_w(g, (), W, K)
+    b = _bf(g, W)
+    q, sc = _dev(x)
+    if colmajor:
+        sc = sc.t().contiguous().t()
+    out = cgd.linear((q, sc), _dev(w), bias=_dev(b), activation=act)
+    torch.cuda.synchronize()
+    y, _, t, _ = _ref(xd, wd, b, act, O, steps=2.0 ** -16 + (K + 3) * 2.0 ** -24)
+    _near(out, y, t, BF16, "out")
+
+
+def _offsets(g, G, rows, empty=()):
+    share = torch.rand(G, generator=g) ** 2
+    share[list(empty)] = 0
+    edge = torch.round(torch.cumsum(share, 0) / share.sum().clamp_min(1e-9) * rows).to(torch.int32)
+    edge[-1] = rows
+    return torch.cat([torch.zeros(1, dtype=torch.int32), edge])
+
+
+SHAPES = [(1, 1, 64, 16), (1, 100, 128, 256), (3, 7, 72, 40), (8, 40, 256, 130), (16, 1000, 512, 256),
+          (33, 500, 136, 257), (5, 1400, 320, 520), (65, 700, 128, 64), (512, 2000, 64, 24), (4, 2500, 256, 5000),
+          (300, 100, 128, 136)]
+
+
+@pytest.mark.parametrize("G,N,K,O", SHAPES)
+@pytest.mark.parametrize("act,bias", [(None, False), ("gelu", True), ("swiglu", True)])
+def test_grouped(G, N, K, O, act, bias):
+    say(f"grouped G={G} N={N} K={K} O={O} act={act}")
+    g = _gen(G + N + K + O)
+    W = 2 * O if act == "swiglu" else O
+    off = _offsets(g, G, N, empty=(G // 2,) if G > 2 else ())
+    x, w = _bf(g, N, K), _bf(g, G, W, K, scale=1 / math.sqrt(K))
+    b = _bf(g, G, W) if bias else None
+    out, pre = cgd.grouped_linear(_dev(x), _dev(w), _dev(off), bias=_dev(b), activation=act, return_preact=True)
+    torch.cuda.synchronize()
+    out, pre = out.cpu(), pre.cpu()
+    for e in range(G):
+        a, z = int(off[e]), int(off[e + 1])
+        y, p, t, tp = _ref(x[a:z], w[e], None if b is None else b[e], act, O)
+        _near(out[a:z], y, t, BF16, f"out of group {e}")
+        _near(pre[a:z], p, tp, BF16, f"preact of group {e}")
+
+
+@pytest.mark.parametrize("G,N,K,O", [(1, 5, 128, 16), (3, 200, 256, 130), (16, 1000, 512, 256), (40, 3000, 256, 384),
+                                     (4, 2500, 256, 5120)])
+@pytest.mark.parametrize("act", [None, "swiglu"])
+@pytest.mark.parametrize("fmt", [cgd.SCALE_F32, cgd.SCALE_UE8M0])
+def test_grouped_fp8(G, N, K, O, act, fmt):
+    say(f"grouped fp8 G={G} N={N} K={K} O={O} act={act} fmt={fmt}")
+    g = _gen(G + N + K + O)
+    if act == "swiglu":
+        O = max(128, O // 128 * 128)
+    W = 2 * O if act == "swiglu" else O
+    off = _offsets(g, G, N, empty=(0,) if G > 2 else ())
+    x, xd = _fp8_x(g, N, K, fmt=fmt)
+    w, wd = _fp8_w(g, (G,), W, K)
+    out = cgd.grouped_linear(_dev(x), _dev(w), _dev(off), activation=act).cpu()
+    for e in range(G):
+        a, z = int(off[e]), int(off[e + 1])
+        y, _, t, _ = _ref(xd[a:z], wd[e], None, act, O, steps=2.0 ** -16 + (K + 3) * 2.0 ** -24)
+        _near(out[a:z], y, t, BF16, f"group {e}")
+
+
+@pytest.mark.parametrize("G,cap,K,O", [(1, 1, 64, 16), (4, 30, 128, 100), (16, 70, 256, 130), (7, 150, 192, 256),
+                                       (3, 600, 128, 512)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_packed_rows_past_the_counts_stay(G, cap, K, O, fp8):
+    say(f"packed G={G} cap={cap} K={K} O={O} fp8={fp8}")
+    g = _gen(G + cap)
+    K = max(128, K // 128 * 128) if fp8 else K
+    cnt = torch.randint(0, cap + 1, (G,), generator=g, dtype=torch.int32)
+    cnt[0] = cap
+    if G > 1:
+        cnt[1] = 0
+    if fp8:
+        x, xd = _fp8_x(g, G, cap, K)
+        w, wd = _fp8_w(g, (G,), O, K)
+        steps = 2.0 ** -16 + (K + 3) * 2.0 ** -24
+    else:
+        x, w = _bf(g, G, cap, K), _bf(g, G, O, K)
+        for e in range(G):  # what lies past a count may be anything
+            x[e, int(cnt[e]):] = float("nan")
+        xd, wd, steps = x, w, 2.0 ** -24
+    out = torch.full((G, cap, O), -7.0, dtype=BF16, device=DEV)
+    pack = cgd.grouped_linear(_dev(x), _dev(w), _dev(cnt), out=out)
+    torch.cuda.synchronize()
+    assert pack is out
+    out = out.cpu()
+    for e in range(G):
+        n = int(cnt[e])
+        y, _, t, _ = _ref(xd[e, :n], wd[e], None, None, O, steps=steps)
+        _near(out[e, :n], y, t, BF16, f"group {e}")
+        assert (out[e, n:] == -7.0).all()
+
+
+def _act_slope64(v, act):
+    if act == "relu":
+        return (v > 0).to(F64)
+    if act == "silu":
+        s = torch.sigmoid(v)
+        return s + v * s * (1 - s)
+    if act == "gelu":
+        return 0.5 * (1 + torch.erf(v / math.sqrt(2))) + v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    return torch.ones_like(v)
+
+
+def _d64(grad, pre, act, O):
+    """-> (d, its fp32 error)."""
+    grad = grad.to(F64)
+    if act is None:
+        return grad, torch.zeros_like(grad)
+    p = pre.to(F64)
+    if act == "swiglu":
+        gt, up = p[..., :O], p[..., O:]
+        d = torch.cat([grad * up * _act_slope64(gt, "silu"), grad * gt * torch.sigmoid(gt)], -1)
+        t = torch.cat([grad.abs() * up.abs(), grad.abs()], -1) * (1 + gt.abs()).repeat(1, 2) * 2.0 ** -20
+        return d, t
+    return grad * _act_slope64(p, act), grad.abs() * (1 + p.abs()) * 2.0 ** -20
+
+
+def _check_grads(grad, x, w, pre, act, O, gx, gw, gb, rounded, what):
+    d, td = _d64(grad, pre, act, O)
+    x, w = x.to(F64), w.to(F64)
+    r = 2.0 ** -8 if rounded else 0.0
+    if gx is not None:
+        S = d.abs() @ w.abs()
+        _near(gx, d @ w, (r + d.shape[1] * 2.0 ** -24) * S + td @ w.abs() * 1.01, BF16, what + " grad_x")
+    S = d.abs().mT @ x.abs()
+    _near(gw, d.mT @ x, (r + d.shape[0] * 2.0 ** -24) * S + td.mT @ x.abs() * 1.01, BF16, what + " grad_weight")
+    if gb is not None:
+        _near(gb, d.sum(0), d.abs().sum(0) * d.shape[0] * 2.0 ** -24 + td.sum(0), BF16, what + " grad_bias")
+
+
+@pytest.mark.parametrize("T,K,O", [(1, 8, 1), (1, 256, 64), (7, 72, 24), (65, 136, 130), (128, 512, 256),
+                                   (300, 264, 333), (1000, 1024, 520), (4100, 320, 1028), (2100, 4104, 600)])
+@pytest.mark.parametrize("act,bias", [(None, False), (None, True), ("relu", True), ("silu", False), ("gelu", True),
+                                      ("swiglu", True)])
+def test_linear_backward(T, K, O, act, bias):
+    say(f"linear_backward T={T} K={K} O={O} act={act} bias={bias}")
+    g = _gen(T + K + O)
+    W = 2 * O if act == "swiglu" else O
+    x, w = _bf(g, T, K), _bf(g, W, K, scale=1 / math.sqrt(K))
+    pre = _bf(g, T, W) if act else None
+    grad = _bf(g, T, O)
+    gx, gw, gb = cgd.linear_backward(_dev(grad), _dev(x), _dev(w), preact=_dev(pre), activation=act, bias_grad=bias)
+    torch.cuda.synchronize()
+    assert (gb is not None) == bias
+    _check_grads(grad, x, w, pre, act, O, gx, gw, gb, act is not None, "dense")
+
+
+@pytest.mark.parametrize("G,N,K,O", SHAPES)
+@pytest.mark.parametrize("act,bias", [(None, False), ("gelu", True), ("swiglu", True)])
+def test_grouped_backward(G, N, K, O, act, bias):
+    say(f"grouped_backward G={G} N={N} K={K} O={O} act={act}")
+    g = _gen(G + N + K + O)
+    W = 2 * O if act == "swiglu" else O
+    off = _offsets(g, G, N, empty=(G // 2,) if G > 2 else ())
+    x, w = _bf(g, N, K), _bf(g, G, W, K, scale=1 / math.sqrt(K))
+    pre = _bf(g, N, W) if act else None
+    grad = _bf(g, N, O)
+    gx, gw, gb = cgd.grouped_linear_backward(_dev(grad), _dev(x), _dev(w), _dev(off), preact=_dev(pre),
+                                             activation=act, bias_grad=bias)
+    torch.cuda.synchronize()
+    gx, gw = gx.cpu(), gw.cpu()
+    for e in range(G):
+        a, z = int(off[e]), int(off[e + 1])
+        _check_grads(grad[a:z], x[a:z], w[e], None if pre is None else pre[a:z], act, O, gx[a:z], gw[e],
+                     None if gb is None else gb[e].cpu(), act is not None, f"group {e}")
