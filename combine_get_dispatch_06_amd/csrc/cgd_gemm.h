@@ -35,6 +35,7 @@ typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
 typedef short short8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
+typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef int int4_t __attribute__((ext_vector_type(4)));
 typedef int int8_t_ __attribute__((ext_vector_type(8)));
 
@@ -44,28 +45,41 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
     return (uint32_t)(uintptr_t)(const CGD_LDS(char)*)p;
 }
 
-// A raw buffer descriptor over `bytes` bytes at `base` (held in scalar
-// registers): loads at or past `bytes` return zero.
-struct Buffer {
-    uint64_t base;
-    uint32_t bytes;
-    __device__ __forceinline__ int4_t words() const {
-        int4_t r;
-        r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
-        r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32) & 0xFFFF);
-        r.z = __builtin_amdgcn_readfirstlane((int)bytes);
-        r.w = 0x00020000;
-        return r;
-    }
-};
-constexpr uint32_t kPastEnd = 0x80000000u;  // an offset past every descriptor (those end below 2^31)
+// A raw buffer descriptor from `base` on. Reads at kPastEnd return zero without
+// touching memory; every lane offset is either inside the operand or kPastEnd.
+__device__ __forceinline__ int4_t buffer_from(uint64_t base) {
+    int4_t r;
+    r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)base);
+    r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(base >> 32));  // addresses end below 2^48
+    r.z = 0x7FFFFFF0;
+    r.w = 0x00020000;
+    return r;
+}
+__device__ __forceinline__ void advance(int4_t& buf, int64_t bytes) {
+    const uint64_t b = (((uint64_t)(uint32_t)buf.y << 32) | (uint32_t)buf.x) + (uint64_t)bytes;
+    buf.x = (int)(uint32_t)b;
+    buf.y = (int)(uint32_t)(b >> 32);
+}
+constexpr uint32_t kPastEnd = 0x80000000u;  // past every descriptor's end
 
-// 16 bytes per lane from buffer offset `off` to LDS address lds + 16 * lane.
+// 16 bytes per lane from buffer offset `off` to LDS address lds + AT + 16 * lane.
 // The load has no register result; the waits for it are written out where a
-// stage is needed (wait_stage).
+// stage is needed (wait_loads).
+template <int AT>
 __device__ __forceinline__ void load_to_lds16(const int4_t& buf, uint32_t off, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(buf)
-                 : "memory", "m0");
+    asm volatile("s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off),
+                 "s"(buf), "n"(AT)
+                 : "memory", "m0", "scc");
+}
+// The same in two parts, with at least one instruction that is not theirs in
+// between (the address register needs one wait state): nothing else in these
+// kernels uses that register.
+template <int AT>
+__device__ __forceinline__ void aim_load(uint32_t lds) {
+    asm volatile("s_add_u32 m0, %0, %1" ::"s"(lds), "n"(AT) : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void aimed_load(const int4_t& buf, uint32_t off) {
+    asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(buf) : "memory");
 }
 // 4 bytes (fp32) or 1 byte (widened to 4) per lane to lds + 4 * lane.
 __device__ __forceinline__ void load_to_lds4(const int4_t& buf, uint32_t off, uint32_t lds) {
@@ -82,6 +96,12 @@ __device__ __forceinline__ void wait_loads() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void block_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+// LDS writes of the block's waves before the reads that follow, and the other way round
+__device__ __forceinline__ void block_sync() {
+    wait_loads<0>();
+    block_barrier();
+}
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
@@ -169,6 +189,27 @@ __device__ __forceinline__ Piece find_piece(const Groups& g, int bm, int want) {
     return r;
 }
 
+template <int V>
+struct Const {
+    static constexpr int value = V;
+};
+
+// 8 values of k for one row of a transposed tile, from k rows at `p` and `next` bytes on
+__device__ __forceinline__ bf16x8_t turned(const CGD_LDS(char)* p, int next) {
+    const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)p);
+    const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)(p + next));
+    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// f(Const<0>), ..., f(Const<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    if constexpr (I < N) {
+        f(Const<I>());
+        each<N, I + 1>(f);
+    }
+}
+
 // ---- activations, in fp32 -------------------------------------------------
 __device__ __forceinline__ float sigmoid_f(float v) { return 1.0f / (1.0f + __expf(-v)); }
 __device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
@@ -181,6 +222,17 @@ __device__ __forceinline__ float act_f(float v, int act) {
 }
 
 __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+
+// c += p q^T (16 x 16, 32 of k) with c in accumulation registers. The compiler,
+// given the choice, keeps part of 256 sums in the others and moves them over
+// and back in every step; written out, they stay. Results may be read after
+// settle().
+__device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const bf16x8_t& q) {
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
+}
+// Waits until the last matrix instructions have written their results (the
+// compiler does not see them in multiply(), so it inserts no waits of its own).
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // Stores N (4 or 8) consecutive values of one output row from column c on, as
 // bf16 or fp32, in 8- or 16-byte pieces where the row allows it (`wide`).
@@ -233,36 +285,46 @@ __device__ __forceinline__ void load_run(const uint16_t* p, int have, bool wide,
     }
 }
 
-// The 128-byte LDS rows of a k-contiguous tile hold their 16-byte pieces in an
-// order that depends on the row: piece c of row r is at c ^ key(r), so that the
-// 16 rows a matrix instruction takes are spread over the banks. The rows of one
-// instruction are 16 consecutive rows of Q, and for P the rows
-// (i / 4) * RUN + i % 4 (RUN consecutive columns per lane): key depends on i only.
-template <int RUN>
+// The LDS rows (RB = 128 or 64 bytes) of a k-contiguous tile hold their 16-byte
+// pieces in an order that depends on the row: piece c of row r is at c ^ key(r),
+// so that the 16 rows a matrix instruction takes are spread over all banks (no
+// conflict counted). The rows of one instruction are 16 consecutive rows of Q,
+// and for P the rows (i / 4) * RUN + i % 4 (RUN consecutive columns per lane):
+// key depends on i only.
+template <int RB, int RUN>
 __device__ __forceinline__ int row_key(int row) {
-    return (row & 3) | (((row / RUN) & 1) << 2);
+    return RB == 64 ? -(row / RUN) & 3 : (row & 3) | (((row / RUN) & 1) << 2);
 }
+// The same for transposed tiles (rows of one k): the LDS transposing read takes
+// 32 bytes from each of 8 rows at a time (rows 0-3 and 8-11, ...).
+__device__ __forceinline__ int k_key(int kr) { return ((kr & 3) << 1) | (kr & 8); }
 
 // Kernel arguments: see GemmArgs in cgd_experts_launch.h.
-template <int BM, int BN, int WM, int WN, int ST, bool QT, bool PT, bool FP8>
-__global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a) {
+template <int BM, int BN, int WM, int WN, int ST, int RB, bool QT, bool PT, bool FP8>
+__global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const GemmArgs a) {
     constexpr int NW = WM * WN;              // waves
     constexpr int TM = BM / WM, TN = BN / WN;  // a wave's part
     constexpr int MT = TM / 16, NT = TN / 16, NH = NT / 2;
     constexpr int RUN = 4 * NH;              // consecutive columns per lane
-    constexpr int BK = FP8 ? 128 : 64;       // 128 bytes of k
-    constexpr int QB = BM * 128, PB = BN * 128;
+    constexpr int BK = FP8 ? RB : RB / 2;    // RB bytes of k in a stage
+    constexpr int QB = BM * RB, PB = BN * RB;
+    constexpr int RPL = 1024 / RB;           // tile rows in one 1-KB load, CPR 16-byte pieces in each
+    constexpr int CPR = RB / 16;
+    constexpr int KS = RB / 64;              // matrix instructions along k (bf16) in a stage
     // scales of a stage: one per row, the weights', and a place that is never read
     constexpr int SROWS = BM < 64 ? 64 : BM;
     constexpr int SB = FP8 ? SROWS * 4 + 512 : 0;
     constexpr int STAGE = QB + PB + SB;
-    constexpr int QL = BM / 8 / NW, PL = BN / 8 / NW;  // 1-KB loads per wave
+    constexpr int QL = QB / 1024 / NW, PL = PB / 1024 / NW;  // 1-KB loads per wave
     constexpr int SL = FP8 ? 1 : 0;
     constexpr int LOADS = QL + PL + SL;
     static_assert(QL >= 1 && PL >= 2 && NT % 2 == 0 && MT >= 1, "tile too small for its waves");
-    static_assert(!FP8 || (!QT && !PT), "FP8 tiles are k-contiguous");
+    static_assert(!FP8 || (!QT && !PT && RB == 128), "FP8 tiles are k-contiguous");
+    static_assert(RB == 128 || RB == 64, "a stage holds 128 or 64 bytes of k");
+    static_assert(PT || (NW * RPL % ((RB == 64 ? 4 : 2) * RUN) == 0 && (BN / 2) % ((RB == 64 ? 4 : 2) * RUN) == 0), "a lane's piece of k is the same in all its loads");
     static_assert(!FP8 || SROWS / 64 + 1 <= NW, "one wave loads 64 row scales, one the weights'");
-    __shared__ __attribute__((aligned(1024))) char smem[ST * STAGE];
+    // ST stages of both operands; or (ST = 0) two of Q and three of P, all 160 KB
+    __shared__ __attribute__((aligned(1024))) char smem[ST ? ST * STAGE : 2 * QB + 3 * PB];
 
     const int lane = lane_id();
     const int wave = uniform(threadIdx.x / kWave);
@@ -334,150 +396,141 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a
 
     // ---- where the operands are --------------------------------------------
     // Q: k-contiguous: rows qrow0 .. ; transposed: columns m0 .. of rows qrow0 ..
-    Buffer qb, pb0, pb1;
+    // A lane that has nothing to load in any stage (rows or columns past the
+    // tile's) keeps kPastEnd; k is checked stage by stage against k_left.
+    uint64_t qb, pb0, pb1;
     uint32_t qv[QL], pv[PL];
-    const int64_t ES = FP8 ? 1 : 2;
-    int64_t q_left = 0, p_left = 0;  // transposed operands: rows of k left
+    int qk[QT ? QL : 1], pk[PT ? PL : 1];  // where in the stage's k a lane's loads are
+    constexpr int ES = FP8 ? 1 : 2;
+    const int ldq = (int)a.ldq, ldp = (int)a.ldp;
     if (!QT) {
-        qb.base = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + k0 * ES);
-        const int64_t r = rows < BM ? rows : BM;
-        qb.bytes = (uint32_t)(r * a.ldq - k0 * ES);
+        qb = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + k0 * ES);
+        qk[0] = ((lane & (CPR - 1)) ^ row_key<RB, 4>(wave * RPL + lane / CPR)) * (16 / ES);
 #pragma unroll
         for (int j = 0; j < QL; ++j) {
-            const int row = (j * NW + wave) * 8 + lane / 8;
-            qv[j] = (uint32_t)(row * (int)a.ldq + (((lane & 7) ^ row_key<4>(row)) << 4));
+            const int row = (j * NW + wave) * RPL + lane / CPR;
+            qv[j] = row < rows ? (uint32_t)(row * ldq + qk[0] * ES) : kPastEnd;
         }
     } else {
         constexpr int RPI = 512 / BM;  // k rows per 1-KB load
-        qb.base = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + m0 * 2);
-        q_left = klen;
-        qb.bytes = (uint32_t)((q_left < 64 ? q_left : 64) * a.ldq - m0 * 2);
-        if (q_left <= 0) qb.bytes = 0;
+        qb = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + m0 * 2);
 #pragma unroll
         for (int j = 0; j < QL; ++j) {
-            const int kr = (j * NW + wave) * RPI + lane / (64 / RPI);
-            const int s = lane & (64 / RPI - 1);
-            qv[j] = (uint32_t)(kr * (int)a.ldq + ((s ^ ((kr & 3) << 1)) << 4));
+            qk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
+            const int c = ((lane & (64 / RPI - 1)) ^ k_key(qk[j])) * 16;
+            qv[j] = m0 * 2 + c < a.ldq ? (uint32_t)(qk[j] * ldq + c) : kPastEnd;
         }
     }
     if (!PT) {
-        const uint64_t pbase = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group);
+        const uint64_t base = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group + k0 * ES);
         const int64_t second = a.glu ? a.n + n0 : n0 + BN / 2;  // first weight row of the tile's upper half
-        const int64_t r0 = a.n - n0 < BN / 2 ? a.n - n0 : BN / 2;
-        int64_t r1 = a.glu ? r0 : a.n - second;
-        r1 = r1 < 0 ? 0 : (r1 > BN / 2 ? BN / 2 : r1);
-        pb0.base = pbase + (uint64_t)(n0 * a.ldp + k0 * ES);
-        pb0.bytes = (uint32_t)(r0 * a.ldp - k0 * ES);
-        pb1.base = pbase + (uint64_t)(second * a.ldp + k0 * ES);
-        pb1.bytes = r1 > 0 ? (uint32_t)(r1 * a.ldp - k0 * ES) : 0u;
+        const int64_t left0 = a.n - n0, left1 = a.glu ? left0 : a.n - second;
+        pb0 = base + (uint64_t)(n0 * a.ldp);
+        pb1 = base + (uint64_t)(second * a.ldp);
+        pk[0] = ((lane & (CPR - 1)) ^ row_key<RB, RUN>(wave * RPL + lane / CPR)) * (16 / ES);
 #pragma unroll
         for (int j = 0; j < PL; ++j) {
-            const int row = ((j % (PL / 2)) * NW + wave) * 8 + lane / 8;
-            pv[j] = (uint32_t)(row * (int)a.ldp + (((lane & 7) ^ row_key<RUN>(row)) << 4));
+            const int row = ((j % (PL / 2)) * NW + wave) * RPL + lane / CPR;
+            pv[j] = row < (j < PL / 2 ? left0 : left1) ? (uint32_t)(row * ldp + pk[0] * ES) : kPastEnd;
         }
     } else {
         constexpr int RPI = 512 / BN;
-        pb0.base = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group + (prow0 + k0) * a.ldp + n0 * 2);
-        p_left = klen;
-        pb0.bytes = (uint32_t)((p_left < 64 ? p_left : 64) * a.ldp - n0 * 2);
-        if (p_left <= 0) pb0.bytes = 0;
-        pb1 = pb0;
+        pb0 = pb1 = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group + prow0 * a.ldp + n0 * 2);
 #pragma unroll
         for (int j = 0; j < PL; ++j) {
-            const int kr = (j * NW + wave) * RPI + lane / (64 / RPI);
-            const int s = lane & (64 / RPI - 1);
-            pv[j] = (uint32_t)(kr * (int)a.ldp + ((s ^ ((kr & 3) << 2)) << 4));
+            pk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
+            const int c = ((lane & (64 / RPI - 1)) ^ k_key(pk[j])) * 16;
+            pv[j] = n0 * 2 + c < a.ldp ? (uint32_t)(pk[j] * ldp + c) : kPastEnd;
         }
     }
     // FP8 scales: wave w < BM/64 brings those of rows 64 w .., the last wave
     // those of the two weight blocks the tile's halves lie in (lanes 0 and 1:
     // the halves are at most 128 wide and start at multiples of their width,
     // and SwiGLU's up rows start at a multiple of 128).
-    Buffer sb;
+    uint64_t sb = 0;
     uint32_t sv = kPastEnd;
     int64_t s_step = 0;
     bool s_byte = false;
     if (FP8) {
-        const int kb0 = (int)(k0 / 128);
+        const int64_t kb0 = k0 / 128;
         if (wave == NW - 1) {
-            sb.base = (uint64_t)a.ps + (uint64_t)((int64_t)group * a.ps_group * 4);
-            sb.bytes = (uint32_t)(a.ps_group * 4);
+            sb = (uint64_t)a.ps + (uint64_t)(((int64_t)group * a.ps_group + kb0) * 4);
             const int64_t second = a.glu ? a.n + n0 : n0 + BN / 2;
             const int64_t row = lane == 0 ? n0 : second;
-            const int64_t blk = row / 128;
-            if (lane < 2 && row < a.n * (a.glu ? 2 : 1)) sv = (uint32_t)((blk * a.ps_row + kb0) * 4);
+            if (lane < 2 && row < a.n * (a.glu ? 2 : 1)) sv = (uint32_t)(row / 128 * a.ps_row * 4);
             s_step = 4;
         } else {
             const int row = wave * 64 + lane;
-            const int sbytes = a.qs_byte ? 1 : 4;
-            sb.base = (uint64_t)a.qs + (uint64_t)((qrow0 * a.qs_row + kb0 * a.qs_blk) * sbytes);
-            sb.bytes = 0x7FFFFFF0u;
-            if (row < BM && row < rows) sv = (uint32_t)(row * a.qs_row * sbytes);
-            s_step = a.qs_blk * sbytes;
+            const int size = a.qs_byte ? 1 : 4;
+            sb = (uint64_t)a.qs + (uint64_t)((qrow0 * a.qs_row + kb0 * a.qs_blk) * size);
+            if (row < BM && row < rows) sv = (uint32_t)(row * a.qs_row * size);
+            s_step = a.qs_blk * size;
             s_byte = a.qs_byte;
         }
     }
 
-    const uint32_t lds0 = uniform((int)lds_address(smem));
-    const int64_t q_step = QT ? 64 * a.ldq : 128, p_step = PT ? 64 * a.ldp : 128;
-    int64_t k_left = klen;  // of the next stage to load
+    int4_t qd = buffer_from(qb), pd0 = buffer_from(pb0), pd1 = buffer_from(pb1), sd = buffer_from(sb);
+    const uint32_t lds0 = uniform((int)lds_address(smem)) + wave * 1024;
+    const int64_t q_step = QT ? BK * a.ldq : RB, p_step = PT ? BK * a.ldp : RB;
+    int kq_left = uniform((int)klen), kp_left = kq_left;  // of the next stage of each to load
 
-    auto load_stage = [&](int buf) {
+    // From the last stage on (a whole one included, once it is past) lanes whose
+    // piece of k lies behind the end load nothing.
+    auto mask_q = [&]() {
+        if (kq_left >= BK) return;
+#pragma unroll
+        for (int i = 0; i < QL; ++i) qv[i] = qk[QT ? i : 0] < kq_left ? qv[i] : kPastEnd;
+        if (FP8) sv = kq_left > 0 ? sv : kPastEnd;
+    };
+    auto mask_p = [&]() {
+        if (kp_left >= BK) return;
+#pragma unroll
+        for (int j = 0; j < PL; ++j) pv[j] = pk[PT ? j : 0] < kp_left ? pv[j] : kPastEnd;
+    };
+    mask_q();
+    mask_p();
+    // Load `I` of the next stage of Q (of P, of the scales); l: this wave's
+    // place in the stage's slot (its loads go NW KB apart).
+    auto load_q = [&](auto I, uint32_t l) { load_to_lds16<decltype(I)::value * NW * 1024>(qd, qv[decltype(I)::value], l); };
+    auto load_p = [&](auto J, uint32_t l) {
+        constexpr int j = decltype(J)::value;
+        load_to_lds16<j * NW * 1024>(!PT && j >= PL / 2 ? pd1 : pd0, pv[j], l);
+    };
+    auto load_s = [&](uint32_t l) {
+        // waves with neither rows nor the weights' scales load zeros into the
+        // unread place: every wave has the same count of loads to wait for
+        const uint32_t dst = l - wave * 1024 + (wave == NW - 1 ? SROWS * 4 : wave * 64 < SROWS ? wave * 256 : SROWS * 4 + 256);
+        if (s_byte)
+            load_to_lds1(sd, sv, dst);
+        else
+            load_to_lds4(sd, sv, dst);
+    };
+    auto next_q = [&]() {
+        advance(qd, q_step);
+        if (FP8) advance(sd, s_step);
+        kq_left -= BK;
+        mask_q();
+    };
+    auto next_p = [&]() {
+        advance(pd0, p_step);
+        if (!PT) advance(pd1, p_step);
+        kp_left -= BK;
+        mask_p();
+    };
+    auto load_piece = [&](auto I, int buf) {
+        constexpr int i = decltype(I)::value;
         const uint32_t l = lds0 + (uint32_t)(buf * STAGE);
-        const bool tail = k_left < BK;
-        const int left = (int)(tail ? k_left : BK);
-        const int4_t qw = qb.words(), pw0 = pb0.words(), pw1 = pb1.words();
-#pragma unroll
-        for (int j = 0; j < QL; ++j) {
-            uint32_t v = qv[j];
-            if (!QT && tail) {
-                const int row = (j * NW + wave) * 8 + lane / 8;
-                const int c = (lane & 7) ^ row_key<4>(row);
-                v = c * (FP8 ? 16 : 8) < left ? v : kPastEnd;
-            }
-            load_to_lds16(qw, v, l + (j * NW + wave) * 1024);
-        }
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            uint32_t v = pv[j];
-            if (!PT && tail) {
-                const int row = ((j % (PL / 2)) * NW + wave) * 8 + lane / 8;
-                const int c = (lane & 7) ^ row_key<RUN>(row);
-                v = c * (FP8 ? 16 : 8) < left ? v : kPastEnd;
-            }
-            load_to_lds16(!PT && j >= PL / 2 ? pw1 : pw0, v, l + QB + (j * NW + wave) * 1024);
-        }
-        if (FP8) {
-            const int4_t sw = sb.words();
-            // waves with neither rows nor the weights' scales load zeros into the
-            // unread place: every wave has the same count of loads to wait for
-            const uint32_t dst = l + QB + PB + (wave == NW - 1 ? SROWS * 4 : wave * 64 < SROWS ? wave * 256 : SROWS * 4 + 256);
-            if (s_byte)
-                load_to_lds1(sw, sv, dst);
-            else
-                load_to_lds4(sw, sv, dst);
-            sb.base += s_step;
-            if (wave == NW - 1) sb.bytes = sb.bytes > 4 ? sb.bytes - 4 : 0;
-        }
-        qb.base += q_step;
-        pb0.base += p_step;
-        pb1.base += p_step;
-        if (QT) {
-            q_left -= 64;
-            const int64_t r = q_left < 0 ? 0 : (q_left < 64 ? q_left : 64);
-            qb.bytes = r > 0 ? (uint32_t)(r * a.ldq - m0 * 2) : 0u;
-        } else {
-            qb.bytes = qb.bytes > 128 ? qb.bytes - 128 : 0;
-        }
-        if (PT) {
-            p_left -= 64;
-            const int64_t r = p_left < 0 ? 0 : (p_left < 64 ? p_left : 64);
-            pb0.bytes = r > 0 ? (uint32_t)(r * a.ldp - n0 * 2) : 0u;
-        } else {
-            pb0.bytes = pb0.bytes > 128 ? pb0.bytes - 128 : 0;
-            pb1.bytes = pb1.bytes > 128 ? pb1.bytes - 128 : 0;
-        }
-        k_left -= BK;
+        if constexpr (i < QL)
+            load_q(I, l);
+        else if constexpr (i < QL + PL)
+            load_p(Const<i - QL>(), l + QB);
+        else
+            load_s(l + QB + PB);
+    };
+    auto load_stage = [&](int buf) {
+        each<LOADS>([&](auto I) { load_piece(I, buf); });
+        next_q();
+        next_p();
     };
 
     float4_t acc[MT][NT];
@@ -489,47 +542,176 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a
     // ---- LDS addresses of a lane's fragments -------------------------------
     const CGD_LDS(char)* sm = (const CGD_LDS(char)*)smem;
     // k-contiguous: piece (ks * 4 + lg) of the row, for ks = 0, 1
-    int qa[4], pa[2];
+    int qa[QT ? MT : 2], pa[PT ? NT : 2];
     if (!QT) {
         const int row = wm * TM + li;
-        qa[0] = row * 128 + ((lg ^ row_key<4>(row)) << 4);
-        qa[1] = row * 128 + (((4 + lg) ^ row_key<4>(row)) << 4);
-        qa[2] = qa[3] = 0;
+        qa[0] = row * RB + ((lg ^ row_key<RB, 4>(row)) << 4);
+        qa[1] = row * RB + (((4 + lg) ^ row_key<RB, 4>(row)) << 4);
     } else {
-        // four columns of k row lg * 8 + li / 4; column piece of 16-row tile mt
+        // four columns of 16-row tile u from k row lg * 8 + li / 4
         const int kr = lg * 8 + (li >> 2);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < MT; ++u) {
             const int col = wm * TM + u * 16 + (li & 3) * 4;
-            qa[u] = kr * (BM * 2) + (((col >> 3) ^ ((kr & 3) << 1)) << 4) + (col & 7) * 2;
+            qa[u] = kr * (BM * 2) + (((col >> 3) ^ k_key(kr)) << 4) + (col & 7) * 2;
         }
     }
     if (!PT) {
         const int row = wn * (TN / 2) + (li >> 2) * RUN + (li & 3);
-        pa[0] = QB + row * 128 + ((lg ^ row_key<RUN>(row)) << 4);
-        pa[1] = QB + row * 128 + (((4 + lg) ^ row_key<RUN>(row)) << 4);
+        pa[0] = row * RB + ((lg ^ row_key<RB, RUN>(row)) << 4);
+        pa[1] = row * RB + (((4 + lg) ^ row_key<RB, RUN>(row)) << 4);
     } else {
-        pa[0] = pa[1] = 0;
+        const int kr = lg * 8 + (li >> 2);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int col = t / NH * (BN / 2) + wn * (TN / 2) + t % NH * 16 + (li & 3) * 4;
+            pa[t] = kr * (BN * 2) + (((col >> 3) ^ k_key(kr)) << 4) + (col & 7) * 2;
+        }
     }
     auto q_frag = [&](int base, int ks, int mt) -> bf16x8_t {
-        if (!QT) return *(const CGD_LDS(bf16x8_t)*)(sm + base + qa[ks] + mt * 2048);
-        const int at = base + qa[mt & 3] + (mt >> 2) * 128 + ks * 32 * (BM * 2);
-        const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)(sm + at));
-        const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)(sm + at + 4 * (BM * 2)));
-        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        if (!QT) return *(const CGD_LDS(bf16x8_t)*)(sm + base + qa[ks] + mt * 16 * RB);
+        const int at = base + qa[mt] + ks * 32 * (BM * 2);
+        return turned(sm + at, 4 * (BM * 2));
     };
     auto p_frag = [&](int base, int ks, int nt) -> bf16x8_t {
         const int h = nt / NH, t = nt % NH;
-        if (!PT) return *(const CGD_LDS(bf16x8_t)*)(sm + base + pa[ks] + h * (BN / 2) * 128 + t * 512);
-        const int kr = lg * 8 + (li >> 2);
-        const int col = h * (BN / 2) + wn * (TN / 2) + (li & 3) * RUN + t * 4;
-        const int at = base + QB + kr * (BN * 2) + (((col >> 3) ^ ((kr & 3) << 2)) << 4) + (col & 7) * 2 + ks * 32 * (BN * 2);
-        const short4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)(sm + at));
-        const short4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((CGD_LDS(short4_t)*)(sm + at + 4 * (BN * 2)));
-        return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        if (!PT) return *(const CGD_LDS(bf16x8_t)*)(sm + base + pa[ks] + h * (BN / 2) * RB + t * 4 * RB);
+        const int at = base + pa[nt] + ks * 32 * (BN * 2);
+        return turned(sm + at, 4 * (BN * 2));
     };
 
     // ---- main loop ----------------------------------------------------------
+    if constexpr (ST == 0) {
+        // Few, large waves: the 64 products of half a stage (32 of k) run on
+        // operands that were read from LDS during the half before, with one LDS
+        // read, load or address slipped behind a product each, so that one wave
+        // per SIMD keeps its matrix unit fed. Half way through stage k every
+        // wave has read all of it: after the barrier there the loads of Q's
+        // stage k + 2 (needed a stage later, so they go first) and P's stage
+        // k + 3 (needed two stages later) take its place. Loads past the end
+        // are issued all the same (they touch no memory), which keeps the count
+        // of loads to wait for the same in every step.
+        static_assert(ST || (QL == 8 && PL == 8 && MT == 8 && NT == 8), "the schedule below is for 64 products in half a stage");
+        auto pslot = [&](int slot) { return 2 * QB + slot * PB; };
+        int p_read = 0;  // P's slot of stage kt
+        each<QL>([&](auto I) { load_q(I, lds0); });
+        next_q();
+        each<PL>([&](auto I) { load_p(I, lds0 + pslot(0)); });
+        next_p();
+        each<PL>([&](auto I) { load_p(I, lds0 + pslot(1)); });
+        next_p();
+        each<QL>([&](auto I) { load_q(I, lds0 + QB); });
+        next_q();
+        each<PL>([&](auto I) { load_p(I, lds0 + pslot(2)); });
+        next_p();
+        bf16x8_t qf[2][MT], pf[2][NT];
+        // fragment n of the next half stage: P's first, all of which its first row needs
+        auto fetch = [&](auto N, auto SET, int ks, int qbase, int pbase) {
+            constexpr int n = decltype(N)::value, set = decltype(SET)::value;
+            if constexpr (n < NT)
+                pf[set][n] = p_frag(pbase, ks, n);
+            else
+                qf[set][n - NT] = q_frag(qbase, ks, n - NT);
+        };
+        wait_loads<QL + 2 * PL>();
+        block_barrier();
+        each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, 0, pslot(0)); });
+        for (int kt = 0;;) {  // at least one stage: an empty reduction multiplies zeros
+            const int qbase = (kt & 1) * QB, pbase = pslot(p_read);
+            p_read = p_read == 2 ? 0 : p_read + 1;
+            const int qnext = QB - qbase, pnext = pslot(p_read);
+            const uint32_t fq = lds0 + qbase, fp = lds0 + pbase;
+            __builtin_amdgcn_sched_barrier(0);
+            each<64>([&](auto G) {
+                constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
+                multiply(acc[i][j], pf[0][j], qf[0][i]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (g % 3 == 0 && g < 48) fetch(Const<g / 3>(), Const<1>(), 1, qbase, pbase);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            // Q's and P's stage kt + 1 have landed; P's kt + 2 may still be on its way
+            wait_loads<PL>();
+            block_barrier();
+            each<64>([&](auto G) {
+                constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
+                multiply(acc[i][j], pf[1][j], qf[1][i]);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (g < 16) {
+                    if constexpr (g % 2 == 0)
+                        aim_load<g / 2 * NW * 1024>(fq);
+                    else
+                        aimed_load(qd, qv[g / 2]);
+                } else if constexpr (g < 48) {
+                    constexpr int n = (g - 16) / 2;
+                    if constexpr (g % 2 == 0)
+                        fetch(Const<n>(), Const<0>(), 0, qnext, pnext);
+                    else if constexpr (n % 2 == 0)
+                        aim_load<n / 2 * NW * 1024>(fp);
+                    else
+                        aimed_load(!PT && n / 2 >= PL / 2 ? pd1 : pd0, pv[n / 2]);
+                } else if constexpr (g == 50) {
+                    next_q();
+                } else if constexpr (g == 54) {
+                    next_p();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if (++kt >= nk) {
+                settle();  // on the way out, before the sums are touched
+                break;
+            }
+        }
+    } else if constexpr (RB == 64) {
+        // Operands are read from LDS one stage ahead into the other of two
+        // register sets, so the matrix instructions of a stage wait for
+        // nothing; ST stages are on their way or being read. Loads past the
+        // end are issued all the same (they touch no memory), which keeps the
+        // count of loads to wait for the same in every step.
+#pragma unroll
+        for (int s = 0; s < ST; ++s) load_stage(s);
+        bf16x8_t qf[2][MT], pf[2][NT];
+        wait_loads<(ST - 1) * LOADS>();
+        block_barrier();
+#pragma unroll
+        for (int j = 0; j < NT; ++j) pf[0][j] = p_frag(QB, 0, j);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) qf[0][i] = q_frag(0, 0, i);
+        int slot = 0;  // of stage kt
+        auto step = [&](auto set) {
+            constexpr int S = decltype(set)::value;
+            // stage kt + 1 has landed for every wave, and every wave has read stage kt
+            wait_loads<(ST - 2) * LOADS>();
+            block_barrier();
+            const int refill = slot;
+            slot = slot + 1 == ST ? 0 : slot + 1;
+            const int base = slot * STAGE;
+            __builtin_amdgcn_sched_barrier(0);
+            // row by row: LDS reads for the next stage, matrix instructions of
+            // this one, a load of the stage that takes the freed slot
+            each<MT>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+#pragma unroll
+                for (int j = i * NT / MT; j < (i + 1) * NT / MT; ++j) pf[1 - S][j] = p_frag(base + QB, 0, j);
+                qf[1 - S][i] = q_frag(base, 0, i);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[S][j], qf[S][i], acc[i][j], 0, 0, 0);
+                if constexpr (i < LOADS) load_piece(I, refill);
+                if (i == LOADS) {
+                    next_q();
+                    next_p();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            static_assert(LOADS < MT, "one load for each row of the wave's tile");
+        };
+        int kt = 0;
+        for (; kt + 1 < nk; kt += 2) {
+            step(Const<0>());
+            step(Const<1>());
+        }
+        if (kt < nk) step(Const<0>());
+    } else {
 #pragma unroll
     for (int s = 0; s < ST - 1; ++s)
         if (s < nk) load_stage(s);
@@ -550,7 +732,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a
             for (int ks = 0; ks < 2; ++ks) {
                 bf16x8_t qf[MT], pf[NT];
 #pragma unroll
-                for (int j = 0; j < NT; ++j) pf[j] = p_frag(base, ks, j);
+                for (int j = 0; j < NT; ++j) pf[j] = p_frag(base + QB, ks, j);
 #pragma unroll
                 for (int i = 0; i < MT; ++i) qf[i] = q_frag(base, ks, i);
 #pragma unroll
@@ -565,7 +747,7 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a
             int8_t_ pf[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const int4_t lo = __builtin_bit_cast(int4_t, p_frag(base, 0, j)), hi = __builtin_bit_cast(int4_t, p_frag(base, 1, j));
+                const int4_t lo = __builtin_bit_cast(int4_t, p_frag(base + QB, 0, j)), hi = __builtin_bit_cast(int4_t, p_frag(base + QB, 1, j));
                 pf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             }
 #pragma unroll
@@ -591,78 +773,96 @@ __global__ __launch_bounds__(WM* WN* kWave, 2) void gemm_kernel(const GemmArgs a
         buf = buf + 1 == ST ? 0 : buf + 1;
         next = next + 1 == ST ? 0 : next + 1;
     }
+    }
 
     // ---- epilogue -----------------------------------------------------------
-    // A lane holds, for each 16-row tile, one row and RUN consecutive columns
-    // in the lower half of the tile and RUN in the upper half.
-    const int64_t lim = rows < BM ? rows : BM;
-    const int64_t c0 = n0 + wn * (TN / 2) + lg * RUN;                                   // lower half's columns
-    const int64_t c1 = (a.glu ? a.n : (int64_t)BN / 2) + c0;                            // upper half's (weight rows)
-    const int have0 = (int)(a.n - c0 < RUN ? a.n - c0 : RUN);
-    const int64_t end1 = a.glu ? 2 * a.n : a.n;
-    const int have1 = a.glu ? have0 : (int)(end1 - c1 < RUN ? end1 - c1 : RUN);
-    float bias0[RUN], bias1[RUN];
+    // The sums go through LDS, half of each wave's rows at a time, so that the
+    // rest is a short loop (unrolled over the registers it was 170 KB of code,
+    // fetched once for each tile) that takes 8 columns of the tile's lower half
+    // and the same 8 of its upper half per lane, consecutive lanes along a row.
+    constexpr int ROWS = BM / 2, LD = BN + 4;  // 16 bytes of padding spread a column over the banks
+    static_assert(sizeof(smem) >= ROWS * LD * 4 && MT % 2 == 0, "half of the rows fit");
+    const int64_t end1 = a.glu ? 2 * a.n : a.n;            // weight rows
+    const int64_t second = a.glu ? a.n : (int64_t)BN / 2;  // from the lower half's columns to the upper half's
+    const int64_t orow0 = QT ? (int64_t)group * a.m + m0 : qrow0;
+    const bool wide_w = (end1 & 7) == 0 && (!a.glu || (a.n & 7) == 0), wide_n = (a.n & 7) == 0;
+    CGD_LDS(float)* st = (CGD_LDS(float)*)smem;
+    constexpr int RUNS = BN / 16;  // runs of 8 columns in half a tile
+    constexpr int STEP = NW * kWave / RUNS;
+    const int run = threadIdx.x % RUNS;
+    const int64_t c0 = n0 + run * 8, c1 = second + c0;
+    const int have0 = (int)(a.n - c0 < 8 ? a.n - c0 : 8);
+    const int have1 = a.glu ? have0 : (int)(a.n - c1 < 8 ? a.n - c1 : 8);
+    float bias0[8], bias1[8];
 #pragma unroll
-    for (int r = 0; r < RUN; ++r) bias0[r] = bias1[r] = 0.0f;
+    for (int q = 0; q < 8; ++q) bias0[q] = bias1[q] = 0.0f;
     if (a.bias && a.splits == 1) {
         const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (int64_t)group * end1;
-        load_run<RUN>(b + c0, have0, false, bias0);
-        load_run<RUN>(b + c1, have1, false, bias1);
+        load_run<8>(b + c0, have0, false, bias0);
+        load_run<8>(b + c1, have1, false, bias1);
     }
-    const int64_t orow0 = QT ? (int64_t)group * a.m + m0 : qrow0;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int64_t r = wm * TM + i * 16 + li;
-        if (r >= lim) continue;
-        float v0[RUN], v1[RUN];
+    for (int h = 0; h < 2; ++h) {
+        block_sync();
 #pragma unroll
-        for (int t = 0; t < NH; ++t)
+        for (int i = 0; i < MT / 2; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                v0[t * 4 + q] = acc[i][t][q];
-                v1[t * 4 + q] = acc[i][NH + t][q];
+            for (int j = 0; j < NT; ++j) {
+                const int c = j / NH * (BN / 2) + wn * (TN / 2) + (PT ? j % NH * 16 + lg * 4 : lg * RUN + j % NH * 4);
+                *(CGD_LDS(float4_t)*)(st + (wm * (TM / 2) + i * 16 + li) * LD + c) = acc[h * (MT / 2) + i][j];
             }
-        const int64_t row = orow0 + r;
-        if (a.splits > 1) {  // partial sums, joined by join_kernel
-            const int64_t at = ((int64_t)split * a.g.total + row) * end1;
-            store_run<RUN>(a.partial, at + c0, v0, have0, true, (end1 & 3) == 0);
-            store_run<RUN>(a.partial, at + c1, v1, have1, true, (end1 & 3) == 0 && (!a.glu || (a.n & 3) == 0));
-            continue;
-        }
+        block_sync();
+#pragma unroll 1
+        for (int lr = threadIdx.x / RUNS; lr < ROWS; lr += STEP) {
+            const int r = lr / (TM / 2) * TM + h * (TM / 2) + lr % (TM / 2);
+            if (r >= rows) continue;
+            float v0[8], v1[8];
 #pragma unroll
-        for (int q = 0; q < RUN; ++q) {
-            v0[q] += bias0[q];
-            v1[q] += bias1[q];
-        }
-        if (a.preact) {
-            store_run<RUN>(a.preact, row * end1 + c0, v0, have0, false, (end1 & 7) == 0);
-            store_run<RUN>(a.preact, row * end1 + c1, v1, have1, false, (end1 & 7) == 0 && (!a.glu || (a.n & 7) == 0));
-        }
-        if (a.glu) {
+            for (int q = 0; q < 8; q += 4) {
+                const float4_t x = *(const CGD_LDS(float4_t)*)(st + lr * LD + run * 8 + q);
+                const float4_t y = *(const CGD_LDS(float4_t)*)(st + lr * LD + BN / 2 + run * 8 + q);
 #pragma unroll
-            for (int q = 0; q < RUN; ++q) v0[q] = silu_f(v0[q]) * v1[q];
-        } else if (a.act) {
-#pragma unroll
-            for (int q = 0; q < RUN; ++q) {
-                v0[q] = act_f(v0[q], a.act);
-                v1[q] = act_f(v1[q], a.act);
+                for (int t = 0; t < 4; ++t) {
+                    v0[q + t] = x[t] + bias0[q + t];
+                    v1[q + t] = y[t] + bias1[q + t];
+                }
             }
-        }
-        if (a.residual) {
-            const uint16_t* res = static_cast<const uint16_t*>(a.residual) + row * a.n;
-            float z[RUN];
-            load_run<RUN>(res + c0, have0, (a.n & 7) == 0, z);
-#pragma unroll
-            for (int q = 0; q < RUN; ++q) v0[q] += z[q];
-            if (!a.glu) {
-                load_run<RUN>(res + c1, have1, (a.n & 7) == 0, z);
-#pragma unroll
-                for (int q = 0; q < RUN; ++q) v1[q] += z[q];
+            const int64_t row = orow0 + r;
+            if (a.splits > 1) {  // partial sums, joined by join_kernel
+                const int64_t at = ((int64_t)split * a.g.total + row) * end1;
+                store_run<8>(a.partial, at + c0, v0, have0, true, wide_w);
+                store_run<8>(a.partial, at + c1, v1, have1, true, wide_w);
+                continue;
             }
+            if (a.preact) {
+                store_run<8>(a.preact, row * end1 + c0, v0, have0, false, wide_w);
+                store_run<8>(a.preact, row * end1 + c1, v1, have1, false, wide_w);
+            }
+            if (a.glu) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v0[q] = silu_f(v0[q]) * v1[q];
+            } else if (a.act) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    v0[q] = act_f(v0[q], a.act);
+                    v1[q] = act_f(v1[q], a.act);
+                }
+            }
+            if (a.residual) {
+                const uint16_t* res = static_cast<const uint16_t*>(a.residual) + row * a.n;
+                float z[8];
+                load_run<8>(res + c0, have0, wide_n, z);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v0[q] += z[q];
+                if (!a.glu) {
+                    load_run<8>(res + c1, have1, wide_n, z);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v1[q] += z[q];
+                }
+            }
+            store_run<8>(a.out, row * a.n + c0, v0, have0, a.out_f32, wide_n);
+            if (!a.glu) store_run<8>(a.out, row * a.n + c1, v1, have1, a.out_f32, wide_n);
         }
-        const bool wide = a.out_f32 ? (a.n & 3) == 0 : (a.n & 7) == 0;
-        store_run<RUN>(a.out, row * a.n + c0, v0, have0, a.out_f32, wide);
-        if (!a.glu) store_run<RUN>(a.out, row * a.n + c1, v1, have1, a.out_f32, wide);
     }
 }
 

@@ -99,13 +99,13 @@ hipError_t launch_forward(const GemmArgs& in, const GemmPlan& p, bool fp8, bool 
     if (fp8)
         err = launch_forward_fp8(a, p, grouped, stream);
     else if (p.tile == 0)
-        err = launch_gemm<256, 256, 2, 4, 2, false, false, false>(a, grouped, stream);
+        err = launch_gemm<256, 256, 2, 2, 0, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 1)
-        err = launch_gemm<128, 128, 2, 2, 2, false, false, false>(a, grouped, stream);
+        err = launch_gemm<128, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 2)
-        err = launch_gemm<64, 128, 1, 4, 3, false, false, false>(a, grouped, stream);
+        err = launch_gemm<64, 128, 1, 4, 3, 128, false, false, false>(a, grouped, stream);
     else
-        err = launch_gemm<32, 128, 1, 4, 4, false, false, false>(a, grouped, stream);
+        err = launch_gemm<32, 128, 1, 4, 4, 128, false, false, false>(a, grouped, stream);
     if (err == hipSuccess && p.splits > 1) err = launch_join(a, grouped, stream);
     return err;
 }

@@ -12,14 +12,14 @@ inline int64_t worst_pieces(const Groups& g, int bm, bool grouped) {
     return g.total / bm + (g.groups < g.total ? g.groups : g.total);
 }
 
-template <int BM, int BN, int WM, int WN, int ST, bool QT, bool PT, bool FP8>
+template <int BM, int BN, int WM, int WN, int ST, int RB, bool QT, bool PT, bool FP8>
 hipError_t launch_gemm(const GemmArgs& a, bool grouped, hipStream_t stream) {
     const int64_t half = a.glu ? BN / 2 : BN;
     const int64_t tn = (a.n + half - 1) / half;
     const int64_t tm = QT ? (int64_t)a.g.groups * ((a.m + BM - 1) / BM) : worst_pieces(a.g, BM, grouped);
     const int64_t blocks = (tm * tn * a.splits + 7) / 8 * 8;  // 8 runs of tiles, one for each XCD
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, ST, QT, PT, FP8>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
+    hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, ST, RB, QT, PT, FP8>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
                        stream, a);
     return hipGetLastError();
 }
