@@ -6,13 +6,13 @@
 // the matrix cores take bf16 pairs (a second bf16 part would double both
 // products for 8 bits that their own bf16 result cannot show).
 // Memory-bound: one pass over grad_out and preact, 16 bytes per lane. A block
-// takes 64 rows of one group and 512 columns; column sums go up through LDS
+// takes 32 rows of one group and 512 columns; column sums go up through LDS
 // in a fixed order, one fp32 row per block, which a second kernel adds in order.
 #include "cgd_gemm_launch.h"
 
 namespace cgd {
 
-constexpr int kActRows = 64;
+constexpr int kActRows = 32;
 
 __device__ __forceinline__ float act_slope(float v, int act) {
     if (act == kActRelu) return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v);
@@ -51,17 +51,29 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
     for (int q = 0; q < 8; ++q) s0[q] = s1[q] = 0.0f;
     // columns past the width, up to the row pitch of d, are zeros: the products read them
     const int64_t pad_end = a.ldd;
-    for (int i = wave; i < rows; i += 4) {
-        const int64_t row = pc.row0 + i;
-        float g[8], z[8], u[8], d0[8], d1[8];
-        if (have > 0) {
-            load_run<8>(a.grad + row * a.n + c, have, wide, g);
-            if (a.act) load_run<8>(a.pre + row * width + c, have, wide, z);
-            if (glu) load_run<8>(a.pre + row * width + a.n + c, have, wide, u);
-        } else {
+    constexpr int U = 2;  // rows of a wave on their way at a time
+    for (int i0 = wave; i0 < rows; i0 += 4 * U) {
+        float gs[U][8], zs[U][8], us[U][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) g[q] = z[q] = u[q] = 0.0f;
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + 4 * k;
+            const int64_t row = pc.row0 + i;
+            const int n = i < rows ? have : 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) zs[k][q] = us[k][q] = 0.0f;
+            load_run<8>(a.grad + row * a.n + c, n, wide, gs[k]);
+            if (a.act) load_run<8>(a.pre + row * width + c, n, wide, zs[k]);
+            if (glu) load_run<8>(a.pre + row * width + a.n + c, n, wide, us[k]);
         }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+        const int i = i0 + 4 * k;
+        if (i >= rows) break;
+        const int64_t row = pc.row0 + i;
+        float d0[8], d1[8];
+        const float(&g)[8] = gs[k];
+        const float(&z)[8] = zs[k];
+        const float(&u)[8] = us[k];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             if (glu) {
@@ -91,6 +103,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
                     for (int64_t p = width; p < pad_end; ++p) o[p] = 0;
             }
         }
+        }
     }
     if (!a.partial) return;
 #pragma unroll
@@ -108,19 +121,21 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
     }
 }
 
-// grad_b[e][c]: the partial rows of e's pieces, added in order.
+// grad_b[e][c]: the partial rows of e's pieces. A block takes 64 columns; its
+// four waves add every fourth piece in order, and their sums in order.
 __global__ __launch_bounds__(256) void bias_join_kernel(const Groups g, const float* partial, int64_t width,
                                                         uint16_t* out) {
-    const int e = blockIdx.y;
+    __shared__ float sums[4][kWave];
+    const int e = blockIdx.y, lane = lane_id(), wave = threadIdx.x / kWave;
     int before = 0, mine = 0;  // pieces of the groups before e, pieces of e
     if (!g.offset && !g.count && g.groups == 1) {
         mine = (int)((g.total + kActRows - 1) / kActRows);
     } else {
         for (int e0 = 0; e0 <= e; e0 += kWave) {
-            const int i = e0 + lane_id();
+            const int i = e0 + lane;
             int64_t b, n = 0;
             if (i <= e) group_rows(g, i, &b, &n);
-            int p = (int)((n + kActRows - 1) / kActRows);
+            const int p = (int)((n + kActRows - 1) / kActRows);
             if (i == e) mine = p;
             int sum = i < e ? p : 0;
 #pragma unroll
@@ -129,11 +144,25 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const Groups g, const fl
         }
         mine = __shfl(mine, e & (kWave - 1), kWave);
     }
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= width) return;
+    const int64_t c = (int64_t)blockIdx.x * kWave + lane;
     float s = 0.0f;
-    for (int p = 0; p < mine; ++p) s += partial[(int64_t)(before + p) * width + c];
-    out[(int64_t)e * width + c] = (uint16_t)pack_bf16x2(s, 0.0f);
+    if (c < width) {
+        const float* p = partial + (int64_t)before * width + c;
+        int i = wave;
+        for (; i + 12 < mine; i += 16) {
+            float x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) x[u] = p[(int64_t)(i + 4 * u) * width];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) s += x[u];
+        }
+        for (; i < mine; i += 4) s += p[(int64_t)i * width];
+    }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < width)
+        out[(int64_t)e * width + c] =
+            (uint16_t)pack_bf16x2(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane], 0.0f);
 }
 
 size_t act_grad_workspace_bytes(int64_t total, int groups, int64_t width, bool bias_grad) {
@@ -161,7 +190,7 @@ hipError_t launch_act_grad(const void* grad_out, const void* preact, int act, in
         if (err != hipSuccess) return err;
     }
     if (bias_grad)
-        hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((width + 255) / 256), (unsigned)g.groups), dim3(256), 0,
+        hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((width + kWave - 1) / kWave), (unsigned)g.groups), dim3(256), 0,
                            stream, g, partial, width, static_cast<uint16_t*>(bias_grad));
     return hipGetLastError();
 }

@@ -103,6 +103,16 @@ __device__ __forceinline__ void block_sync() {
     block_barrier();
 }
 
+// The same for LDS accesses alone: loads from memory stay on their way.
+__device__ __forceinline__ void sync_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// The same value, worked out anew where it is used: what follows from it is not
+// kept in registers over the main loop for the next tile.
+__device__ __forceinline__ int afresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
@@ -267,17 +277,54 @@ __device__ __forceinline__ void store_run(void* out, int64_t at, const float* v,
     }
 }
 
+// 8 values to (bf16 or fp32), or bf16 values added from, columns `apart` apart:
+// in whole 16-byte pieces where they are consecutive, the row is aligned
+// (apart == 1) and all are there.
+__device__ __forceinline__ void store_spaced(void* out, int64_t at, const float* v, int have, int apart, bool f32) {
+    if (apart == 1 && have == 8) {
+        store_run<8>(out, at, v, 8, f32, true);
+    } else if (f32) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < have) static_cast<float*>(out)[at + q * apart] = v[q];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (q < have) static_cast<uint16_t*>(out)[at + q * apart] = (uint16_t)pack_bf16x2(v[q], 0.0f);
+    }
+}
+__device__ __forceinline__ void add_spaced(const uint16_t* p, float* v, int have, int apart) {
+    if (apart == 1 && have == 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 8; q += 2) {
+            v[q] += bf16_lo(x[q / 2]);
+            v[q + 1] += bf16_hi(x[q / 2]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < have) v[q] += bf16_at(p + q * apart);
+}
+
 // Loads up to N consecutive bf16 values as fp32 (zero past `have`).
 template <int N>
 __device__ __forceinline__ void load_run(const uint16_t* p, int have, bool wide, float* v) {
     if (wide && have >= N) {
+        uint32_t w[N / 2];
+        if constexpr (N == 8) {
+            const uint4 q = *reinterpret_cast<const uint4*>(p);
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2*>(p);
+            w[0] = q.x, w[1] = q.y;
+        }
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint2 q = *reinterpret_cast<const uint2*>(p + i);
-            v[i] = bf16_lo(q.x);
-            v[i + 1] = bf16_hi(q.x);
-            v[i + 2] = bf16_lo(q.y);
-            v[i + 3] = bf16_hi(q.y);
+        for (int i = 0; i < N; i += 2) {
+            v[i] = bf16_lo(w[i / 2]);
+            v[i + 1] = bf16_hi(w[i / 2]);
         }
     } else {
 #pragma unroll
@@ -334,145 +381,69 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // ---- which tile -------------------------------------------------------
     // Blocks go to the 8 XCDs in turn; each XCD takes one run of consecutive
     // tiles, and within a run 4 row tiles share a column of tiles, so that the
-    // tiles in flight on an XCD share operands in its L2.
+    // tiles in flight on an XCD share operands in its L2. A block takes every
+    // gridDim / 8th tile of its XCD's run.
+    constexpr int GM = 4;
     const int half_n = a.glu ? BN / 2 : BN;  // output columns of a tile
     const int ntn = (int)((a.n + half_n - 1) / half_n);
-    int group, split = 0;
-    int64_t m0, rows, k0 = 0, klen;
-    int tn;
-    int64_t qrow0, prow0 = 0;
-    if (!QT) {
-        Piece pc = find_piece<false>(a.g, BM, 0);
-        const int nsplit = a.splits;
-        const int tiles = pc.total * ntn * nsplit;
-        const int per = (tiles + 7) / 8;
-        const int t0 = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-        if ((int)(blockIdx.x >> 3) >= per || t0 >= tiles) return;
-        int t = t0;
-        split = t / (pc.total * ntn);
-        t -= split * (pc.total * ntn);
-        constexpr int GM = 4;
-        const int sr = t / (GM * ntn);
-        const int gm = pc.total - sr * GM < GM ? pc.total - sr * GM : GM;
-        const int in = t - sr * GM * ntn;
-        tn = in / gm;
-        pc = find_piece<true>(a.g, BM, sr * GM + in % gm);
-        if (pc.group < 0) return;
-        group = uniform(pc.group);
-        qrow0 = uniform64(pc.row0);
-        rows = uniform64(pc.rows);
-        m0 = 0;
-        k0 = (int64_t)split * a.ksplit;
-        klen = a.k - k0 < a.ksplit ? a.k - k0 : a.ksplit;
-    } else {
-        // weight gradient: a fixed grid of tiles, the reduction over a group's rows
-        const int ntm = (int)((a.m + BM - 1) / BM);
-        const int per_group = ntm * ntn;
-        const int tiles = per_group * a.g.groups;
-        const int per = (tiles + 7) / 8;
-        const int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-        if ((int)(blockIdx.x >> 3) >= per || t >= tiles) return;
-        group = t / per_group;
-        const int in0 = t - group * per_group;
-        constexpr int GM = 4;
+    const int ntm = QT ? (int)((a.m + BM - 1) / BM) : uniform(find_piece<false>(a.g, BM, 0).total);
+    const int tiles = ntm * ntn * (QT ? a.g.groups : a.splits);
+    const int run_len = (tiles + 7) / 8;
+    struct Tile {
+        int group, split;
+        int64_t m0, rows;    // weight gradient: first output row; rows of the tile that exist (may exceed BM)
+        int64_t row0;        // first row of x (of d and x: of the reduction)
+        int64_t n0, k0, klen;
+    };
+    auto locate = [&](int seq, Tile* t) -> bool {
+        const int id = (int)(blockIdx.x & 7) * run_len + seq;
+        if (seq >= run_len || id >= tiles) return false;
+        t->split = id / (ntm * ntn);
+        const int in0 = id - t->split * (ntm * ntn);
         const int sr = in0 / (GM * ntn);
         const int gm = ntm - sr * GM < GM ? ntm - sr * GM : GM;
         const int in = in0 - sr * GM * ntn;
-        tn = in / gm;
-        m0 = (int64_t)(sr * GM + in % gm) * BM;
-        int64_t b, n;
-        if (!a.g.offset && !a.g.count && a.g.groups == 1) {
-            b = 0;
-            n = a.g.total;
-        } else {
-            group_rows(a.g, group, &b, &n);
+        const int tm = sr * GM + in % gm;
+        t->n0 = (int64_t)uniform(in / gm) * half_n;
+        if (!QT) {
+            const Piece pc = find_piece<true>(a.g, BM, tm);
+            if (pc.group < 0) return false;
+            t->group = uniform(pc.group);
+            t->row0 = uniform64(pc.row0);
+            t->rows = uniform64(pc.rows);
+            t->m0 = 0;
+            t->k0 = uniform64((int64_t)t->split * a.ksplit);
+            t->klen = uniform64(a.k - t->k0 < a.ksplit ? a.k - t->k0 : a.ksplit);
+        } else {  // the reduction goes over a group's rows
+            t->group = uniform(t->split);
+            t->split = 0;
+            int64_t b = 0, n = a.g.total;
+            if (a.g.offset || a.g.count || a.g.groups > 1) group_rows(a.g, t->group, &b, &n);
+            t->row0 = uniform64(b);
+            t->klen = uniform64(n);
+            t->k0 = 0;
+            t->m0 = (int64_t)uniform(tm) * BM;
+            t->rows = a.m - t->m0;
         }
-        qrow0 = prow0 = uniform64(b);
-        klen = uniform64(n);
-        rows = a.m - m0;
-    }
-    const int64_t n0 = (int64_t)tn * half_n;
-    const int nk = uniform((int)((klen + BK - 1) / BK));
+        return true;
+    };
+    int seq = (int)(blockIdx.x >> 3);
+    Tile cur;
+    if (!locate(seq, &cur)) return;
 
     // ---- where the operands are --------------------------------------------
-    // Q: k-contiguous: rows qrow0 .. ; transposed: columns m0 .. of rows qrow0 ..
+    // Q: k-contiguous: rows row0 .. ; transposed: columns m0 .. of rows row0 ..
     // A lane that has nothing to load in any stage (rows or columns past the
     // tile's) keeps kPastEnd; k is checked stage by stage against k_left.
-    uint64_t qb, pb0, pb1;
-    uint32_t qv[QL], pv[PL];
+    int4_t qd, pd0, pd1, sd;
+    uint32_t qv[QL], pv[PL], sv = kPastEnd;
     int qk[QT ? QL : 1], pk[PT ? PL : 1];  // where in the stage's k a lane's loads are
+    int kq_left, kp_left;                  // k left from the next stage of each on
     constexpr int ES = FP8 ? 1 : 2;
     const int ldq = (int)a.ldq, ldp = (int)a.ldp;
-    if (!QT) {
-        qb = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + k0 * ES);
-        qk[0] = ((lane & (CPR - 1)) ^ row_key<RB, 4>(wave * RPL + lane / CPR)) * (16 / ES);
-#pragma unroll
-        for (int j = 0; j < QL; ++j) {
-            const int row = (j * NW + wave) * RPL + lane / CPR;
-            qv[j] = row < rows ? (uint32_t)(row * ldq + qk[0] * ES) : kPastEnd;
-        }
-    } else {
-        constexpr int RPI = 512 / BM;  // k rows per 1-KB load
-        qb = (uint64_t)a.q + (uint64_t)(qrow0 * a.ldq + m0 * 2);
-#pragma unroll
-        for (int j = 0; j < QL; ++j) {
-            qk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
-            const int c = ((lane & (64 / RPI - 1)) ^ k_key(qk[j])) * 16;
-            qv[j] = m0 * 2 + c < a.ldq ? (uint32_t)(qk[j] * ldq + c) : kPastEnd;
-        }
-    }
-    if (!PT) {
-        const uint64_t base = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group + k0 * ES);
-        const int64_t second = a.glu ? a.n + n0 : n0 + BN / 2;  // first weight row of the tile's upper half
-        const int64_t left0 = a.n - n0, left1 = a.glu ? left0 : a.n - second;
-        pb0 = base + (uint64_t)(n0 * a.ldp);
-        pb1 = base + (uint64_t)(second * a.ldp);
-        pk[0] = ((lane & (CPR - 1)) ^ row_key<RB, RUN>(wave * RPL + lane / CPR)) * (16 / ES);
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            const int row = ((j % (PL / 2)) * NW + wave) * RPL + lane / CPR;
-            pv[j] = row < (j < PL / 2 ? left0 : left1) ? (uint32_t)(row * ldp + pk[0] * ES) : kPastEnd;
-        }
-    } else {
-        constexpr int RPI = 512 / BN;
-        pb0 = pb1 = (uint64_t)a.p + (uint64_t)((int64_t)group * a.p_group + prow0 * a.ldp + n0 * 2);
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-            pk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
-            const int c = ((lane & (64 / RPI - 1)) ^ k_key(pk[j])) * 16;
-            pv[j] = n0 * 2 + c < a.ldp ? (uint32_t)(pk[j] * ldp + c) : kPastEnd;
-        }
-    }
-    // FP8 scales: wave w < BM/64 brings those of rows 64 w .., the last wave
-    // those of the two weight blocks the tile's halves lie in (lanes 0 and 1:
-    // the halves are at most 128 wide and start at multiples of their width,
-    // and SwiGLU's up rows start at a multiple of 128).
-    uint64_t sb = 0;
-    uint32_t sv = kPastEnd;
-    int64_t s_step = 0;
-    bool s_byte = false;
-    if (FP8) {
-        const int64_t kb0 = k0 / 128;
-        if (wave == NW - 1) {
-            sb = (uint64_t)a.ps + (uint64_t)(((int64_t)group * a.ps_group + kb0) * 4);
-            const int64_t second = a.glu ? a.n + n0 : n0 + BN / 2;
-            const int64_t row = lane == 0 ? n0 : second;
-            if (lane < 2 && row < a.n * (a.glu ? 2 : 1)) sv = (uint32_t)(row / 128 * a.ps_row * 4);
-            s_step = 4;
-        } else {
-            const int row = wave * 64 + lane;
-            const int size = a.qs_byte ? 1 : 4;
-            sb = (uint64_t)a.qs + (uint64_t)((qrow0 * a.qs_row + kb0 * a.qs_blk) * size);
-            if (row < BM && row < rows) sv = (uint32_t)(row * a.qs_row * size);
-            s_step = a.qs_blk * size;
-            s_byte = a.qs_byte;
-        }
-    }
-
-    int4_t qd = buffer_from(qb), pd0 = buffer_from(pb0), pd1 = buffer_from(pb1), sd = buffer_from(sb);
-    const uint32_t lds0 = uniform((int)lds_address(smem)) + wave * 1024;
     const int64_t q_step = QT ? BK * a.ldq : RB, p_step = PT ? BK * a.ldp : RB;
-    int kq_left = uniform((int)klen), kp_left = kq_left;  // of the next stage of each to load
+    int64_t s_step = 0;
+    const bool s_byte = FP8 && a.qs_byte && wave != NW - 1;
 
     // From the last stage on (a whole one included, once it is past) lanes whose
     // piece of k lies behind the end load nothing.
@@ -487,8 +458,77 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
 #pragma unroll
         for (int j = 0; j < PL; ++j) pv[j] = pk[PT ? j : 0] < kp_left ? pv[j] : kPastEnd;
     };
-    mask_q();
-    mask_p();
+    auto aim = [&](const Tile& t) {
+        const int lane = afresh(threadIdx.x) & (kWave - 1);
+        if (!QT) {
+            qd = buffer_from((uint64_t)a.q + (uint64_t)(t.row0 * a.ldq + t.k0 * ES));
+            qk[0] = ((lane & (CPR - 1)) ^ row_key<RB, 4>(wave * RPL + lane / CPR)) * (16 / ES);
+#pragma unroll
+            for (int j = 0; j < QL; ++j) {
+                const int row = (j * NW + wave) * RPL + lane / CPR;
+                qv[j] = row < t.rows ? (uint32_t)(row * ldq + qk[0] * ES) : kPastEnd;
+            }
+        } else {
+            constexpr int RPI = 512 / BM;  // k rows per 1-KB load
+            qd = buffer_from((uint64_t)a.q + (uint64_t)(t.row0 * a.ldq + t.m0 * 2));
+#pragma unroll
+            for (int j = 0; j < QL; ++j) {
+                qk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
+                const int c = ((lane & (64 / RPI - 1)) ^ k_key(qk[j])) * 16;
+                qv[j] = t.m0 * 2 + c < a.ldq ? (uint32_t)(qk[j] * ldq + c) : kPastEnd;
+            }
+        }
+        if (!PT) {
+            const uint64_t base = (uint64_t)a.p + (uint64_t)((int64_t)t.group * a.p_group + t.k0 * ES);
+            const int64_t second = a.glu ? a.n + t.n0 : t.n0 + BN / 2;  // first weight row of the tile's upper half
+            const int64_t left0 = a.n - t.n0, left1 = a.glu ? left0 : a.n - second;
+            pd0 = buffer_from(base + (uint64_t)(t.n0 * a.ldp));
+            pd1 = buffer_from(base + (uint64_t)(second * a.ldp));
+            pk[0] = ((lane & (CPR - 1)) ^ row_key<RB, RUN>(wave * RPL + lane / CPR)) * (16 / ES);
+#pragma unroll
+            for (int j = 0; j < PL; ++j) {
+                const int row = ((j % (PL / 2)) * NW + wave) * RPL + lane / CPR;
+                pv[j] = row < (j < PL / 2 ? left0 : left1) ? (uint32_t)(row * ldp + pk[0] * ES) : kPastEnd;
+            }
+        } else {
+            constexpr int RPI = 512 / BN;
+            pd0 = pd1 = buffer_from((uint64_t)a.p + (uint64_t)((int64_t)t.group * a.p_group + (QT ? t.row0 * a.ldp : 0) + t.n0 * 2));
+#pragma unroll
+            for (int j = 0; j < PL; ++j) {
+                pk[j] = (j * NW + wave) * RPI + lane / (64 / RPI);
+                const int c = ((lane & (64 / RPI - 1)) ^ k_key(pk[j])) * 16;
+                pv[j] = t.n0 * 2 + c < a.ldp ? (uint32_t)(pk[j] * ldp + c) : kPastEnd;
+            }
+        }
+        // FP8 scales: wave w < BM/64 brings those of rows 64 w .., the last wave
+        // those of the two weight blocks the tile's halves lie in (lanes 0 and 1:
+        // the halves are at most 128 wide and start at multiples of their width,
+        // and SwiGLU's up rows start at a multiple of 128).
+        if (FP8) {
+            const int64_t kb0 = t.k0 / 128;
+            uint64_t sb = 0;
+            sv = kPastEnd;
+            if (wave == NW - 1) {
+                sb = (uint64_t)a.ps + (uint64_t)(((int64_t)t.group * a.ps_group + kb0) * 4);
+                const int64_t second = a.glu ? a.n + t.n0 : t.n0 + BN / 2;
+                const int64_t row = lane == 0 ? t.n0 : second;
+                if (lane < 2 && row < a.n * (a.glu ? 2 : 1)) sv = (uint32_t)(row / 128 * a.ps_row * 4);
+                s_step = 4;
+            } else {
+                const int row = wave * 64 + lane;
+                const int size = a.qs_byte ? 1 : 4;
+                sb = (uint64_t)a.qs + (uint64_t)((t.row0 * a.qs_row + kb0 * a.qs_blk) * size);
+                if (row < BM && row < t.rows) sv = (uint32_t)(row * a.qs_row * size);
+                s_step = a.qs_blk * size;
+            }
+            sd = buffer_from(sb);
+        }
+        kq_left = kp_left = uniform((int)t.klen);
+        mask_q();
+        mask_p();
+    };
+
+    const uint32_t lds0 = uniform((int)lds_address(smem)) + wave * 1024;
     // Load `I` of the next stage of Q (of P, of the scales); l: this wave's
     // place in the stage's slot (its loads go NW KB apart).
     auto load_q = [&](auto I, uint32_t l) { load_to_lds16<decltype(I)::value * NW * 1024>(qd, qv[decltype(I)::value], l); };
@@ -534,10 +574,32 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     };
 
     float4_t acc[MT][NT];
+    // A lane holds one row of each 16-row tile i and 4 consecutive columns of
+    // each column piece j: j < NH in the lower half of the tile, the others the
+    // same columns of the upper half.
+    auto column = [&](int j, int lg) -> int {  // within its half
+        return wn * (TN / 2) + (PT ? j % NH * 16 + lg * 4 : lg * RUN + j % NH * 4);
+    };
+    auto clear_sums = [&](const Tile& t) {  // to the bias
+        const int lg = (afresh(threadIdx.x) & (kWave - 1)) >> 4;
+        float4_t z[NT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int j = 0; j < NT; ++j) z[j] = float4_t{0.f, 0.f, 0.f, 0.f};
+        if (!PT && a.bias && a.splits == 1) {
+            const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (int64_t)t.group * (a.glu ? 2 * a.n : a.n);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < NT; ++j) {
+                const int64_t c = t.n0 + column(j, lg) + (j >= NH && !a.glu ? BN / 2 : 0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < a.n) z[j][q] = bf16_at(b + (j >= NH && a.glu ? a.n : 0) + c + q);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j) acc[i][j] = z[j];
+    };
 
     // ---- LDS addresses of a lane's fragments -------------------------------
     const CGD_LDS(char)* sm = (const CGD_LDS(char)*)smem;
@@ -580,289 +642,375 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         return turned(sm + at, 4 * (BN * 2));
     };
 
-    // ---- main loop ----------------------------------------------------------
-    if constexpr (ST == 0) {
-        // Few, large waves: the 64 products of half a stage (32 of k) run on
-        // operands that were read from LDS during the half before, with one LDS
-        // read, load or address slipped behind a product each, so that one wave
-        // per SIMD keeps its matrix unit fed. Half way through stage k every
-        // wave has read all of it: after the barrier there the loads of Q's
-        // stage k + 2 (needed a stage later, so they go first) and P's stage
-        // k + 3 (needed two stages later) take its place. Loads past the end
-        // are issued all the same (they touch no memory), which keeps the count
-        // of loads to wait for the same in every step.
-        static_assert(ST || (QL == 8 && PL == 8 && MT == 8 && NT == 8), "the schedule below is for 64 products in half a stage");
-        auto pslot = [&](int slot) { return 2 * QB + slot * PB; };
-        int p_read = 0;  // P's slot of stage kt
-        each<QL>([&](auto I) { load_q(I, lds0); });
-        next_q();
-        each<PL>([&](auto I) { load_p(I, lds0 + pslot(0)); });
-        next_p();
-        each<PL>([&](auto I) { load_p(I, lds0 + pslot(1)); });
-        next_p();
-        each<QL>([&](auto I) { load_q(I, lds0 + QB); });
-        next_q();
-        each<PL>([&](auto I) { load_p(I, lds0 + pslot(2)); });
-        next_p();
-        bf16x8_t qf[2][MT], pf[2][NT];
-        // fragment n of the next half stage: P's first, all of which its first row needs
-        auto fetch = [&](auto N, auto SET, int ks, int qbase, int pbase) {
-            constexpr int n = decltype(N)::value, set = decltype(SET)::value;
-            if constexpr (n < NT)
-                pf[set][n] = p_frag(pbase, ks, n);
-            else
-                qf[set][n - NT] = q_frag(qbase, ks, n - NT);
-        };
-        wait_loads<QL + 2 * PL>();
-        block_barrier();
-        each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, 0, pslot(0)); });
-        for (int kt = 0;;) {  // at least one stage: an empty reduction multiplies zeros
-            const int qbase = (kt & 1) * QB, pbase = pslot(p_read);
-            p_read = p_read == 2 ? 0 : p_read + 1;
-            const int qnext = QB - qbase, pnext = pslot(p_read);
-            const uint32_t fq = lds0 + qbase, fp = lds0 + pbase;
-            __builtin_amdgcn_sched_barrier(0);
-            each<64>([&](auto G) {
-                constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
-                multiply(acc[i][j], pf[0][j], qf[0][i]);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (g % 3 == 0 && g < 48) fetch(Const<g / 3>(), Const<1>(), 1, qbase, pbase);
-                __builtin_amdgcn_sched_barrier(0);
-            });
-            // Q's and P's stage kt + 1 have landed; P's kt + 2 may still be on its way
-            wait_loads<PL>();
-            block_barrier();
-            each<64>([&](auto G) {
-                constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
-                multiply(acc[i][j], pf[1][j], qf[1][i]);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (g < 16) {
-                    if constexpr (g % 2 == 0)
-                        aim_load<g / 2 * NW * 1024>(fq);
-                    else
-                        aimed_load(qd, qv[g / 2]);
-                } else if constexpr (g < 48) {
-                    constexpr int n = (g - 16) / 2;
-                    if constexpr (g % 2 == 0)
-                        fetch(Const<n>(), Const<0>(), 0, qnext, pnext);
-                    else if constexpr (n % 2 == 0)
-                        aim_load<n / 2 * NW * 1024>(fp);
-                    else
-                        aimed_load(!PT && n / 2 >= PL / 2 ? pd1 : pd0, pv[n / 2]);
-                } else if constexpr (g == 50) {
-                    next_q();
-                } else if constexpr (g == 54) {
-                    next_p();
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            });
-            if (++kt >= nk) {
-                settle();  // on the way out, before the sums are touched
-                break;
+    // ---- loads ahead of the main loop ----------------------------------------
+    auto pslot = [&](int slot) { return 2 * QB + slot * PB; };
+    // (four-wave tiles: all that does not go where the epilogue works; then the rest)
+    auto start = [&](const Tile& t) {
+        aim(t);
+        if constexpr (ST == 0) {
+            each<QL>([&](auto I) { load_q(I, lds0); });
+            next_q();
+            each<PL>([&](auto I) { load_p(I, lds0 + pslot(0)); });
+            next_p();
+            each<QL>([&](auto I) { load_q(I, lds0 + QB); });
+            next_q();
+        } else if constexpr (RB == 64) {
+#pragma unroll
+            for (int s = 0; s < ST; ++s) load_stage(s);
+        } else {
+#pragma unroll
+            for (int s = 0; s < ST - 1; ++s)
+                if (s * BK < t.klen) load_stage(s);
+        }
+    };
+    auto start_rest = [&]() {
+        if constexpr (ST == 0) {
+#pragma unroll
+            for (int s = 1; s < 3; ++s) {
+                each<PL>([&](auto I) { load_p(I, lds0 + pslot(s)); });
+                next_p();
             }
         }
-    } else if constexpr (RB == 64) {
-        // Operands are read from LDS one stage ahead into the other of two
-        // register sets, so the matrix instructions of a stage wait for
-        // nothing; ST stages are on their way or being read. Loads past the
-        // end are issued all the same (they touch no memory), which keeps the
-        // count of loads to wait for the same in every step.
-#pragma unroll
-        for (int s = 0; s < ST; ++s) load_stage(s);
-        bf16x8_t qf[2][MT], pf[2][NT];
-        wait_loads<(ST - 1) * LOADS>();
-        block_barrier();
-#pragma unroll
-        for (int j = 0; j < NT; ++j) pf[0][j] = p_frag(QB, 0, j);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) qf[0][i] = q_frag(0, 0, i);
-        int slot = 0;  // of stage kt
-        auto step = [&](auto set) {
-            constexpr int S = decltype(set)::value;
-            // stage kt + 1 has landed for every wave, and every wave has read stage kt
-            wait_loads<(ST - 2) * LOADS>();
+    };
+
+    // ---- main loop ----------------------------------------------------------
+    auto multiply_tile = [&](const int nk) {
+        if constexpr (ST == 0) {
+            // Few, large waves: the 64 products of half a stage (32 of k) run on
+            // operands that were read from LDS during the half before, with one LDS
+            // read, load or address slipped behind a product each, so that one wave
+            // per SIMD keeps its matrix unit fed. Half way through stage k every
+            // wave has read all of it: after the barrier there the loads of Q's
+            // stage k + 2 (needed a stage later, so they go first) and P's stage
+            // k + 3 (needed two stages later) take its place. Loads past the end
+            // are issued all the same (they touch no memory), which keeps the count
+            // of loads to wait for the same in every step.
+            static_assert(ST || (QL == 8 && PL == 8 && MT == 8 && NT == 8), "the schedule below is for 64 products in half a stage");
+            int p_read = 0;  // P's slot of stage kt
+            bf16x8_t qf[2][MT], pf[2][NT];
+            // fragment n of the next half stage: P's first, all of which its first row needs
+            auto fetch = [&](auto N, auto SET, int ks, int qbase, int pbase) {
+                constexpr int n = decltype(N)::value, set = decltype(SET)::value;
+                if constexpr (n < NT)
+                    pf[set][n] = p_frag(pbase, ks, n);
+                else
+                    qf[set][n - NT] = q_frag(qbase, ks, n - NT);
+            };
+            wait_loads<QL + 2 * PL>();
             block_barrier();
-            const int refill = slot;
-            slot = slot + 1 == ST ? 0 : slot + 1;
-            const int base = slot * STAGE;
-            __builtin_amdgcn_sched_barrier(0);
-            // row by row: LDS reads for the next stage, matrix instructions of
-            // this one, a load of the stage that takes the freed slot
-            each<MT>([&](auto I) {
-                constexpr int i = decltype(I)::value;
-#pragma unroll
-                for (int j = i * NT / MT; j < (i + 1) * NT / MT; ++j) pf[1 - S][j] = p_frag(base + QB, 0, j);
-                qf[1 - S][i] = q_frag(base, 0, i);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[S][j], qf[S][i], acc[i][j], 0, 0, 0);
-                if constexpr (i < LOADS) load_piece(I, refill);
-                if (i == LOADS) {
-                    next_q();
-                    next_p();
-                }
+            each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, 0, pslot(0)); });
+            for (int kt = 0;;) {  // at least one stage: an empty reduction multiplies zeros
+                const int qbase = (kt & 1) * QB, pbase = pslot(p_read);
+                p_read = p_read == 2 ? 0 : p_read + 1;
+                const int qnext = QB - qbase, pnext = pslot(p_read);
+                const uint32_t fq = lds0 + qbase, fp = lds0 + pbase;
                 __builtin_amdgcn_sched_barrier(0);
-            });
-            static_assert(LOADS < MT, "one load for each row of the wave's tile");
-        };
-        int kt = 0;
-        for (; kt + 1 < nk; kt += 2) {
-            step(Const<0>());
-            step(Const<1>());
-        }
-        if (kt < nk) step(Const<0>());
-    } else {
+                each<64>([&](auto G) {
+                    constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
+                    multiply(acc[i][j], pf[0][j], qf[0][i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (g % 3 == 0 && g < 48) fetch(Const<g / 3>(), Const<1>(), 1, qbase, pbase);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                // Q's and P's stage kt + 1 have landed; P's kt + 2 may still be on its way
+                wait_loads<PL>();
+                block_barrier();
+                each<64>([&](auto G) {
+                    constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
+                    multiply(acc[i][j], pf[1][j], qf[1][i]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (g < 16) {
+                        if constexpr (g % 2 == 0)
+                            aim_load<g / 2 * NW * 1024>(fq);
+                        else
+                            aimed_load(qd, qv[g / 2]);
+                    } else if constexpr (g < 48) {
+                        constexpr int n = (g - 16) / 2;
+                        if constexpr (g % 2 == 0)
+                            fetch(Const<n>(), Const<0>(), 0, qnext, pnext);
+                        else if constexpr (n % 2 == 0)
+                            aim_load<n / 2 * NW * 1024>(fp);
+                        else
+                            aimed_load(!PT && n / 2 >= PL / 2 ? pd1 : pd0, pv[n / 2]);
+                    } else if constexpr (g == 50) {
+                        next_q();
+                    } else if constexpr (g == 54) {
+                        next_p();
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                if (++kt >= nk) {
+                    settle();  // on the way out, before the sums are touched
+                    break;
+                }
+            }
+        } else if constexpr (RB == 64) {
+            // Operands are read from LDS one stage ahead into the other of two
+            // register sets, so the matrix instructions of a stage wait for
+            // nothing; ST stages are on their way or being read. Loads past the
+            // end are issued all the same (they touch no memory), which keeps the
+            // count of loads to wait for the same in every step.
+            bf16x8_t qf[2][MT], pf[2][NT];
+            wait_loads<(ST - 1) * LOADS>();
+            block_barrier();
 #pragma unroll
-    for (int s = 0; s < ST - 1; ++s)
-        if (s < nk) load_stage(s);
-    int buf = 0, next = ST - 1;
-    for (int kt = 0; kt < nk; ++kt) {
-        // stage kt has landed once at most the loads of the stages after it are
-        // still on their way; past the barrier it has for every wave, and the
-        // stage read in the last step may be overwritten
-        if (ST > 2 && kt + ST - 2 < nk)
-            wait_loads<(ST - 2) * LOADS>();
-        else
-            wait_loads<0>();
-        block_barrier();
-        if (kt + ST - 1 < nk) load_stage(next);
-        const int base = buf * STAGE;
-        if constexpr (!FP8) {
+            for (int j = 0; j < NT; ++j) pf[0][j] = p_frag(QB, 0, j);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8_t qf[MT], pf[NT];
+            for (int i = 0; i < MT; ++i) qf[0][i] = q_frag(0, 0, i);
+            int slot = 0;  // of stage kt
+            auto step = [&](auto set) {
+                constexpr int S = decltype(set)::value;
+                // stage kt + 1 has landed for every wave, and every wave has read stage kt
+                wait_loads<(ST - 2) * LOADS>();
+                block_barrier();
+                const int refill = slot;
+                slot = slot + 1 == ST ? 0 : slot + 1;
+                const int base = slot * STAGE;
+                __builtin_amdgcn_sched_barrier(0);
+                // row by row: LDS reads for the next stage, matrix instructions of
+                // this one, a load of the stage that takes the freed slot
+                each<MT>([&](auto I) {
+                    constexpr int i = decltype(I)::value;
 #pragma unroll
-                for (int j = 0; j < NT; ++j) pf[j] = p_frag(base + QB, ks, j);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) qf[i] = q_frag(base, ks, i);
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
+                    for (int j = i * NT / MT; j < (i + 1) * NT / MT; ++j) pf[1 - S][j] = p_frag(base + QB, 0, j);
+                    qf[1 - S][i] = q_frag(base, 0, i);
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[j], qf[i], acc[i][j], 0, 0, 0);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[S][j], qf[S][i], acc[i][j], 0, 0, 0);
+                    if constexpr (i < LOADS) load_piece(I, refill);
+                    if constexpr (i == MT - 1) {
+                        next_q();
+                        next_p();
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                static_assert(LOADS <= MT, "one load for each row of the wave's tile");
+            };
+            int kt = 0;
+            for (; kt + 1 < nk; kt += 2) {
+                step(Const<0>());
+                step(Const<1>());
             }
+            if (kt < nk) step(Const<0>());
         } else {
-            const CGD_LDS(float)* sc = (const CGD_LDS(float)*)(sm + base + QB + PB);
-            const float w0 = sc[SROWS], w1 = sc[SROWS + 1];
-            int8_t_ pf[NT];
+        int buf = 0, next = ST - 1;
+        for (int kt = 0; kt < nk; ++kt) {
+            // stage kt has landed once at most the loads of the stages after it are
+            // still on their way; past the barrier it has for every wave, and the
+            // stage read in the last step may be overwritten
+            if (ST > 2 && kt + ST - 2 < nk)
+                wait_loads<(ST - 2) * LOADS>();
+            else
+                wait_loads<0>();
+            block_barrier();
+            if (kt + ST - 1 < nk) load_stage(next);
+            const int base = buf * STAGE;
+            if constexpr (!FP8) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int4_t lo = __builtin_bit_cast(int4_t, p_frag(base + QB, 0, j)), hi = __builtin_bit_cast(int4_t, p_frag(base + QB, 1, j));
-                pf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-            }
+                for (int ks = 0; ks < 2; ++ks) {
+                    bf16x8_t qf[MT], pf[NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int4_t lo = __builtin_bit_cast(int4_t, q_frag(base, 0, i)), hi = __builtin_bit_cast(int4_t, q_frag(base, 1, i));
-                const int8_t_ qf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-                float s = sc[wm * TM + i * 16 + li];
-                if (a.qs_byte) {
-                    const uint32_t e = __float_as_uint(s);
-                    s = __uint_as_float(e ? e << 23 : 0x00400000u);
+                    for (int j = 0; j < NT; ++j) pf[j] = p_frag(base + QB, ks, j);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) qf[i] = q_frag(base, ks, i);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf[j], qf[i], acc[i][j], 0, 0, 0);
                 }
-                const float s0 = s * w0, s1 = s * w1;
+            } else {
+                const CGD_LDS(float)* sc = (const CGD_LDS(float)*)(sm + base + QB + PB);
+                const float w0 = sc[SROWS], w1 = sc[SROWS + 1];
+                int8_t_ pf[NT];
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float4_t z = {0.f, 0.f, 0.f, 0.f};
-                    const float4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[j], qf, z, 0, 0, 0, 127, 0, 127);
-                    const float f = j < NH ? s0 : s1;
+                    const int4_t lo = __builtin_bit_cast(int4_t, p_frag(base + QB, 0, j)), hi = __builtin_bit_cast(int4_t, p_frag(base + QB, 1, j));
+                    pf[j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                }
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], f, acc[i][j][r]);
+                for (int i = 0; i < MT; ++i) {
+                    const int4_t lo = __builtin_bit_cast(int4_t, q_frag(base, 0, i)), hi = __builtin_bit_cast(int4_t, q_frag(base, 1, i));
+                    const int8_t_ qf = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+                    float s = sc[wm * TM + i * 16 + li];
+                    if (a.qs_byte) {
+                        const uint32_t e = __float_as_uint(s);
+                        s = __uint_as_float(e ? e << 23 : 0x00400000u);
+                    }
+                    const float s0 = s * w0, s1 = s * w1;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float4_t z = {0.f, 0.f, 0.f, 0.f};
+                        const float4_t d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(pf[j], qf, z, 0, 0, 0, 127, 0, 127);
+                        const float f = j < NH ? s0 : s1;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], f, acc[i][j][r]);
+                    }
                 }
             }
+            buf = buf + 1 == ST ? 0 : buf + 1;
+            next = next + 1 == ST ? 0 : next + 1;
         }
-        buf = buf + 1 == ST ? 0 : buf + 1;
-        next = next + 1 == ST ? 0 : next + 1;
-    }
-    }
+        }
+    };
 
     // ---- epilogue -----------------------------------------------------------
-    // The sums go through LDS, half of each wave's rows at a time, so that the
-    // rest is a short loop (unrolled over the registers it was 170 KB of code,
-    // fetched once for each tile) that takes 8 columns of the tile's lower half
-    // and the same 8 of its upper half per lane, consecutive lanes along a row.
-    constexpr int ROWS = BM / 2, LD = BN + 4;  // 16 bytes of padding spread a column over the banks
-    static_assert(sizeof(smem) >= ROWS * LD * 4 && MT % 2 == 0, "half of the rows fit");
-    const int64_t end1 = a.glu ? 2 * a.n : a.n;            // weight rows
-    const int64_t second = a.glu ? a.n : (int64_t)BN / 2;  // from the lower half's columns to the upper half's
-    const int64_t orow0 = QT ? (int64_t)group * a.m + m0 : qrow0;
-    const bool wide_w = (end1 & 7) == 0 && (!a.glu || (a.n & 7) == 0), wide_n = (a.n & 7) == 0;
-    CGD_LDS(float)* st = (CGD_LDS(float)*)smem;
-    constexpr int RUNS = BN / 16;  // runs of 8 columns in half a tile
-    constexpr int STEP = NW * kWave / RUNS;
-    const int run = threadIdx.x % RUNS;
-    const int64_t c0 = n0 + run * 8, c1 = second + c0;
-    const int have0 = (int)(a.n - c0 < 8 ? a.n - c0 : 8);
-    const int have1 = a.glu ? have0 : (int)(a.n - c1 < 8 ? a.n - c1 : 8);
-    float bias0[8], bias1[8];
+    // The sums go through LDS, some 16-row tiles of each wave at a time, so that
+    // what follows is a short loop over rows (written out over the registers it
+    // is code that is fetched once for each tile, which took longer than the
+    // work), with 8 columns of the tile's lower half and the same 8 of its upper
+    // half per lane and lanes along a row. Four-wave tiles use two of P's slots
+    // for it, so that the next tile's first loads can travel meanwhile.
+    constexpr int PASSES = ST == 0 ? 4 : MT > 2 ? 2 : 1, IPP = MT / PASSES;
+    constexpr int STAGED = 2 * QB + PB;  // of four-wave tiles
+    constexpr int ROWS = WM * IPP * 16;
+    constexpr int RUNS = BN / 16;        // lanes along a row
+    constexpr int STEP = NW * kWave / RUNS, ITER = ROWS / STEP;
+    static_assert(MT % PASSES == 0 && ROWS % STEP == 0 && ROWS * BN * 4 + (ST ? 0 : STAGED) <= sizeof(smem), "rows of a pass fit");
+    const bool wide_n = (a.n & 7) == 0;
+    const int64_t np = (a.n + 7) / 8 * 8;  // columns of a partial sum's row: padded to whole stores
+    auto finish = [&](const Tile& t) {
+        const int tid = afresh(threadIdx.x), lane = tid & (kWave - 1), li = lane & 15, lg = lane >> 4;
+        CGD_LDS(float)* st = (CGD_LDS(float)*)(smem + (ST ? 0 : STAGED));
+        // 16-byte unit u of row r lies at u ^ key(r): 16 rows' units are spread over the banks
+        auto key = [](int r) { return (r & 15) ^ ((~r & 4) << 1); };
+        auto put = [&](auto H) {
+            constexpr int i0 = decltype(H)::value * IPP;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) bias0[q] = bias1[q] = 0.0f;
-    if (a.bias && a.splits == 1) {
-        const uint16_t* b = static_cast<const uint16_t*>(a.bias) + (int64_t)group * end1;
-        load_run<8>(b + c0, have0, false, bias0);
-        load_run<8>(b + c1, have1, false, bias1);
-    }
+            for (int i = 0; i < IPP; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        block_sync();
-#pragma unroll
-        for (int i = 0; i < MT / 2; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int c = j / NH * (BN / 2) + wn * (TN / 2) + (PT ? j % NH * 16 + lg * 4 : lg * RUN + j % NH * 4);
-                *(CGD_LDS(float4_t)*)(st + (wm * (TM / 2) + i * 16 + li) * LD + c) = acc[h * (MT / 2) + i][j];
-            }
-        block_sync();
-#pragma unroll 1
-        for (int lr = threadIdx.x / RUNS; lr < ROWS; lr += STEP) {
-            const int r = lr / (TM / 2) * TM + h * (TM / 2) + lr % (TM / 2);
-            if (r >= rows) continue;
-            float v0[8], v1[8];
-#pragma unroll
-            for (int q = 0; q < 8; q += 4) {
-                const float4_t x = *(const CGD_LDS(float4_t)*)(st + lr * LD + run * 8 + q);
-                const float4_t y = *(const CGD_LDS(float4_t)*)(st + lr * LD + BN / 2 + run * 8 + q);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    v0[q + t] = x[t] + bias0[q + t];
-                    v1[q + t] = y[t] + bias1[q + t];
+                for (int j = 0; j < NT; ++j) {
+                    const int r = (wm * IPP + i) * 16 + li, u = (j / NH * (BN / 2) + column(j, lg)) / 4;
+                    *(CGD_LDS(float4_t)*)(st + r * BN + (u ^ key(r)) * 4) = acc[i0 + i][j];
                 }
+        };
+        const int64_t out0 = QT ? (int64_t)t.group * a.m + t.m0 : t.row0;
+        const int64_t width = a.glu ? 2 * a.n : a.n;
+        const int64_t second = a.glu ? a.n : (int64_t)BN / 2;  // from the lower half's columns to the upper half's
+        const int run = tid % RUNS;
+        // where the loop below can store whole 16-byte pieces
+        const bool whole = a.splits > 1 ||
+                           (t.n0 + half_n <= a.n && !a.act &&
+                            (wide_n || (a.out_f32 && (a.n & 3) == 0 && !a.preact && !a.residual)));
+#pragma unroll 1
+        for (int h = 0; h < PASSES; ++h) {
+            sync_lds();
+            switch (h) {
+                case 0: put(Const<0>()); break;
+                case 1: put(Const<(PASSES > 1 ? 1 : 0)>()); break;
+                case 2: put(Const<(PASSES > 2 ? 2 : 0)>()); break;
+                default: put(Const<PASSES - 1>());
             }
-            const int64_t row = orow0 + r;
-            if (a.splits > 1) {  // partial sums, joined by join_kernel
-                const int64_t at = ((int64_t)split * a.g.total + row) * end1;
-                store_run<8>(a.partial, at + c0, v0, have0, true, wide_w);
-                store_run<8>(a.partial, at + c1, v1, have1, true, wide_w);
+            sync_lds();
+            auto tile_row = [&](int lr) { return lr / (IPP * 16) * TM + h * (IPP * 16) + lr % (IPP * 16); };
+            if (whole) {
+                const int64_t c0 = t.n0 + run * 8, c1 = second + c0;
+                float v0[ITER][8], v1[ITER][8];
+#pragma unroll
+                for (int k = 0; k < ITER; ++k) {
+                    const int lr = tid / RUNS + k * STEP;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float4_t x = *(const CGD_LDS(float4_t)*)(st + lr * BN + ((run * 2 + q) ^ key(lr)) * 4);
+                        const float4_t y = *(const CGD_LDS(float4_t)*)(st + lr * BN + ((BN / 8 + run * 2 + q) ^ key(lr)) * 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v0[k][q * 4 + e] = x[e];
+                            v1[k][q * 4 + e] = y[e];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < ITER; ++k) {
+                    const int r = tile_row(tid / RUNS + k * STEP);
+                    if (r >= t.rows) continue;
+                    const int64_t row = out0 + r;
+                    if (a.splits > 1) {  // partial sums, joined by join_kernel
+                        float* p = a.partial + ((int64_t)t.split * a.g.total + row) * (a.glu ? 2 * np : np);
+                        if (c0 < np) store_run<8>(p, c0, v0[k], 8, true, true);
+                        const int64_t d1 = a.glu ? np + c0 : c1;
+                        if (a.glu ? c0 < np : c1 < np) store_run<8>(p, d1, v1[k], 8, true, true);
+                        continue;
+                    }
+                    if (a.preact) {
+                        store_run<8>(a.preact, row * width + c0, v0[k], 8, false, true);
+                        store_run<8>(a.preact, row * width + c1, v1[k], 8, false, true);
+                    }
+                    if (a.glu) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v0[k][q] = silu_f(v0[k][q]) * v1[k][q];
+                    }
+                    if (a.residual) {
+                        const uint16_t* res = static_cast<const uint16_t*>(a.residual) + row * a.n;
+                        add_spaced(res + c0, v0[k], 8, 1);
+                        if (!a.glu) add_spaced(res + c1, v1[k], 8, 1);
+                    }
+                    store_run<8>(a.out, row * a.n + c0, v0[k], 8, a.out_f32, true);
+                    if (!a.glu) store_run<8>(a.out, row * a.n + c1, v1[k], 8, a.out_f32, true);
+                }
                 continue;
             }
-            if (a.preact) {
-                store_run<8>(a.preact, row * end1 + c0, v0, have0, false, wide_w);
-                store_run<8>(a.preact, row * end1 + c1, v1, have1, false, wide_w);
-            }
-            if (a.glu) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v0[q] = silu_f(v0[q]) * v1[q];
-            } else if (a.act) {
+            // everything else (an activation, a tile that sticks out to the right,
+            // rows that are not a multiple of 16 bytes): single values are stored
+            // RUNS columns apart, so that lanes store next to each other
+            const int first = wide_n ? run * 8 : run, apart = wide_n ? 1 : RUNS;
+            const int64_t c0 = t.n0 + first, c1 = second + c0;
+            const int64_t left0 = a.n - c0, left1 = a.glu ? left0 : a.n - c1;
+            const int have0 = left0 <= 0 ? 0 : left0 > 7 * apart ? 8 : (int)((left0 + apart - 1) / apart);
+            const int have1 = left1 <= 0 ? 0 : left1 > 7 * apart ? 8 : (int)((left1 + apart - 1) / apart);
+#pragma unroll 1
+            for (int lr = tid / RUNS; lr < ROWS; lr += STEP) {
+                const int r = tile_row(lr);
+                if (r >= t.rows) continue;
+                float v0[8], v1[8];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    v0[q] = act_f(v0[q], a.act);
-                    v1[q] = act_f(v1[q], a.act);
+                    const int c = first + q * apart;
+                    v0[q] = st[lr * BN + ((c / 4) ^ key(lr)) * 4 + c % 4];
+                    v1[q] = st[lr * BN + ((BN / 8 + c / 4) ^ key(lr)) * 4 + c % 4];
                 }
-            }
-            if (a.residual) {
-                const uint16_t* res = static_cast<const uint16_t*>(a.residual) + row * a.n;
-                float z[8];
-                load_run<8>(res + c0, have0, wide_n, z);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v0[q] += z[q];
-                if (!a.glu) {
-                    load_run<8>(res + c1, have1, wide_n, z);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v1[q] += z[q];
+                const int64_t row = out0 + r;
+                if (a.preact) {
+                    store_spaced(a.preact, row * width + c0, v0, have0, apart, false);
+                    store_spaced(a.preact, row * width + c1, v1, have1, apart, false);
                 }
+                if (a.glu) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v0[q] = silu_f(v0[q]) * v1[q];
+                } else if (a.act) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        v0[q] = act_f(v0[q], a.act);
+                        v1[q] = act_f(v1[q], a.act);
+                    }
+                }
+                if (a.residual) {
+                    const uint16_t* res = static_cast<const uint16_t*>(a.residual) + row * a.n;
+                    add_spaced(res + c0, v0, have0, apart);
+                    if (!a.glu) add_spaced(res + c1, v1, have1, apart);
+                }
+                store_spaced(a.out, row * a.n + c0, v0, have0, apart, a.out_f32);
+                if (!a.glu) store_spaced(a.out, row * a.n + c1, v1, have1, apart, a.out_f32);
             }
-            store_run<8>(a.out, row * a.n + c0, v0, have0, a.out_f32, wide_n);
-            if (!a.glu) store_run<8>(a.out, row * a.n + c1, v1, have1, a.out_f32, wide_n);
         }
+    };
+
+    // ---- the block's tiles ----------------------------------------------------
+    start(cur);
+    start_rest();
+    for (;;) {
+        Tile next;
+        seq += (int)(gridDim.x >> 3);
+        const bool more = ST == 0 && locate(seq, &next);
+        clear_sums(cur);
+        multiply_tile(uniform((int)((cur.klen + BK - 1) / BK)));
+        block_sync();  // every wave is done with LDS, and no load is on its way there
+        if (more) start(next);
+        finish(cur);
+        if (!more) return;
+        sync_lds();
+        start_rest();
+        cur = next;
     }
 }
 

@@ -38,7 +38,7 @@ GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, 
             const int64_t each = (steps + s - 1) / s;
             p.splits = (int)((steps + each - 1) / each);
             p.ksplit = each * bk;
-            if (p.splits > 1) p.partial_bytes = (size_t)p.splits * g.total * wide * 4;
+            if (p.splits > 1) p.partial_bytes = (size_t)p.splits * g.total * ((n + 7) / 8 * 8 * (glu ? 2 : 1)) * 4;
         }
     }
     p.blocks = p.blocks * p.splits + 8;
@@ -46,41 +46,67 @@ GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, 
 }
 
 // Sums the pieces of a split reduction in order and applies the epilogue. A
-// block takes 8 rows of one group (dense: of the batch) and 256 columns.
-constexpr int kJoinRows = 8;
+// wave takes 256 columns of one row, 4 per lane: all its loads are independent
+// and several are on their way at a time.
+constexpr int kJoinRows = 4;
+
+__device__ __forceinline__ float4_t join_pieces(const float* p, int64_t slice, int splits) {
+    float4_t v = {0.f, 0.f, 0.f, 0.f};
+    int s = 0;
+    for (; s + 4 <= splits; s += 4) {
+        float4_t x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4_t*>(p + (s + u) * slice);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v += x[u];
+    }
+    for (; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(p + s * slice);
+    return v;
+}
+
 __global__ __launch_bounds__(256) void join_kernel(const GemmArgs a) {
     const Piece pc = find_piece<true>(a.g, kJoinRows, (int)blockIdx.x);
     if (pc.group < 0) return;
-    const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
-    if (c >= a.n) return;
-    const int64_t wide = a.glu ? 2 * a.n : a.n;
-    const int64_t slice = a.g.total * wide;
-    const int rows = pc.rows < kJoinRows ? (int)pc.rows : kJoinRows;
-    const uint16_t* b = static_cast<const uint16_t*>(a.bias);
-    const float bias0 = b ? bf16_at(b + pc.group * wide + c) : 0.0f;
-    const float bias1 = b && a.glu ? bf16_at(b + pc.group * wide + a.n + c) : 0.0f;
-    for (int i = 0; i < rows; ++i) {
-        const int64_t row = pc.row0 + i;
-        const float* p = a.partial + row * wide + c;
-        float v = 0.0f, u = 0.0f;
-        for (int s = 0; s < a.splits; ++s) {
-            v += p[s * slice];
-            if (a.glu) u += p[s * slice + a.n];
-        }
-        v += bias0;
-        u += bias1;
-        if (a.preact) {
-            uint16_t* z = static_cast<uint16_t*>(a.preact) + row * wide;
-            z[c] = (uint16_t)pack_bf16x2(v, 0.0f);
-            if (a.glu) z[a.n + c] = (uint16_t)pack_bf16x2(u, 0.0f);
-        }
-        v = a.glu ? silu_f(v) * u : act_f(v, a.act);
-        if (a.residual) v += bf16_at(static_cast<const uint16_t*>(a.residual) + row * a.n + c);
-        if (a.out_f32)
-            static_cast<float*>(a.out)[row * a.n + c] = v;
-        else
-            static_cast<uint16_t*>(a.out)[row * a.n + c] = (uint16_t)pack_bf16x2(v, 0.0f);
+    const int r = threadIdx.x / kWave;
+    const int64_t c = (int64_t)blockIdx.y * 256 + lane_id() * 4;
+    if (c >= a.n || r >= pc.rows) return;
+    const int have = (int)(a.n - c < 4 ? a.n - c : 4);
+    const int64_t width = a.glu ? 2 * a.n : a.n;
+    const int64_t np = (a.n + 7) / 8 * 8, pitch = a.glu ? 2 * np : np;  // a partial row, padded
+    const int64_t slice = a.g.total * pitch, row = pc.row0 + r;
+    const bool wide = (a.n & 3) == 0;
+    float v[4], u[4] = {0.f, 0.f, 0.f, 0.f}, z[4];
+    const float4_t sv = join_pieces(a.partial + row * pitch + c, slice, a.splits);
+    float4_t su = {0.f, 0.f, 0.f, 0.f};
+    if (a.glu) su = join_pieces(a.partial + row * pitch + np + c, slice, a.splits);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[q] = sv[q];
+        u[q] = su[q];
     }
+    if (a.bias) {
+        const uint16_t* b = static_cast<const uint16_t*>(a.bias) + pc.group * width;
+        load_run<4>(b + c, have, false, z);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += z[q];
+        if (a.glu) {
+            load_run<4>(b + a.n + c, have, false, z);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) u[q] += z[q];
+        }
+    }
+    if (a.preact) {
+        store_run<4>(a.preact, row * width + c, v, have, false, wide);
+        if (a.glu) store_run<4>(a.preact, row * width + a.n + c, u, have, false, wide);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = a.glu ? silu_f(v[q]) * u[q] : act_f(v[q], a.act);
+    if (a.residual) {
+        load_run<4>(static_cast<const uint16_t*>(a.residual) + row * a.n + c, have, wide, z);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] += z[q];
+    }
+    store_run<4>(a.out, row * a.n + c, v, have, a.out_f32, wide);
 }
 
 hipError_t launch_join(const GemmArgs& a, bool grouped, hipStream_t stream) {
@@ -101,7 +127,7 @@ hipError_t launch_forward(const GemmArgs& in, const GemmPlan& p, bool fp8, bool 
     else if (p.tile == 0)
         err = launch_gemm<256, 256, 2, 2, 0, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 1)
-        err = launch_gemm<128, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
+        err = launch_gemm<128, 128, 2, 2, 5, 64, false, false, false>(a, grouped, stream);
     else if (p.tile == 2)
         err = launch_gemm<64, 128, 1, 4, 3, 128, false, false, false>(a, grouped, stream);
     else

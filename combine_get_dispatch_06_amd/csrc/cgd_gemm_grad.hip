@@ -27,18 +27,18 @@ int64_t grad_blocks(const Groups& g, bool grouped, int64_t width, int64_t k) {
 hipError_t launch_input_grad(const GemmArgs& a, bool grouped, hipStream_t stream) {
     const int tile = input_tile(a.g, grouped, a.n);
     if (tile == 0) return launch_gemm<256, 256, 2, 2, 0, 128, false, true, false>(a, grouped, stream);
-    if (tile == 1) return launch_gemm<128, 128, 2, 2, 2, 128, false, true, false>(a, grouped, stream);
-    return launch_gemm<64, 128, 1, 4, 3, 128, false, true, false>(a, grouped, stream);
+    if (tile == 1) return launch_gemm<128, 128, 2, 2, 5, 64, false, true, false>(a, grouped, stream);
+    return launch_gemm<64, 128, 1, 4, 6, 64, false, true, false>(a, grouped, stream);
 }
 
 hipError_t launch_weight_grad(const GemmArgs& a, hipStream_t stream) {
     if (weight_tile(a.g, a.m, a.n) == 0) return launch_gemm<256, 256, 2, 2, 0, 128, true, true, false>(a, true, stream);
-    return launch_gemm<128, 128, 2, 2, 2, 128, true, true, false>(a, true, stream);
+    return launch_gemm<128, 128, 2, 2, 5, 64, true, true, false>(a, true, stream);
 }
 
 hipError_t preload_gemm_grad() {
     hipFuncAttributes at;
-    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&gemm_kernel<128, 128, 2, 2, 2, 128, true, true, false>));
+    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&gemm_kernel<128, 128, 2, 2, 5, 64, true, true, false>));
 }
 
 }  // namespace cgd
