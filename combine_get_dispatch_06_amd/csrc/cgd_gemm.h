@@ -370,8 +370,8 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     static_assert(RB == 128 || RB == 64, "a stage holds 128 or 64 bytes of k");
     static_assert(PT || (NW * RPL % ((RB == 64 ? 4 : 2) * RUN) == 0 && (BN / 2) % ((RB == 64 ? 4 : 2) * RUN) == 0), "a lane's piece of k is the same in all its loads");
     static_assert(!FP8 || SROWS / 64 + 1 <= NW, "one wave loads 64 row scales, one the weights'");
-    // ST stages of both operands; or (ST = 0) two of Q and three of P, all 160 KB
-    __shared__ __attribute__((aligned(1024))) char smem[ST ? ST * STAGE : 2 * QB + 3 * PB];
+    // ST stages of both operands; or (ST = 0) two of P and three of Q, all 160 KB
+    __shared__ __attribute__((aligned(1024))) char smem[ST ? ST * STAGE : 3 * QB + 2 * PB];
 
     const int lane = lane_id();
     const int wave = uniform(threadIdx.x / kWave);
@@ -643,17 +643,17 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     };
 
     // ---- loads ahead of the main loop ----------------------------------------
-    auto pslot = [&](int slot) { return 2 * QB + slot * PB; };
+    auto qslot = [&](int slot) { return 2 * PB + slot * QB; };
     // (four-wave tiles: all that does not go where the epilogue works; then the rest)
     auto start = [&](const Tile& t) {
         aim(t);
         if constexpr (ST == 0) {
-            each<QL>([&](auto I) { load_q(I, lds0); });
-            next_q();
-            each<PL>([&](auto I) { load_p(I, lds0 + pslot(0)); });
+            each<PL>([&](auto I) { load_p(I, lds0); });
             next_p();
-            each<QL>([&](auto I) { load_q(I, lds0 + QB); });
+            each<QL>([&](auto I) { load_q(I, lds0 + qslot(0)); });
             next_q();
+            each<PL>([&](auto I) { load_p(I, lds0 + PB); });
+            next_p();
         } else if constexpr (RB == 64) {
 #pragma unroll
             for (int s = 0; s < ST; ++s) load_stage(s);
@@ -667,8 +667,8 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         if constexpr (ST == 0) {
 #pragma unroll
             for (int s = 1; s < 3; ++s) {
-                each<PL>([&](auto I) { load_p(I, lds0 + pslot(s)); });
-                next_p();
+                each<QL>([&](auto I) { load_q(I, lds0 + qslot(s)); });
+                next_q();
             }
         }
     };
@@ -680,13 +680,17 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
             // operands that were read from LDS during the half before, with one LDS
             // read, load or address slipped behind a product each, so that one wave
             // per SIMD keeps its matrix unit fed. Half way through stage k every
-            // wave has read all of it: after the barrier there the loads of Q's
-            // stage k + 2 (needed a stage later, so they go first) and P's stage
-            // k + 3 (needed two stages later) take its place. Loads past the end
-            // are issued all the same (they touch no memory), which keeps the count
-            // of loads to wait for the same in every step.
+            // wave has read all of it: after the barrier there the loads of P's
+            // stage k + 2 (needed a stage later, so they go first) and Q's stage
+            // k + 3 (needed two stages later) take its place. Three slots for Q
+            // (activations, which come from HBM and are shared by fewer tiles in
+            // flight) and two for P measured 1350 us at 32768 x 4096 x 7168, the
+            // other way round 1425. Loads past the end are issued all the same
+            // (they touch no memory), which keeps the count of loads to wait for
+            // the same in every step. 32 x 32 products need half the instructions
+            // but measured slower (more traffic of sums for the same power).
             static_assert(ST || (QL == 8 && PL == 8 && MT == 8 && NT == 8), "the schedule below is for 64 products in half a stage");
-            int p_read = 0;  // P's slot of stage kt
+            int q_read = 0;  // Q's slot of stage kt
             bf16x8_t qf[2][MT], pf[2][NT];
             // fragment n of the next half stage: P's first, all of which its first row needs
             auto fetch = [&](auto N, auto SET, int ks, int qbase, int pbase) {
@@ -696,13 +700,13 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                 else
                     qf[set][n - NT] = q_frag(qbase, ks, n - NT);
             };
-            wait_loads<QL + 2 * PL>();
+            wait_loads<PL + 2 * QL>();
             block_barrier();
-            each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, 0, pslot(0)); });
+            each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, qslot(0), 0); });
             for (int kt = 0;;) {  // at least one stage: an empty reduction multiplies zeros
-                const int qbase = (kt & 1) * QB, pbase = pslot(p_read);
-                p_read = p_read == 2 ? 0 : p_read + 1;
-                const int qnext = QB - qbase, pnext = pslot(p_read);
+                const int pbase = (kt & 1) * PB, qbase = qslot(q_read);
+                q_read = q_read == 2 ? 0 : q_read + 1;
+                const int pnext = PB - pbase, qnext = qslot(q_read);
                 const uint32_t fq = lds0 + qbase, fp = lds0 + pbase;
                 __builtin_amdgcn_sched_barrier(0);
                 each<64>([&](auto G) {
@@ -712,8 +716,8 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                     if constexpr (g % 3 == 0 && g < 48) fetch(Const<g / 3>(), Const<1>(), 1, qbase, pbase);
                     __builtin_amdgcn_sched_barrier(0);
                 });
-                // Q's and P's stage kt + 1 have landed; P's kt + 2 may still be on its way
-                wait_loads<PL>();
+                // Q's and P's stage kt + 1 have landed; Q's kt + 2 may still be on its way
+                wait_loads<QL>();
                 block_barrier();
                 each<64>([&](auto G) {
                     constexpr int g = decltype(G)::value, i = g / 8, j = g % 8;
@@ -721,17 +725,17 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                     __builtin_amdgcn_sched_barrier(0);
                     if constexpr (g < 16) {
                         if constexpr (g % 2 == 0)
-                            aim_load<g / 2 * NW * 1024>(fq);
+                            aim_load<g / 2 * NW * 1024>(fp);
                         else
-                            aimed_load(qd, qv[g / 2]);
+                            aimed_load(!PT && g / 2 >= PL / 2 ? pd1 : pd0, pv[g / 2]);
                     } else if constexpr (g < 48) {
                         constexpr int n = (g - 16) / 2;
                         if constexpr (g % 2 == 0)
                             fetch(Const<n>(), Const<0>(), 0, qnext, pnext);
                         else if constexpr (n % 2 == 0)
-                            aim_load<n / 2 * NW * 1024>(fp);
+                            aim_load<n / 2 * NW * 1024>(fq);
                         else
-                            aimed_load(!PT && n / 2 >= PL / 2 ? pd1 : pd0, pv[n / 2]);
+                            aimed_load(qd, qv[n / 2]);
                     } else if constexpr (g == 50) {
                         next_q();
                     } else if constexpr (g == 54) {
@@ -859,10 +863,10 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // what follows is a short loop over rows (written out over the registers it
     // is code that is fetched once for each tile, which took longer than the
     // work), with 8 columns of the tile's lower half and the same 8 of its upper
-    // half per lane and lanes along a row. Four-wave tiles use two of P's slots
+    // half per lane and lanes along a row. Four-wave tiles use two of Q's slots
     // for it, so that the next tile's first loads can travel meanwhile.
     constexpr int PASSES = ST == 0 ? 4 : MT > 2 ? 2 : 1, IPP = MT / PASSES;
-    constexpr int STAGED = 2 * QB + PB;  // of four-wave tiles
+    constexpr int STAGED = 2 * PB + QB;  // of four-wave tiles
     constexpr int ROWS = WM * IPP * 16;
     constexpr int RUNS = BN / 16;        // lanes along a row
     constexpr int STEP = NW * kWave / RUNS, ITER = ROWS / STEP;

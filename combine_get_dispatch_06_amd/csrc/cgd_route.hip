@@ -35,28 +35,46 @@ __device__ __forceinline__ uint32_t order_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, kWave));
-    return v;
+// Reductions over the wave, by lane moves within the vector unit: shifts by 1, 2,
+// 4 and 8 within rows of 16 lanes, then each row's last lane to the rows behind.
+// Lane 63 ends up with all 64; lanes that a move does not reach keep `own`.
+template <int CTRL>
+__device__ __forceinline__ uint32_t move_lanes(uint32_t own, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)own, (int)v, CTRL, 0xF, 0xF, false);
 }
-// LDS writes of this wave's lanes before its reads that follow
-__device__ __forceinline__ void wave_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-template <typename T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, kWave);
-    return v;
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t identity, F f) {
+    v = f(v, move_lanes<0x111>(identity, v));
+    v = f(v, move_lanes<0x112>(identity, v));
+    v = f(v, move_lanes<0x114>(identity, v));
+    v = f(v, move_lanes<0x118>(identity, v));
+    // row_bcast 15 reaches rows 1 and 3, row_bcast 31 rows 2 and 3
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x142, 0xA, 0xF, false));
+    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x143, 0xC, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
 }
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ uint32_t wave_umin(uint32_t v) {
+    return wave_reduce(v, ~0u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+__device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
+    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), __float_as_uint(-INFINITY), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+__device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        const uint32_t o = __shfl_xor(v, d, kWave);
-        v = o > v ? o : v;
-    }
+    for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, kWave);
     return v;
 }
 __device__ __forceinline__ uint64_t wave_umax64(uint64_t v) {
@@ -66,6 +84,12 @@ __device__ __forceinline__ uint64_t wave_umax64(uint64_t v) {
         v = o > v ? o : v;
     }
     return v;
+}
+
+// LDS writes of this wave's lanes before its reads that follow
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i) {
@@ -144,7 +168,18 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
         if (WIDE) {
             if (lane < a.groups) {
                 double b1 = -INFINITY, b2 = -INFINITY;
-                for (int i = 0; i < per_group; ++i) {
+                int i = 0;
+                for (; i + 8 <= per_group; i += 8) {  // eight reads on their way at a time
+                    double x[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) x[u] = all[wave][lane * per_group + i + u];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        b2 = fmax(b2, fmin(b1, x[u]));
+                        b1 = fmax(b1, x[u]);
+                    }
+                }
+                for (; i < per_group; ++i) {
                     const double x = all[wave][lane * per_group + i];
                     b2 = fmax(b2, fmin(b1, x));
                     b1 = fmax(b1, x);
@@ -179,6 +214,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
     uint32_t lo = 1u;
     if (a.E > kWave && __popcll(ballot(mine >= 1u)) > a.K) {
         // invariant: at least K lanes reach lo, fewer than K reach hi
+        lo = wave_umin(mine);
+        lo = lo > 1u ? lo : 1u;
         uint32_t hi = wave_umax(mine);
         if (__popcll(ballot(mine >= hi)) >= a.K) {
             lo = hi;
@@ -208,8 +245,12 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
             const uint64_t m = ballot(k32[j] >= lo);
             if (k32[j] >= lo) {
                 const int p = at + __popcll(m & lanemask_lt());
-                cand_key[wave][p] = WIDE ? order_key64(c[j]) : (uint64_t)k32[j];
-                cand_id[wave][p] = lane + j * kWave;
+                if (WIDE) {
+                    cand_key[wave][p] = order_key64(c[j]);
+                    cand_id[wave][p] = lane + j * kWave;
+                } else {
+                    cand_key[wave][p] = ((uint64_t)k32[j] << 32) | (uint32_t)(lane + j * kWave);
+                }
             }
             at += __popcll(m);
         }
@@ -217,17 +258,31 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
         uint64_t key = 0;
         if (lane < found) {
             key = cand_key[wave][lane];
-            id = cand_id[wave][lane];
+            id = WIDE ? cand_id[wave][lane] : (int)(uint32_t)key;
+            if (!WIDE) key >>= 32;
         }
-        int ahead = 0;
-        for (int i = 0; i < found; ++i) {
-            const uint32_t oh = __builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i);
-            const uint32_t ol = __builtin_amdgcn_readlane((int)(uint32_t)key, i);
-            const int oi = __builtin_amdgcn_readlane(id, i);
-            const uint64_t o = ((uint64_t)oh << 32) | ol;
-            ahead += (o > key || (o == key && oi < id)) ? 1 : 0;
+        // the candidates are in ascending order of index: of equal values the one
+        // in a lower lane is ahead
+        uint32_t ahead = 0;
+        if (WIDE) {
+            for (int i = 0; i < found; ++i) {
+                const uint64_t o = ((uint64_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, i);
+                ahead += o > key ? 1u : 0u;
+            }
+        } else {
+            const uint32_t k = (uint32_t)key;
+            for (int i = 0; i < found; ++i) ahead += (uint32_t)__builtin_amdgcn_readlane((int)k, i) > k ? 1u : 0u;
         }
-        if (lane < found) place = ahead;
+        // without equal values the places are 0 .. found - 1
+        if (wave_usum(lane < found ? ahead : 0u) != (uint32_t)(found * (found - 1) / 2)) {
+            for (int i = 0; i < found; ++i) {
+                const uint64_t o = ((uint64_t)__builtin_amdgcn_readlane((int)(uint32_t)(key >> 32), i) << 32) |
+                                   (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, i);
+                ahead += o == key && i < lane ? 1u : 0u;
+            }
+        }
+        if (lane < found) place = (int)ahead;
     } else {
         // rounds: the best value, then among its holders the lowest index
         for (int k = 0; k < a.K; ++k) {
@@ -259,21 +314,24 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 
     // weights of the chosen
     const bool chosen = id >= 0 && place < a.K;
-    double s = 0.0;
+    float s = 0.0f;
     if (chosen) {
         const float x = load_logit(a.logits, a.logits_bf16, t * a.E + id);
-        if (a.sigmoid)
-            s = 1.0 / (1.0 + exp(-(double)x));
-        else
-            s = WIDE ? exp((double)x - (double)top) / norm : (double)expf(x - top) / norm;
+        // renormalised softmax needs no denominator: it cancels
+        s = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : a.renormalize ? expf(x - top) : expf(x - top) / (float)norm;
     }
     if (a.renormalize) {
-        const double total = wave_sum(s);
-        s = total > 0.0 ? s / total : 0.0;
+        if (a.sigmoid && wave_max(s) < 1e-30f) {  // scores this small: all of them scaled up by the same factor
+            const float x = chosen ? load_logit(a.logits, a.logits_bf16, t * a.E + id) : -INFINITY;
+            const float best = wave_max(x);
+            s = chosen && best > -745.0f ? expf(x - best) : 0.0f;  // below that they are zero in 64 bits too
+        }
+        const float total = wave_sum(s);
+        s = total > 0.0f ? s / total : 0.0f;
     }
     if (chosen) {
         a.topk_idx[t * a.K + place] = id;
-        a.topk_weights[t * a.K + place] = (float)(s * (double)a.scale);
+        a.topk_weights[t * a.K + place] = s * a.scale;
     }
     const int n = __popcll(ballot(chosen));
     if (lane >= n && lane < a.K) {
@@ -284,9 +342,9 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 
 // Gradient of the weights with respect to the logits:
 //   softmax:               dl_e = scale * p_e * (G_e - sum_i G_i p_i), G_e = sum of g over e's slots
-//   softmax, renormalised: the same over the chosen alone (p renormalised)
 //   sigmoid:               dl_e = scale * G_e * s_e (1 - s_e)
-//   sigmoid, renormalised: dl_e = scale * sum over e's slots (g - sum_j g_j s_j / S) / S * s_e (1 - s_e), S = sum_j s_j
+//   renormalised, with shares w = s / (sum of s over the slots):
+//                          dl_e = scale * w_e * sum over e's slots (g - sum_j g_j w_j), times (1 - s_e) for sigmoid
 // One wave per token, one pass. An expert that appears in several slots of a
 // token collects them in slot order; values outside [0, E) are no slot.
 template <int PER>
@@ -316,60 +374,59 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(const Ro
         }
     }
     top = wave_max(top);
-    const bool none = top == -INFINITY;
 
-    // score of the slot's expert, and the denominators
-    float ps, inv = 1.0f;
-    if (a.sigmoid) {
-        ps = id >= 0 ? 1.0f / (1.0f + expf(-x)) : 0.0f;
-    } else {
-        ps = id >= 0 && !none ? expf(x - top) : 0.0f;
-    }
-    float p[PER];
-    if (a.sigmoid) {
-#pragma unroll
-        for (int j = 0; j < PER; ++j) p[j] = 1.0f / (1.0f + expf(-l[j]));
-    } else {
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            p[j] = none ? 0.0f : expf(l[j] - top);
-            sum += p[j];
-        }
-        sum = wave_sum(sum);
-        inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) p[j] *= inv;
-        ps *= inv;
-    }
+    // p: the score of each expert; ps: that of the slot's. Renormalised: the share
+    // of the chosen total instead, from exponentials relative to the largest
+    // chosen logit (softmax; sigmoid where all chosen scores are tiny).
+    float p[PER], ps = 0.0f;
+    float ref = top, inv = 1.0f;
+    bool by_exp = !a.sigmoid;
     if (a.renormalize) {
-        // a chosen share of the chosen total: its gradient in the scores first
-        const float total = wave_sum(ps);
-        const float it = total > 0.0f ? 1.0f / total : 0.0f;
-        const float dot = wave_sum(g * ps) * it;
-        g = id >= 0 ? (g - dot) * it : 0.0f;
+        ref = wave_max(x);
+        by_exp = by_exp || ref < -60.0f;
+    }
+    const bool none = ref == -INFINITY || (a.sigmoid && ref < -745.0f);  // zero in 64 bits too
+    if (!none && id >= 0) ps = by_exp ? expf(x - ref) : 1.0f / (1.0f + expf(-x));
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        // (renormalised, experts above the largest chosen one get no gradient: kept finite)
+        p[j] = none ? 0.0f : by_exp ? expf(fminf(l[j] - ref, 0.0f)) : 1.0f / (1.0f + expf(-l[j]));
+        sum += p[j];
+    }
+    if (a.renormalize)
+        sum = wave_sum(ps);
+    else
+        sum = a.sigmoid ? 1.0f : wave_sum(sum);
+    inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) p[j] *= inv;
+    ps *= inv;
+    if (a.renormalize) {
+        const float dot = wave_sum(g * ps);
+        g = id >= 0 ? g - dot : 0.0f;
     }
     // one sum for each expert, in slot order, written by its first slot
-    float sum = 0.0f;
+    float slots = 0.0f;
     bool first = id >= 0;
     for (int k = 0; k < a.K; ++k) {
         const int oi = __builtin_amdgcn_readlane(id, k);
         const float og = __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(g), k));
         if (oi == id) {
-            sum += og;
+            slots += og;
             if (k < lane) first = false;
         }
     }
     wave_fence();
-    if (first) slot_grad[wave][id] = sum;
+    if (first) slot_grad[wave][id] = slots;
     wave_fence();
-    const float dot = a.sigmoid ? 0.0f : wave_sum(id >= 0 ? g * ps : 0.0f);
+    const float dot = a.sigmoid || a.renormalize ? 0.0f : wave_sum(id >= 0 ? g * ps : 0.0f);
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = lane + j * kWave;
         if (e >= a.E) continue;
-        const float G = slot_grad[wave][e];
-        const float d = a.sigmoid ? G * p[j] * (1.0f - p[j]) : p[j] * (G - dot);
+        float d = p[j] * (slot_grad[wave][e] - dot);
+        if (a.sigmoid) d *= 1.0f / (1.0f + expf(l[j]));  // 1 - s
         if (a.logits_bf16)
             static_cast<uint16_t*>(a.grad_logits)[t * a.E + e] = (uint16_t)pack_bf16x2(d, 0.0f);
         else
