@@ -29,46 +29,46 @@ namespace cgd {
 constexpr int kRouteWaves = 4;
 constexpr int kRouteMaxGroups = 64;
 
-// fp32 -> unsigned with the same order; 0 is below every value
+// fp32 -> unsigned with the same order; kNone is -inf, and there is nothing below it
+constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t order_key(float v) {
     const uint32_t b = __float_as_uint(v);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float from_key(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
 // Reductions over the wave, by lane moves within the vector unit: shifts by 1, 2,
 // 4 and 8 within rows of 16 lanes, then each row's last lane to the rows behind.
-// Lane 63 ends up with all 64; lanes that a move does not reach keep `own`.
-template <int CTRL>
-__device__ __forceinline__ uint32_t move_lanes(uint32_t own, uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)own, (int)v, CTRL, 0xF, 0xF, false);
+// Lanes that a move does not reach get 0, which changes neither a sum nor a
+// maximum of unsigned values, so that move and operation are one instruction.
+// Lane 63 ends up with all 64.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, ROWS == 0xF);
 }
 template <typename F>
-__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t identity, F f) {
-    v = f(v, move_lanes<0x111>(identity, v));
-    v = f(v, move_lanes<0x112>(identity, v));
-    v = f(v, move_lanes<0x114>(identity, v));
-    v = f(v, move_lanes<0x118>(identity, v));
-    // row_bcast 15 reaches rows 1 and 3, row_bcast 31 rows 2 and 3
-    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x142, 0xA, 0xF, false));
-    v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)identity, (int)v, 0x143, 0xC, 0xF, false));
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+    v = f(v, moved<0x111, 0xF>(v));
+    v = f(v, moved<0x112, 0xF>(v));
+    v = f(v, moved<0x114, 0xF>(v));
+    v = f(v, moved<0x118, 0xF>(v));
+    v = f(v, moved<0x142, 0xA>(v));  // rows 1 and 3 from the row before
+    v = f(v, moved<0x143, 0xC>(v));  // rows 2 and 3 from row 1
     return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
 }
 __device__ __forceinline__ uint32_t wave_umax(uint32_t v) {
-    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ uint32_t wave_umin(uint32_t v) {
-    return wave_reduce(v, ~0u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-}
+__device__ __forceinline__ uint32_t wave_umin(uint32_t v) { return ~wave_umax(~v); }
 __device__ __forceinline__ uint32_t wave_usum(uint32_t v) {
-    return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a + b; });
+    return wave_reduce(v, [](uint32_t a, uint32_t b) { return a + b; });
 }
-__device__ __forceinline__ float wave_max(float v) {
-    return __uint_as_float(wave_reduce(__float_as_uint(v), __float_as_uint(-INFINITY), [](uint32_t a, uint32_t b) {
-        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-    }));
-}
+__device__ __forceinline__ float wave_max(float v) { return from_key(wave_umax(order_key(v))); }
 __device__ __forceinline__ float wave_sum(float v) {
-    return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __uint_as_float(wave_reduce(__float_as_uint(v), [](uint32_t a, uint32_t b) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
@@ -92,10 +92,26 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ float load_logit(const void* p, bool bf16, int64_t i) {
-    float v = bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
-    if (!(v == v)) v = -INFINITY;
-    return v > 3.402823466e38f ? 3.402823466e38f : v;
+// A logit as fp32, cleaned: NaN counts as -inf, +inf as the largest finite value.
+__device__ __forceinline__ float clean(float v) {
+    return fminf(fmaxf(v, -INFINITY), 3.402823466e38f);  // fmaxf gives the other operand for NaN
+}
+template <bool BF16>
+__device__ __forceinline__ float raw_logit(const void* p, int64_t i) {
+    return BF16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(p)[i] << 16) : static_cast<const float*>(p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+    return clean(raw_logit<BF16>(p, i));
+}
+// A lane's logits of token t, still uncleaned (nothing waits for them here).
+template <bool BF16, int PER>
+__device__ __forceinline__ void fetch_logits(const void* p, int64_t t, int64_t T, int E, float (&v)[PER]) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = lane_id() + j * kWave;
+        v[j] = e < E && t < T ? raw_logit<BF16>(p, t * E + e) : -INFINITY;
+    }
 }
 
 // 64-bit doubles as unsigned with the same order (-0 counts as +0)
@@ -104,23 +120,27 @@ __device__ __forceinline__ uint64_t order_key64(double v) {
     return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
 }
 
+// Bound by vector instructions (some 400 a token), so 28 waves of a CU that each
+// wait for their own token hide its latency: fewer waves that take tokens in turn
+// with the next one's logits on their way hold twice the registers and measured
+// 39 us against 35 (top-16 of 512, 32768 tokens).
 // WIDE: choices in 64 bits. PER: experts per lane.
-template <bool WIDE, int PER>
+template <bool WIDE, bool BF16, int PER>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteArgs a) {
     __shared__ uint64_t cand_key[kRouteWaves][kWave];
     __shared__ int cand_id[kRouteWaves][kWave];
+    __shared__ float cand_x[kRouteWaves][kWave];
     __shared__ double all[WIDE ? kRouteWaves : 1][WIDE ? PER * kWave : 1];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
     if (t >= a.T) return;  // waves are independent: no block barrier below
-
     float l[PER];
+    fetch_logits<BF16>(a.logits, t, a.T, a.E, l);
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int e = lane + j * kWave;
-        l[j] = e < a.E ? load_logit(a.logits, a.logits_bf16, t * a.E + e) : -INFINITY;
+        l[j] = clean(l[j]);
         top = fmaxf(top, l[j]);
     }
     top = wave_max(top);
@@ -157,8 +177,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 
     // groups
     uint64_t keep = ~0ull;
-    const int per_group = a.E / a.groups;
-    if (a.groups > 1 && a.topk_groups < a.groups) {
+    const int per_group = WIDE ? a.E / a.groups : 1;
+    if (WIDE && a.groups > 1 && a.topk_groups < a.groups) {
         double v = -INFINITY;
         if (WIDE) {
 #pragma unroll
@@ -204,19 +224,17 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = lane + j * kWave;
-        bool ok = e < a.E && l[j] > -INFINITY;
-        if (WIDE) ok = ok && c[j] > -INFINITY;
-        if (a.groups > 1 && ok) ok = (keep >> (e / per_group)) & 1;
-        const float v = WIDE ? (float)c[j] + 0.0f : l[j] + 0.0f;
-        k32[j] = ok ? order_key(v) : 0u;
+        float v = WIDE ? (float)c[j] + 0.0f : l[j] + 0.0f;
+        if (WIDE && a.groups > 1 && e < a.E && !((keep >> (e / per_group)) & 1)) v = -INFINITY;
+        k32[j] = order_key(v);  // -inf: kNone
         mine = k32[j] > mine ? k32[j] : mine;
     }
-    uint32_t lo = 1u;
-    if (a.E > kWave && __popcll(ballot(mine >= 1u)) > a.K) {
+    uint32_t lo = kNone + 1u;
+    if (a.E > kWave && __popcll(ballot(mine > kNone)) > a.K) {
         // invariant: at least K lanes reach lo, fewer than K reach hi
-        lo = wave_umin(mine);
-        lo = lo > 1u ? lo : 1u;
-        uint32_t hi = wave_umax(mine);
+        const uint32_t least = wave_umin(mine);
+        lo = least > lo ? least : lo;
+        uint32_t hi = WIDE ? wave_umax(mine) : order_key(top + 0.0f);
         if (__popcll(ballot(mine >= hi)) >= a.K) {
             lo = hi;
         } else {
@@ -238,13 +256,15 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 
     // candidates -> places
     int id = -1, place = 1 << 20;
+    float x = -INFINITY;  // the candidate's logit
     if (found <= kWave) {
         int at = 0;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
             const uint64_t m = ballot(k32[j] >= lo);
             if (k32[j] >= lo) {
-                const int p = at + __popcll(m & lanemask_lt());
+                const int p = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+                cand_x[wave][p] = l[j];
                 if (WIDE) {
                     cand_key[wave][p] = order_key64(c[j]);
                     cand_id[wave][p] = lane + j * kWave;
@@ -260,6 +280,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
             key = cand_key[wave][lane];
             id = WIDE ? cand_id[wave][lane] : (int)(uint32_t)key;
             if (!WIDE) key >>= 32;
+            x = cand_x[wave][lane];
         }
         // the candidates are in ascending order of index: of equal values the one
         // in a lower lane is ahead
@@ -289,7 +310,7 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
             uint64_t best = 0;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                const uint64_t key = k32[j] ? (WIDE ? order_key64(c[j]) : (uint64_t)k32[j]) : 0ull;
+                const uint64_t key = k32[j] > kNone ? (WIDE ? order_key64(c[j]) : (uint64_t)k32[j]) : 0ull;
                 best = key > best ? key : best;
             }
             best = wave_umax64(best);
@@ -297,17 +318,18 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
             uint32_t first = 0;  // largest of ~index: the lowest index
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                const uint64_t key = k32[j] ? (WIDE ? order_key64(c[j]) : (uint64_t)k32[j]) : 0ull;
+                const uint64_t key = k32[j] > kNone ? (WIDE ? order_key64(c[j]) : (uint64_t)k32[j]) : 0ull;
                 const uint32_t inv = ~(uint32_t)(lane + j * kWave);
                 if (key == best && inv > first) first = inv;
             }
             const int e = (int)~wave_umax(first);
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (lane + j * kWave == e) k32[j] = 0u;
+                if (lane + j * kWave == e) k32[j] = kNone;
             if (lane == k) {
                 id = e;
                 place = k;
+                x = load_logit<BF16>(a.logits, t * a.E + e);
             }
         }
     }
@@ -316,14 +338,12 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
     const bool chosen = id >= 0 && place < a.K;
     float s = 0.0f;
     if (chosen) {
-        const float x = load_logit(a.logits, a.logits_bf16, t * a.E + id);
         // renormalised softmax needs no denominator: it cancels
         s = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : a.renormalize ? expf(x - top) : expf(x - top) / (float)norm;
     }
     if (a.renormalize) {
         if (a.sigmoid && wave_max(s) < 1e-30f) {  // scores this small: all of them scaled up by the same factor
-            const float x = chosen ? load_logit(a.logits, a.logits_bf16, t * a.E + id) : -INFINITY;
-            const float best = wave_max(x);
+            const float best = wave_max(chosen ? x : -INFINITY);
             s = chosen && best > -745.0f ? expf(x - best) : 0.0f;  // below that they are zero in 64 bits too
         }
         const float total = wave_sum(s);
@@ -347,32 +367,39 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
 //                          dl_e = scale * w_e * sum over e's slots (g - sum_j g_j w_j), times (1 - s_e) for sigmoid
 // One wave per token, one pass. An expert that appears in several slots of a
 // token collects them in slot order; values outside [0, E) are no slot.
-template <int PER>
+template <bool BF16, int PER>
 __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(const RouteGradArgs a) {
     __shared__ float slot_grad[kRouteWaves][PER * kWave];
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves + wave;
     if (t >= a.T) return;
-    float l[PER];
+    float l[PER], slot_g = 0.0f;
+    int64_t slot_i = -1;
+    fetch_logits<BF16>(a.logits, t, a.T, a.E, l);
+    if (lane < a.K) {
+        slot_i = a.topk_idx[t * a.K + lane];
+        slot_g = a.grad_weights[t * a.K + lane];
+    }
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
         const int e = lane + j * kWave;
-        l[j] = e < a.E ? load_logit(a.logits, a.logits_bf16, t * a.E + e) : -INFINITY;
+        l[j] = clean(l[j]);
         top = fmaxf(top, l[j]);
-        slot_grad[wave][e] = 0.0f;
+        slot_grad[wave][e] = l[j];  // for the slots to read, then their gradients
     }
+    wave_fence();
     int id = -1;
     float g = 0.0f, x = -INFINITY;
-    if (lane < a.K) {
-        const int64_t i = a.topk_idx[t * a.K + lane];
-        if (i >= 0 && i < a.E) {
-            id = (int)i;
-            g = a.grad_weights[t * a.K + lane] * a.scale;
-            x = load_logit(a.logits, a.logits_bf16, t * a.E + id);
-        }
+    if (slot_i >= 0 && slot_i < a.E) {
+        id = (int)slot_i;
+        g = slot_g * a.scale;
+        x = slot_grad[wave][id];
     }
+    wave_fence();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) slot_grad[wave][lane + j * kWave] = 0.0f;
     top = wave_max(top);
 
     // p: the score of each expert; ps: that of the slot's. Renormalised: the share
@@ -427,52 +454,59 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(const Ro
         if (e >= a.E) continue;
         float d = p[j] * (slot_grad[wave][e] - dot);
         if (a.sigmoid) d *= 1.0f / (1.0f + expf(l[j]));  // 1 - s
-        if (a.logits_bf16)
+        if (BF16)
             static_cast<uint16_t*>(a.grad_logits)[t * a.E + e] = (uint16_t)pack_bf16x2(d, 0.0f);
         else
             static_cast<float*>(a.grad_logits)[t * a.E + e] = d;
     }
 }
 
-template <bool WIDE>
+static dim3 route_grid(int64_t T) { return dim3((unsigned)((T + kRouteWaves - 1) / kRouteWaves)); }
+
+template <bool WIDE, bool BF16>
 static void route_launch(const RouteArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+    const dim3 grid = route_grid(a.T), block(kRouteWaves * kWave);
     if (a.E <= 64)
-        hipLaunchKernelGGL((route_kernel<WIDE, 1>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((route_kernel<WIDE, BF16, 1>), grid, block, 0, stream, a);
     else if (a.E <= 128)
-        hipLaunchKernelGGL((route_kernel<WIDE, 2>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((route_kernel<WIDE, BF16, 2>), grid, block, 0, stream, a);
     else if (a.E <= 256)
-        hipLaunchKernelGGL((route_kernel<WIDE, 4>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((route_kernel<WIDE, BF16, 4>), grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL((route_kernel<WIDE, 8>), grid, block, 0, stream, a);
+        hipLaunchKernelGGL((route_kernel<WIDE, BF16, 8>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
     if (a.bias || a.groups > 1)
-        route_launch<true>(a, stream);
+        a.logits_bf16 ? route_launch<true, true>(a, stream) : route_launch<true, false>(a, stream);
     else
-        route_launch<false>(a, stream);
+        a.logits_bf16 ? route_launch<false, true>(a, stream) : route_launch<false, false>(a, stream);
     return hipGetLastError();
+}
+
+template <bool BF16>
+static void route_grad_launch(const RouteGradArgs& a, hipStream_t stream) {
+    const dim3 grid = route_grid(a.T), block(kRouteWaves * kWave);
+    if (a.E <= 64)
+        hipLaunchKernelGGL((route_grad_kernel<BF16, 1>), grid, block, 0, stream, a);
+    else if (a.E <= 128)
+        hipLaunchKernelGGL((route_grad_kernel<BF16, 2>), grid, block, 0, stream, a);
+    else if (a.E <= 256)
+        hipLaunchKernelGGL((route_grad_kernel<BF16, 4>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((route_grad_kernel<BF16, 8>), grid, block, 0, stream, a);
 }
 
 hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
-    const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
-    if (a.E <= 64)
-        hipLaunchKernelGGL((route_grad_kernel<1>), grid, block, 0, stream, a);
-    else if (a.E <= 128)
-        hipLaunchKernelGGL((route_grad_kernel<2>), grid, block, 0, stream, a);
-    else if (a.E <= 256)
-        hipLaunchKernelGGL((route_grad_kernel<4>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((route_grad_kernel<8>), grid, block, 0, stream, a);
+    a.logits_bf16 ? route_grad_launch<true>(a, stream) : route_grad_launch<false>(a, stream);
     return hipGetLastError();
 }
 
 hipError_t preload_route() {
     hipFuncAttributes at;
-    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&route_grad_kernel<8>));
+    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&route_grad_kernel<false, 8>));
 }
 
 }  // namespace cgd

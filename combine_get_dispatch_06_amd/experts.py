@@ -22,7 +22,7 @@ import ctypes
 
 import torch
 
-from . import (CgdError, DispatchHandle, SCALE_F32, SCALE_UE8M0, _check, _dev_tensor, _ptr, _stream, load)
+from . import DispatchHandle, SCALE_F32, SCALE_UE8M0, _check, _dev_tensor, load
 
 __all__ = ["route", "route_backward", "linear", "linear_backward", "grouped_linear", "grouped_linear_backward"]
 
@@ -57,6 +57,34 @@ def configure(lib):
     lib.cgd_grouped_linear_backward.argtypes = [vp, vp, vp, i64, i32, vp, i64, vp, i64, i64, vp, i32, vp, vp, vp, vp,
                                                 sz, vp]
     return lib
+
+
+class _Current:
+    """Makes a device current for a call, where it is not already (a quarter of
+    the cost of torch.cuda.device there)."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, dev):
+        self.index = dev.index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev):
+    """The current stream's handle (torch.cuda.current_stream makes an object of it first)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _choice(table: dict, value, name: str) -> int:
@@ -122,7 +150,7 @@ def route(logits: torch.Tensor, num_topk: int, scoring: str = "softmax", bias: t
         _shaped(bias, "bias", torch.float32, (E,), dev)
     if num_topk_groups is None:
         num_topk_groups = num_groups
-    with torch.cuda.device(dev):
+    with _Current(dev):
         idx = torch.empty((T, max(num_topk, 0)), dtype=torch.int64, device=dev)
         wts = torch.empty((T, max(num_topk, 0)), dtype=torch.float32, device=dev)
         _check("cgd_route",
@@ -144,7 +172,7 @@ def route_backward(grad_topk_weights: torch.Tensor, logits: torch.Tensor, topk_i
     K = topk_idx.shape[1]
     _shaped(topk_idx, "topk_idx", torch.int64, (T, K), dev)
     _shaped(grad_topk_weights, "grad_topk_weights", torch.float32, (T, K), dev)
-    with torch.cuda.device(dev):
+    with _Current(dev):
         out = torch.empty_like(logits)
         _check("cgd_route_backward",
                lib.cgd_route_backward(_ptr(grad_topk_weights), _ptr(logits), ltype, _ptr(topk_idx), T, E, K, mode,
@@ -239,7 +267,7 @@ def linear(x, weight, bias: torch.Tensor | None = None, activation: str | None =
         _shaped(residual, "residual", torch.bfloat16, (T, O), dev)
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype must be bfloat16 or float32 (got {out_dtype})")
-    with torch.cuda.device(dev):
+    with _Current(dev):
         if out is None:
             out = torch.empty((T, O), dtype=out_dtype, device=dev)
         else:
@@ -301,7 +329,7 @@ def grouped_linear(x, weight, groups, bias: torch.Tensor | None = None, activati
         _shaped(bias, "bias", torch.bfloat16, (G, rows), dev)
     cap = lead[1] if nd == 3 else 0
     N = lead[0] * lead[1] if nd == 3 else lead[0]
-    with torch.cuda.device(dev):
+    with _Current(dev):
         if out is None:
             out = torch.empty((*lead, O), dtype=torch.bfloat16, device=dev)
         else:
@@ -333,7 +361,7 @@ def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
         raise ValueError("preact goes with an activation")
     if preact is not None:
         _shaped(preact, "preact", torch.bfloat16, (T, rows), dev)
-    with torch.cuda.device(dev):
+    with _Current(dev):
         gx, gw = torch.empty_like(x), torch.empty_like(w)
         gb = torch.empty(rows, dtype=torch.bfloat16, device=dev) if bias_grad else None
         nbytes = lib.cgd_linear_backward_workspace_bytes(T, K, O, act, int(bias_grad))
@@ -377,7 +405,7 @@ def grouped_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: tor
         _shaped(preact, "preact", torch.bfloat16, (*lead, rows), dev)
     cap = lead[1] if packed else 0
     N = lead[0] * lead[1] if packed else lead[0]
-    with torch.cuda.device(dev):
+    with _Current(dev):
         gx, gw = torch.empty_like(x), torch.empty_like(w)
         gb = torch.empty((G, rows), dtype=torch.bfloat16, device=dev) if bias_grad else None
         nbytes = lib.cgd_grouped_linear_backward_workspace_bytes(N, G, K, O, act, int(bias_grad))
