@@ -370,8 +370,16 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     static_assert(RB == 128 || RB == 64, "a stage holds 128 or 64 bytes of k");
     static_assert(PT || (NW * RPL % ((RB == 64 ? 4 : 2) * RUN) == 0 && (BN / 2) % ((RB == 64 ? 4 : 2) * RUN) == 0), "a lane's piece of k is the same in all its loads");
     static_assert(!FP8 || SROWS / 64 + 1 <= NW, "one wave loads 64 row scales, one the weights'");
-    // ST stages of both operands; or (ST = 0) two of P and three of Q, all 160 KB
-    __shared__ __attribute__((aligned(1024))) char smem[ST ? ST * STAGE : 3 * QB + 2 * PB];
+    // The epilogue's rows go through LDS PASSES times, IPP 16-row tiles of each wave at a time.
+    constexpr int PASSES = ST == 0 ? 4 : MT > 4 ? MT : MT > 2 ? 2 : 1, IPP = MT / PASSES;
+    constexpr int ROWS = WM * IPP * 16;
+    // Tiles with a CU to themselves: one block for each CU takes them in turn.
+    constexpr bool ALONE = ST == 0 || BM * BN > 128 * 128;
+    // LDS: ST stages of both operands, and where the next tile's loads travel during the epilogue, its rows;
+    // or (ST = 0) two of P and three of Q, all 160 KB, the epilogue's rows in two of Q's.
+    constexpr int STAGED = ST == 0 ? 2 * PB + QB : ALONE ? ST * STAGE : 0;
+    constexpr int LDS_BYTES = ST == 0 ? 3 * QB + 2 * PB : ST * STAGE + (ALONE ? ROWS * BN * 4 : 0);
+    __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
     const int lane = lane_id();
     const int wave = uniform(threadIdx.x / kWave);
@@ -865,17 +873,14 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // work), with 8 columns of the tile's lower half and the same 8 of its upper
     // half per lane and lanes along a row. Four-wave tiles use two of Q's slots
     // for it, so that the next tile's first loads can travel meanwhile.
-    constexpr int PASSES = ST == 0 ? 4 : MT > 2 ? 2 : 1, IPP = MT / PASSES;
-    constexpr int STAGED = 2 * PB + QB;  // of four-wave tiles
-    constexpr int ROWS = WM * IPP * 16;
     constexpr int RUNS = BN / 16;        // lanes along a row
     constexpr int STEP = NW * kWave / RUNS, ITER = ROWS / STEP;
-    static_assert(MT % PASSES == 0 && ROWS % STEP == 0 && ROWS * BN * 4 + (ST ? 0 : STAGED) <= sizeof(smem), "rows of a pass fit");
+    static_assert(MT % PASSES == 0 && ROWS % STEP == 0 && ROWS * BN * 4 + STAGED <= LDS_BYTES, "rows of a pass fit");
     const bool wide_n = (a.n & 7) == 0;
     const int64_t np = (a.n + 7) / 8 * 8;  // columns of a partial sum's row: padded to whole stores
     auto finish = [&](const Tile& t) {
         const int tid = afresh(threadIdx.x), lane = tid & (kWave - 1), li = lane & 15, lg = lane >> 4;
-        CGD_LDS(float)* st = (CGD_LDS(float)*)(smem + (ST ? 0 : STAGED));
+        CGD_LDS(float)* st = (CGD_LDS(float)*)(smem + STAGED);
         // 16-byte unit u of row r lies at u ^ key(r): 16 rows' units are spread over the banks
         auto key = [](int r) { return (r & 15) ^ ((~r & 4) << 1); };
         auto put = [&](auto H) {
@@ -896,15 +901,10 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         const bool whole = a.splits > 1 ||
                            (t.n0 + half_n <= a.n && !a.act &&
                             (wide_n || (a.out_f32 && (a.n & 3) == 0 && !a.preact && !a.residual)));
-#pragma unroll 1
-        for (int h = 0; h < PASSES; ++h) {
+        each<PASSES>([&](auto H) {  // written out: with a variable index the sums would live in memory
+            constexpr int h = decltype(H)::value;
             sync_lds();
-            switch (h) {
-                case 0: put(Const<0>()); break;
-                case 1: put(Const<(PASSES > 1 ? 1 : 0)>()); break;
-                case 2: put(Const<(PASSES > 2 ? 2 : 0)>()); break;
-                default: put(Const<PASSES - 1>());
-            }
+            put(H);
             sync_lds();
             auto tile_row = [&](int lr) { return lr / (IPP * 16) * TM + h * (IPP * 16) + lr % (IPP * 16); };
             if (whole) {
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                     store_run<8>(a.out, row * a.n + c0, v0[k], 8, a.out_f32, true);
                     if (!a.glu) store_run<8>(a.out, row * a.n + c1, v1[k], 8, a.out_f32, true);
                 }
-                continue;
+                return;
             }
             // everything else (an activation, a tile that sticks out to the right,
             // rows that are not a multiple of 16 bytes): single values are stored
@@ -996,7 +996,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                 store_spaced(a.out, row * a.n + c0, v0, have0, apart, a.out_f32);
                 if (!a.glu) store_spaced(a.out, row * a.n + c1, v1, have1, apart, a.out_f32);
             }
-        }
+        });
     };
 
     // ---- the block's tiles ----------------------------------------------------
@@ -1005,7 +1005,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     for (;;) {
         Tile next;
         seq += (int)(gridDim.x >> 3);
-        const bool more = ST == 0 && locate(seq, &next);
+        const bool more = ALONE && locate(seq, &next);
         clear_sums(cur);
         multiply_tile(uniform((int)((cur.klen + BK - 1) / BK)));
         block_sync();  // every wave is done with LDS, and no load is on its way there

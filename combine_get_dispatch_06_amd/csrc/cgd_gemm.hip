@@ -127,7 +127,7 @@ hipError_t launch_forward(const GemmArgs& in, const GemmPlan& p, bool fp8, bool 
     else if (p.tile == 0)
         err = launch_gemm<256, 256, 2, 2, 0, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 1)
-        err = launch_gemm<128, 128, 2, 2, 5, 64, false, false, false>(a, grouped, stream);
+        err = launch_gemm<128, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 2)
         err = launch_gemm<64, 128, 1, 4, 3, 128, false, false, false>(a, grouped, stream);
     else
