@@ -4,34 +4,31 @@
 
 namespace cgd {
 
-// Tile by rows per group (grouped products see the average) and by how many
-// tiles there are:
-//   256 x 256 once it gives most CUs a tile; 128 x 128 below that; 64 and 32
-//   rows where a group has fewer (what is read then is the weights, and a
-//   taller tile would only multiply by zeros).
-// A reduction is split where even so most CUs had no tile.
+// Tile shapes: 256 x 256 (FP8: 192 x 256, which leaves LDS for the epilogue) once
+// there is one for most CUs; 128 x 128 below that, two blocks to a CU; 32 x 128
+// for a dense product of up to 128 rows, where a tall tile leaves fewer blocks to
+// share the weights' read (4096 x 4096 for 64 rows: 13.6 us against 16.8). Grouped
+// products of few rows keep the tall tile: every group's weights are read anyway,
+// and a group that does not fit one tile reads them twice (16 experts, 64 rows
+// each on average, 7168 -> 2 x 2048: 176 us against 206 with 64 rows a tile).
+// A reduction is split where even so there were fewer than 512 blocks (two for a CU).
+constexpr int kSplitBlocks = 512;
+static const int kTileRows[3] = {256, 128, 32}, kTileColumns[3] = {256, 128, 128};
+
 GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, bool grouped) {
     GemmPlan p;
     const int64_t per = grouped ? (g.total + g.groups - 1) / g.groups : g.total;
     const int64_t wide = n * (glu ? 2 : 1);
-    auto tiles = [&](int bm, int bn) { return worst_pieces(g, bm, grouped) * ((wide + bn - 1) / bn); };
-    if (per > 128 && tiles(256, 256) >= 200)
-        p.tile = 0;
-    else if (per > 64)
-        p.tile = 1;
-    else if (per > 32)
-        p.tile = 2;
-    else
-        p.tile = 3;
+    auto tiles = [&](int t) { return worst_pieces(g, kTileRows[t], grouped) * ((wide + kTileColumns[t] - 1) / kTileColumns[t]); };
+    p.tile = per > 128 && tiles(0) >= 200 ? 0 : grouped || per > 128 ? 1 : 2;
     p.splits = 1;
     p.ksplit = k;
     p.partial_bytes = 0;
-    p.blocks = tiles(256, 256);
+    const int64_t t = tiles(p.tile);
     if (p.tile > 0) {
         const int bk = fp8 ? 128 : 64;
-        const int64_t t = p.blocks = tiles(p.tile == 1 ? 128 : p.tile == 2 ? 64 : 32, 128);
         const int64_t steps = (k + bk - 1) / bk;
-        int64_t s = t > 0 ? 512 / t : 1;
+        int64_t s = t > 0 ? kSplitBlocks / t : 1;
         if (s > steps / 4) s = steps / 4;
         if (s > 32) s = 32;
         if (s > 1) {
@@ -41,7 +38,7 @@ GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, 
             if (p.splits > 1) p.partial_bytes = (size_t)p.splits * g.total * ((n + 7) / 8 * 8 * (glu ? 2 : 1)) * 4;
         }
     }
-    p.blocks = p.blocks * p.splits + 8;
+    p.blocks = 2 * t * p.splits + 8;  // (FP8's 192 rows: at most 4/3 as many tiles)
     return p;
 }
 
@@ -128,8 +125,6 @@ hipError_t launch_forward(const GemmArgs& in, const GemmPlan& p, bool fp8, bool 
         err = launch_gemm<256, 256, 2, 2, 0, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 1)
         err = launch_gemm<128, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
-    else if (p.tile == 2)
-        err = launch_gemm<64, 128, 1, 4, 3, 128, false, false, false>(a, grouped, stream);
     else
         err = launch_gemm<32, 128, 1, 4, 4, 128, false, false, false>(a, grouped, stream);
     if (err == hipSuccess && p.splits > 1) err = launch_join(a, grouped, stream);

@@ -9,7 +9,6 @@ namespace cgd {
 hipError_t launch_forward_fp8(const GemmArgs& a, const GemmPlan& p, bool grouped, hipStream_t stream) {
     if (p.tile == 0) return launch_gemm<192, 256, 2, 4, 2, 128, false, false, true>(a, grouped, stream);
     if (p.tile == 1) return launch_gemm<128, 128, 2, 2, 2, 128, false, false, true>(a, grouped, stream);
-    if (p.tile == 2) return launch_gemm<64, 128, 1, 4, 3, 128, false, false, true>(a, grouped, stream);
     return launch_gemm<32, 128, 1, 4, 3, 128, false, false, true>(a, grouped, stream);
 }
 
