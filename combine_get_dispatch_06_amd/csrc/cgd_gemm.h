@@ -244,6 +244,16 @@ __device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const b
 // compiler does not see them in multiply(), so it inserts no waits of its own).
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
+// d = p q over 128 of k, not accumulated. It keeps its place among the volatile
+// statements; results_here() has to stand between it and the first use of d, with
+// four others or settle() before that. After a use it keeps that in its place.
+__device__ __forceinline__ void product_fp8(float4_t& d, const int8_t_& p, const int8_t_& q) {
+    asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, 0" : "=&v"(d) : "v"(p), "v"(q));
+}
+__device__ __forceinline__ void results_here(float4_t (&d)[4]) {
+    asm volatile("" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]));
+}
+
 // Stores N (4 or 8) consecutive values of one output row from column c on, as
 // bf16 or fp32, in 8- or 16-byte pieces where the row allows it (`wide`).
 template <int N>
@@ -375,10 +385,11 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     constexpr int ROWS = WM * IPP * 16;
     // Tiles with a CU to themselves: one block for each CU takes them in turn.
     constexpr bool ALONE = ST == 0 || BM * BN > 128 * 128;
-    // LDS: ST stages of both operands, and where the next tile's loads travel during the epilogue, its rows;
-    // or (ST = 0) two of P and three of Q, all 160 KB, the epilogue's rows in two of Q's.
-    constexpr int STAGED = ST == 0 ? 2 * PB + QB : ALONE ? ST * STAGE : 0;
-    constexpr int LDS_BYTES = ST == 0 ? 3 * QB + 2 * PB : ST * STAGE + (ALONE ? ROWS * BN * 4 : 0);
+    // LDS: ST stages of both operands; or (ST = 0) two of P and three of Q, all
+    // 160 KB, the epilogue's rows in two of Q's; or (FP8) two of P, three of Q and
+    // of the scales, the epilogue's rows in the second of P's.
+    constexpr int STAGED = ST == 0 ? 2 * PB + QB : ALONE ? PB : 0;
+    constexpr int LDS_BYTES = ST == 0 ? 3 * QB + 2 * PB : ALONE ? 2 * PB + 3 * (QB + SB) : ST * STAGE;
     __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
     const int lane = lane_id();
@@ -653,9 +664,19 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // ---- loads ahead of the main loop ----------------------------------------
     auto qslot = [&](int slot) { return 2 * PB + slot * QB; };
     // (four-wave tiles: all that does not go where the epilogue works; then the rest)
+    constexpr int S_AT = 2 * PB + 3 * QB;  // the scales' slots
     auto start = [&](const Tile& t) {
         aim(t);
-        if constexpr (ST == 0) {
+        if constexpr (FP8 && ALONE) {
+            each<PL>([&](auto I) { load_p(I, lds0); });
+            next_p();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                each<QL>([&](auto I) { load_q(I, lds0 + qslot(s)); });
+                load_s(lds0 + S_AT + s * SB);
+                next_q();
+            }
+        } else if constexpr (ST == 0) {
             each<PL>([&](auto I) { load_p(I, lds0); });
             next_p();
             each<QL>([&](auto I) { load_q(I, lds0 + qslot(0)); });
@@ -672,7 +693,10 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         }
     };
     auto start_rest = [&]() {
-        if constexpr (ST == 0) {
+        if constexpr (FP8 && ALONE) {
+            each<PL>([&](auto I) { load_p(I, lds0 + PB); });
+            next_p();
+        } else if constexpr (ST == 0) {
 #pragma unroll
             for (int s = 1; s < 3; ++s) {
                 each<QL>([&](auto I) { load_q(I, lds0 + qslot(s)); });
@@ -683,7 +707,100 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
 
     // ---- main loop ----------------------------------------------------------
     auto multiply_tile = [&](const int nk) {
-        if constexpr (ST == 0) {
+        if constexpr (FP8 && ALONE) {
+            // A step is 128 of k: MT rows of NT products from zero, added with their
+            // scales in the row behind (vector and matrix instructions of two waves
+            // share a SIMD). A row's operand and scale are read one row ahead. The
+            // barrier of a step stands before the last row of the step before, whose
+            // operands are in registers by then: that row, and the sums of the one
+            // before it, cover the first LDS reads.
+            // Its P operands make room one by one for the new step's. They are all in
+            // registers after the first row: a second barrier then frees P's slot, so
+            // two slots give its loads nearly two steps' time as three give Q's.
+            int8_t_ pf[NT], qf[2];
+            float4_t d[2][NT];
+            uint32_t sx[2] = {0, 0};  // as they are in memory
+            float w0 = 0.f, w1 = 0.f;
+            auto whole = [&](const CGD_LDS(char)* at, int a0, int a1, int off) -> int8_t_ {
+                const int4_t lo = *(const CGD_LDS(int4_t)*)(at + a0 + off), hi = *(const CGD_LDS(int4_t)*)(at + a1 + off);
+                return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+            };
+            auto read_p = [&](int base, int j) {
+                return whole(sm + base, pa[0], pa[1], j / NH * (BN / 2) * RB + j % NH * 4 * RB);
+            };
+            auto read_q = [&](int slot, int i) { return whole(sm + qslot(slot), qa[0], qa[1], i * 16 * RB); };
+            const int sa = afresh(S_AT + (wm * TM + li) * 4);
+            auto read_s = [&](int at, int i) { return *(const CGD_LDS(uint32_t)*)(sm + at + i * 64); };
+            auto product = [&](auto I, int j) {
+                constexpr int i = decltype(I)::value & 1;
+                product_fp8(d[i][j], pf[j], qf[i]);
+            };
+            auto add = [&](auto I) {  // row I's products, times both scales; the next row's stand between
+                constexpr int i = decltype(I)::value;
+                results_here(d[i & 1]);
+                const uint32_t v = sx[i & 1];
+                const float x = __uint_as_float(a.qs_byte ? (v ? v << 23 : 0x00400000u) : v);
+                const float f0 = x * w0, f1 = x * w1;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[i & 1][j][r], j < NH ? f0 : f1, acc[i][j][r]);
+                results_here(acc[i]);
+            };
+            static_assert(!(FP8 && ALONE) || (MT == 6 && NT == 4 && QL == 3 && PL == 4), "the schedule below");
+#pragma unroll
+            for (int j = 0; j < NT; ++j) pf[j] = int8_t_{}, d[0][j] = float4_t{0.f, 0.f, 0.f, 0.f};
+            qf[1] = int8_t_{};  // the first step adds two rows of zeros
+            int slot = 0, ahead = 2;  // Q's slots of this step and of the one after the next
+            for (int kt = 0; kt < nk; ++kt) {
+                // this step's operands have landed; every wave has read the last one's
+                wait_loads<QL + PL + 1>();
+                sync_lds();
+                const int pbase = (kt & 1) * PB;
+                qf[0] = read_q(slot, 0);
+                const int s_at = sa + slot * SB;
+                const uint32_t first = read_s(s_at, 0);
+                const CGD_LDS(float)* ws = (const CGD_LDS(float)*)(sm + S_AT + slot * SB + SROWS * 4);
+                const float nw0 = ws[0], nw1 = ws[1];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    product(Const<5>(), j);
+                    pf[j] = read_p(pbase, j);
+                }
+                add(Const<MT - 2>());
+                sx[0] = first;
+                each<QL>([&](auto I) { load_q(I, lds0 + qslot(ahead)); });
+                load_s(lds0 + S_AT + ahead * SB);
+                next_q();
+                __builtin_amdgcn_sched_barrier(0);
+                each<MT - 1>([&](auto I) {
+                    constexpr int i = decltype(I)::value;
+                    if constexpr (i == 1) sync_lds();  // every wave has P's operands
+                    qf[(i + 1) & 1] = read_q(slot, i + 1);
+                    const uint32_t ns = read_s(s_at, i + 1);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) product(I, j);
+                    if constexpr (i == 0) {  // the last row of the step before
+                        add(Const<MT - 1>());
+                        w0 = nw0;
+                        w1 = nw1;
+                    } else {
+                        add(Const<i - 1>());
+                    }
+                    sx[(i + 1) & 1] = ns;
+                    if constexpr (i > 0 && i <= PL) load_p(Const<i - 1>(), lds0 + pbase);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
+                next_p();
+                slot = slot == 2 ? 0 : slot + 1;
+                ahead = ahead == 2 ? 0 : ahead + 1;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) product(Const<MT - 1>(), j);
+            add(Const<MT - 2>());
+            settle();
+            add(Const<MT - 1>());
+        } else if constexpr (ST == 0) {
             // Few, large waves: the 64 products of half a stage (32 of k) run on
             // operands that were read from LDS during the half before, with one LDS
             // read, load or address slipped behind a product each, so that one wave
