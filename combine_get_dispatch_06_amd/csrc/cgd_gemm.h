@@ -401,13 +401,17 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // Blocks go to the 8 XCDs in turn; each XCD takes one run of consecutive
     // tiles, and within a run 4 row tiles share a column of tiles, so that the
     // tiles in flight on an XCD share operands in its L2. A block takes every
-    // gridDim / 8th tile of its XCD's run.
+    // gridDim / 8th tile of its XCD's run. Weight gradients of many groups take as
+    // long a tile as the group has rows: there the XCDs take 16 tiles in turn, which
+    // shares every group out (32 groups of uneven sizes, 16384 rows, 2048 x 4096:
+    // backward 800 us with runs, 747 so).
     constexpr int GM = 4;
     const int half_n = a.glu ? BN / 2 : BN;  // output columns of a tile
     const int ntn = (int)((a.n + half_n - 1) / half_n);
     const int ntm = QT ? (int)((a.m + BM - 1) / BM) : uniform(find_piece<false>(a.g, BM, 0).total);
     const int tiles = ntm * ntn * (QT ? a.g.groups : a.splits);
     const int run_len = (tiles + 7) / 8;
+    const bool shared_out = QT && ALONE && a.g.groups > 1 && run_len >= 128;
     struct Tile {
         int group, split;
         int64_t m0, rows;    // weight gradient: first output row; rows of the tile that exist (may exceed BM)
@@ -415,8 +419,9 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         int64_t n0, k0, klen;
     };
     auto locate = [&](int seq, Tile* t) -> bool {
-        const int id = (int)(blockIdx.x & 7) * run_len + seq;
-        if (seq >= run_len || id >= tiles) return false;
+        const int xcd = (int)(blockIdx.x & 7);
+        const int id = shared_out ? ((seq / 16 * 8 + xcd) * 16) + seq % 16 : xcd * run_len + seq;
+        if ((!shared_out && seq >= run_len) || id >= tiles) return false;
         t->split = id / (ntm * ntn);
         const int in0 = id - t->split * (ntm * ntn);
         const int sr = in0 / (GM * ntn);
