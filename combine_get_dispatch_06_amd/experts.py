@@ -108,6 +108,20 @@ def _shaped(t, name: str, dtype, shape: tuple, dev) -> torch.Tensor:
     return t
 
 
+def _result(out, dtype, shape: tuple, dev, *inputs, over=None) -> torch.Tensor:
+    """The caller's output tensor: it shares no memory with the inputs, which
+    other blocks still read while it is written, but may be `over` itself."""
+    _shaped(out, "out", dtype, shape, dev)
+    begin, end = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for t in (*inputs, over):
+        if t is None or t.numel() == 0 or (t is over and t.data_ptr() == begin and t.dtype == dtype):
+            continue
+        span = 1 + sum((n - 1) * st for n, st in zip(t.shape, t.stride()))
+        if t.data_ptr() < end and begin < t.data_ptr() + span * t.element_size():
+            raise ValueError("out shares memory with an input")
+    return out
+
+
 def _workspace(nbytes: int, dev):
     """Scratch memory for one call, from torch's allocator (a capture's own
     pool while a graph is captured): nothing of it outlives the call."""
@@ -150,9 +164,11 @@ def route(logits: torch.Tensor, num_topk: int, scoring: str = "softmax", bias: t
         _shaped(bias, "bias", torch.float32, (E,), dev)
     if num_topk_groups is None:
         num_topk_groups = num_groups
+    if not 1 <= num_topk <= E:
+        raise ValueError(f"num_topk must be in [1, {E}] (got {num_topk})")
     with _Current(dev):
-        idx = torch.empty((T, max(num_topk, 0)), dtype=torch.int64, device=dev)
-        wts = torch.empty((T, max(num_topk, 0)), dtype=torch.float32, device=dev)
+        idx = torch.empty((T, num_topk), dtype=torch.int64, device=dev)
+        wts = torch.empty((T, num_topk), dtype=torch.float32, device=dev)
         _check("cgd_route",
                lib.cgd_route(_ptr(logits), ltype, T, E, num_topk, mode, _ptr(bias), num_groups, num_topk_groups,
                              group_score_topk, int(renormalize), scale, _ptr(idx), _ptr(wts), _stream(dev)))
@@ -253,7 +269,8 @@ def linear(x, weight, bias: torch.Tensor | None = None, activation: str | None =
     holds O gate rows and then O up rows. bias bf16 [weight rows], residual
     bf16 [T, O]. out_dtype bfloat16, or float32 for bf16 x (a gate's logits).
     With return_preact -> (out, preact bf16 [T, weight rows]), which
-    linear_backward takes."""
+    linear_backward takes. out, if given, shares no memory with an input, but
+    may be residual itself."""
     lib = load()
     X = _X(x, 2)
     T, K = X.t.shape
@@ -271,7 +288,7 @@ def linear(x, weight, bias: torch.Tensor | None = None, activation: str | None =
         if out is None:
             out = torch.empty((T, O), dtype=out_dtype, device=dev)
         else:
-            _shaped(out, "out", out_dtype, (T, O), dev)
+            _result(out, out_dtype, (T, O), dev, X.t, X.scales, w, ws, bias, over=residual)
         pre = torch.empty((T, rows), dtype=torch.bfloat16, device=dev) if return_preact else None
         nbytes = lib.cgd_linear_workspace_bytes(T, K, O, act, X.kind)
         wk = _workspace(nbytes, dev)
@@ -333,7 +350,7 @@ def grouped_linear(x, weight, groups, bias: torch.Tensor | None = None, activati
         if out is None:
             out = torch.empty((*lead, O), dtype=torch.bfloat16, device=dev)
         else:
-            _shaped(out, "out", torch.bfloat16, (*lead, O), dev)
+            _result(out, torch.bfloat16, (*lead, O), dev, X.t, X.scales, w, ws, bias, off, cnt)
         pre = torch.empty((*lead, rows), dtype=torch.bfloat16, device=dev) if return_preact else None
         nbytes = lib.cgd_grouped_linear_workspace_bytes(N, G, cap, K, O, act, X.kind)
         wk = _workspace(nbytes, dev)
