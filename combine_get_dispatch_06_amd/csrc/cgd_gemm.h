@@ -245,14 +245,12 @@ __device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const b
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // d = p q over 128 of k, not accumulated. It keeps its place among the volatile
-// statements; results_here() has to stand between it and the first use of d, with
+// statements; result_here(d) has to stand between it and the first use of d, with
 // four others or settle() before that. After a use it keeps that in its place.
 __device__ __forceinline__ void product_fp8(float4_t& d, const int8_t_& p, const int8_t_& q) {
     asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, 0" : "=&v"(d) : "v"(p), "v"(q));
 }
-__device__ __forceinline__ void results_here(float4_t (&d)[4]) {
-    asm volatile("" : "+v"(d[0]), "+v"(d[1]), "+v"(d[2]), "+v"(d[3]));
-}
+__device__ __forceinline__ void result_here(float4_t& d) { asm volatile("" : "+v"(d)); }
 
 // Stores N (4 or 8) consecutive values of one output row from column c on, as
 // bf16 or fp32, in 8- or 16-byte pieces where the row allows it (`wide`).
@@ -387,9 +385,10 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     constexpr bool ALONE = ST == 0 || BM * BN > 128 * 128;
     // LDS: ST stages of both operands; or (ST = 0) two of P and three of Q, all
     // 160 KB, the epilogue's rows in two of Q's; or (FP8) two of P, three of Q and
-    // of the scales, the epilogue's rows in the second of P's.
-    constexpr int STAGED = ST == 0 ? 2 * PB + QB : ALONE ? PB : 0;
-    constexpr int LDS_BYTES = ST == 0 ? 3 * QB + 2 * PB : ALONE ? 2 * PB + 3 * (QB + SB) : ST * STAGE;
+    // of the scales, the epilogue's rows in the last of Q's and behind it.
+    constexpr int STAGED = ST == 0 ? 2 * PB + QB : ALONE ? 2 * (PB + QB) + 3 * SB : 0;
+    constexpr int LDS_BYTES = ST == 0 ? 3 * QB + 2 * PB : ALONE ? STAGED + ROWS * BN * 4 : ST * STAGE;
+    static_assert(!ALONE || (ST > 0 ? ROWS * BN * 4 >= QB : true), "the last of Q's slots");
     __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
 
     const int lane = lane_id();
@@ -667,16 +666,16 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     };
 
     // ---- loads ahead of the main loop ----------------------------------------
-    auto qslot = [&](int slot) { return 2 * PB + slot * QB; };
+    auto qslot = [&](int slot) { return 2 * PB + slot * QB + (FP8 && slot == 2 ? 3 * SB : 0); };
     // (four-wave tiles: all that does not go where the epilogue works; then the rest)
-    constexpr int S_AT = 2 * PB + 3 * QB;  // the scales' slots
+    constexpr int S_AT = 2 * PB + 2 * QB;  // the scales' slots
     auto start = [&](const Tile& t) {
         aim(t);
         if constexpr (FP8 && ALONE) {
-            each<PL>([&](auto I) { load_p(I, lds0); });
-            next_p();
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
+                each<PL>([&](auto I) { load_p(I, lds0 + s * PB); });
+                next_p();
                 each<QL>([&](auto I) { load_q(I, lds0 + qslot(s)); });
                 load_s(lds0 + S_AT + s * SB);
                 next_q();
@@ -698,10 +697,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         }
     };
     auto start_rest = [&]() {
-        if constexpr (FP8 && ALONE) {
-            each<PL>([&](auto I) { load_p(I, lds0 + PB); });
-            next_p();
-        } else if constexpr (ST == 0) {
+        if constexpr (ST == 0) {
 #pragma unroll
             for (int s = 1; s < 3; ++s) {
                 each<QL>([&](auto I) { load_q(I, lds0 + qslot(s)); });
@@ -713,17 +709,15 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // ---- main loop ----------------------------------------------------------
     auto multiply_tile = [&](const int nk) {
         if constexpr (FP8 && ALONE) {
-            // A step is 128 of k: MT rows of NT products from zero, added with their
-            // scales in the row behind (vector and matrix instructions of two waves
-            // share a SIMD). A row's operand and scale are read one row ahead. The
-            // barrier of a step stands before the last row of the step before, whose
-            // operands are in registers by then: that row, and the sums of the one
-            // before it, cover the first LDS reads.
-            // Its P operands make room one by one for the new step's. They are all in
-            // registers after the first row: a second barrier then frees P's slot, so
-            // two slots give its loads nearly two steps' time as three give Q's.
-            int8_t_ pf[NT], qf[2];
-            float4_t d[2][NT];
+            // A step is 128 of k: MT rows of NT products from zero, each added with its
+            // scales one row later, just before the same place's next product (vector
+            // and matrix instructions of two waves share a SIMD). A row's operand and
+            // scale are read one row ahead, P's operands of the next step in the course
+            // of this one, so nothing waits for LDS behind the barrier; the barrier of a
+            // step stands before the last row of the step before, whose operands are in
+            // registers by then. P has one step's time to arrive, Q two.
+            int8_t_ pf[2][NT], qf[2];
+            float4_t d[NT];
             uint32_t sx[2] = {0, 0};  // as they are in memory
             float w0 = 0.f, w1 = 0.f;
             auto whole = [&](const CGD_LDS(char)* at, int a0, int a1, int off) -> int8_t_ {
@@ -733,78 +727,93 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
             auto read_p = [&](int base, int j) {
                 return whole(sm + base, pa[0], pa[1], j / NH * (BN / 2) * RB + j % NH * 4 * RB);
             };
-            auto read_q = [&](int slot, int i) { return whole(sm + qslot(slot), qa[0], qa[1], i * 16 * RB); };
+            auto read_q = [&](int base, int i) { return whole(sm + base, qa[0], qa[1], i * 16 * RB); };
             const int sa = afresh(S_AT + (wm * TM + li) * 4);
             auto read_s = [&](int at, int i) { return *(const CGD_LDS(uint32_t)*)(sm + at + i * 64); };
-            auto product = [&](auto I, int j) {
-                constexpr int i = decltype(I)::value & 1;
-                product_fp8(d[i][j], pf[j], qf[i]);
+            const int sh = a.qs_byte ? 23 : 0;
+            const uint32_t least = a.qs_byte ? 0x00400000u : 0u;  // (UE8M0: 2^-127)
+            float f0, f1;
+            auto scale = [&](auto I) {  // both of row I's
+                const uint32_t v = sx[decltype(I)::value & 1] << sh;
+                const float x = __uint_as_float(v > least ? v : least);
+                f0 = x * w0;
+                f1 = x * w1;
             };
-            auto add = [&](auto I) {  // row I's products, times both scales; the next row's stand between
+            auto add = [&](auto I, int j) {  // row I's product j, NT - 1 others after it
                 constexpr int i = decltype(I)::value;
-                results_here(d[i & 1]);
-                const uint32_t v = sx[i & 1];
-                const float x = __uint_as_float(a.qs_byte ? (v ? v << 23 : 0x00400000u) : v);
-                const float f0 = x * w0, f1 = x * w1;
+                result_here(d[j]);
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[j][r], j < NH ? f0 : f1, acc[i][j][r]);
+                result_here(acc[i][j]);
+            };
+            auto row = [&](auto I, auto SET) {  // row I's products, the sums of the row before
+                constexpr int i = decltype(I)::value, set = decltype(SET)::value;
+                using Before = Const<i == 0 ? MT - 1 : i - 1>;
+                scale(Before());
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[i & 1][j][r], j < NH ? f0 : f1, acc[i][j][r]);
-                results_here(acc[i]);
+                for (int j = 0; j < NT; ++j) {
+                    add(Before(), j);
+                    product_fp8(d[j], pf[set][j], qf[i & 1]);
+                }
             };
             static_assert(!(FP8 && ALONE) || (MT == 6 && NT == 4 && QL == 3 && PL == 4), "the schedule below");
+            wait_loads<2 * (QL + 1) + PL>();
+            block_barrier();
 #pragma unroll
-            for (int j = 0; j < NT; ++j) pf[j] = int8_t_{}, d[0][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-            qf[1] = int8_t_{};  // the first step adds two rows of zeros
+            for (int j = 0; j < NT; ++j) {
+                pf[0][j] = read_p(0, j);
+                pf[1][j] = int8_t_{};  // the first step adds two rows of zeros
+                d[j] = float4_t{0.f, 0.f, 0.f, 0.f};
+            }
+            qf[1] = int8_t_{};
             int slot = 0, ahead = 2;  // Q's slots of this step and of the one after the next
-            for (int kt = 0; kt < nk; ++kt) {
-                // this step's operands have landed; every wave has read the last one's
-                wait_loads<QL + PL + 1>();
+            auto step = [&](auto SET) {
+                constexpr int set = decltype(SET)::value;
+                // Q and the scales of this step and P of the next have landed; every wave has
+                // read the last one's Q and this one's P
+                wait_loads<QL + 1>();
                 sync_lds();
-                const int pbase = (kt & 1) * PB;
-                qf[0] = read_q(slot, 0);
-                const int s_at = sa + slot * SB;
+                const int qbase = qslot(slot), s_at = sa + slot * SB;
+                each<PL>([&](auto I) { load_p(I, lds0 + set * PB); });
+                next_p();
+                qf[0] = read_q(qbase, 0);
                 const uint32_t first = read_s(s_at, 0);
                 const CGD_LDS(float)* ws = (const CGD_LDS(float)*)(sm + S_AT + slot * SB + SROWS * 4);
                 const float nw0 = ws[0], nw1 = ws[1];
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    product(Const<5>(), j);
-                    pf[j] = read_p(pbase, j);
-                }
-                add(Const<MT - 2>());
+                row(Const<MT - 1>(), Const<1 - set>());
                 sx[0] = first;
-                each<QL>([&](auto I) { load_q(I, lds0 + qslot(ahead)); });
-                load_s(lds0 + S_AT + ahead * SB);
-                next_q();
                 __builtin_amdgcn_sched_barrier(0);
                 each<MT - 1>([&](auto I) {
                     constexpr int i = decltype(I)::value;
-                    if constexpr (i == 1) sync_lds();  // every wave has P's operands
-                    qf[(i + 1) & 1] = read_q(slot, i + 1);
+                    qf[(i + 1) & 1] = read_q(qbase, i + 1);
                     const uint32_t ns = read_s(s_at, i + 1);
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) product(I, j);
-                    if constexpr (i == 0) {  // the last row of the step before
-                        add(Const<MT - 1>());
-                        w0 = nw0;
-                        w1 = nw1;
-                    } else {
-                        add(Const<i - 1>());
-                    }
+                    if constexpr (i < NT) pf[1 - set][i] = read_p((1 - set) * PB, i);
+                    row(I, SET);
+                    if constexpr (i == 0) w0 = nw0, w1 = nw1;
                     sx[(i + 1) & 1] = ns;
-                    if constexpr (i > 0 && i <= PL) load_p(Const<i - 1>(), lds0 + pbase);
+                    if constexpr (i < QL) load_q(I, lds0 + qslot(ahead));
+                    if constexpr (i == QL) load_s(lds0 + S_AT + ahead * SB);
                     __builtin_amdgcn_sched_barrier(0);
                 });
-                next_p();
+                next_q();
                 slot = slot == 2 ? 0 : slot + 1;
                 ahead = ahead == 2 ? 0 : ahead + 1;
+            };
+            int kt = 0;
+            for (; kt + 1 < nk; kt += 2) {
+                step(Const<0>());
+                step(Const<1>());
             }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) product(Const<MT - 1>(), j);
-            add(Const<MT - 2>());
+            if (kt < nk) {
+                step(Const<0>());
+                row(Const<MT - 1>(), Const<0>());
+            } else {
+                row(Const<MT - 1>(), Const<1>());
+            }
             settle();
-            add(Const<MT - 1>());
+            scale(Const<MT - 1>());
+#pragma unroll
+            for (int j = 0; j < NT; ++j) add(Const<MT - 1>(), j);
         } else if constexpr (ST == 0) {
             // Few, large waves: the 64 products of half a stage (32 of k) run on
             // operands that were read from LDS during the half before, with one LDS
