@@ -143,21 +143,23 @@ int forward(const Sizes& s, const void* x, const void* xs, int64_t st, int64_t s
 }
 
 // Workspace of a backward call: d with its row pitch (a multiple of 8
-// elements), then the partial column sums.
+// elements), then the partial column sums, then the weight gradient's pieces.
 struct GradPlan {
     bool make_d;
     int64_t ldd;
-    size_t d_bytes, partial_bytes;
-    size_t bytes() const { return d_bytes + partial_bytes; }
+    int splits;
+    size_t d_bytes, partial_bytes, piece_bytes;
+    size_t bytes() const { return d_bytes + partial_bytes + piece_bytes; }
 };
 
-GradPlan grad_plan(int64_t rows, int groups, int64_t out, int act, bool bias_grad) {
+GradPlan grad_plan(const Sizes& s, bool bias_grad) {
     GradPlan p;
-    const int64_t width = act == CGD_ACT_SWIGLU ? 2 * out : out;
-    p.make_d = act != CGD_ACT_NONE || width % 8 != 0;
-    p.ldd = (width + 7) / 8 * 8;
-    p.d_bytes = p.make_d ? ((size_t)rows * p.ldd * 2 + 255) / 256 * 256 : 0;
-    p.partial_bytes = cgd::act_grad_workspace_bytes(rows, groups, width, bias_grad);
+    p.make_d = s.act != CGD_ACT_NONE || s.width % 8 != 0;
+    p.ldd = (s.width + 7) / 8 * 8;
+    p.splits = cgd::weight_grad_splits(s.g, s.width, s.in);
+    p.d_bytes = p.make_d ? ((size_t)s.rows * p.ldd * 2 + 255) / 256 * 256 : 0;
+    p.partial_bytes = (cgd::act_grad_workspace_bytes(s.rows, s.g.groups, s.width, bias_grad) + 255) / 256 * 256;
+    p.piece_bytes = p.splits > 1 ? (size_t)p.splits * s.g.groups * s.width * s.in * 4 : 0;  // (in: a multiple of 8)
     return p;
 }
 
@@ -170,7 +172,7 @@ int backward(const Sizes& s, const void* grad_out, const void* x, const void* w,
     if (!aligned(grad_out, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(preact, 16) || !aligned(grad_x, 16) ||
         !aligned(grad_w, 16) || !aligned(grad_b, 2))
         return fail(CGD_ERR_INVALID_ARG, "grad_out, x, weight, preact, grad_x and grad_weight must be 16-byte aligned");
-    const GradPlan p = grad_plan(s.rows, s.g.groups, s.out, s.act, grad_b != nullptr);
+    const GradPlan p = grad_plan(s, grad_b != nullptr);
     if (cgd::grad_blocks(s.g, s.grouped, s.width, s.in) > cgd::kMaxGemmBlocks)
         return fail(CGD_ERR_INVALID_ARG, "these sizes need more tiles than one launch holds");
     const int rc = check_workspace(workspace, workspace_bytes, p.bytes());
@@ -205,6 +207,8 @@ int backward(const Sizes& s, const void* grad_out, const void* x, const void* w,
         a.m = s.width;
         a.n = s.in;
         a.out = grad_w;
+        a.splits = p.splits;
+        a.partial = reinterpret_cast<float*>(wsp + p.d_bytes + p.partial_bytes);
         err = cgd::launch_weight_grad(a, stream);
         if (err != hipSuccess) return hip_fail(err, "weight gradient launch");
     }
@@ -327,7 +331,7 @@ size_t cgd_linear_backward_workspace_bytes(int64_t num_tokens, int64_t in_featur
                                            int activation, int bias_grad) {
     Sizes s;
     if (check_sizes(&s, num_tokens, 1, nullptr, 0, nullptr, in_features, out_features, activation, CGD_DTYPE_BF16, false)) return 0;
-    return grad_plan(num_tokens, 1, out_features, activation, bias_grad != 0).bytes();
+    return grad_plan(s, bias_grad != 0).bytes();
 }
 
 int cgd_linear_backward(const void* grad_out, const void* x, const void* weight, int64_t num_tokens,
@@ -347,7 +351,7 @@ size_t cgd_grouped_linear_backward_workspace_bytes(int64_t num_rows, int num_gro
     if (check_sizes(&s, num_rows, num_groups, &kSomeOffset, 0, nullptr, in_features, out_features, activation,
                     CGD_DTYPE_BF16, true))
         return 0;
-    return grad_plan(num_rows, num_groups, out_features, activation, bias_grad != 0).bytes();
+    return grad_plan(s, bias_grad != 0).bytes();
 }
 
 int cgd_grouped_linear_backward(const void* grad_out, const void* x, const void* weight, int64_t num_rows,

@@ -58,11 +58,14 @@ struct GemmPlan {
 constexpr int64_t kMaxGemmBlocks = int64_t(1) << 22;  // of up to 512 threads: work-item ids stay within 32 bits
 
 GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, bool grouped);
+hipError_t launch_join(const GemmArgs& a, bool grouped, hipStream_t stream);  // of a split reduction's pieces
 hipError_t launch_forward(const GemmArgs& a, const GemmPlan& p, bool fp8, bool grouped, hipStream_t stream);
 
 // Input gradient (a.p: weights [groups][k][n], read transposed) and weight
-// gradient (both operands read transposed; out [groups][m][n]).
+// gradient (both operands read transposed; out [groups][m][n], partial
+// [splits][groups][m][n padded to 8] where a.splits > 1).
 int64_t grad_blocks(const Groups& g, bool grouped, int64_t width, int64_t k);  // of the larger of the two launches
+int weight_grad_splits(const Groups& g, int64_t width, int64_t k);  // pieces of each group's rows
 hipError_t launch_input_grad(const GemmArgs& a, bool grouped, hipStream_t stream);
 hipError_t launch_weight_grad(const GemmArgs& a, hipStream_t stream);
 

@@ -408,7 +408,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     const int half_n = a.glu ? BN / 2 : BN;  // output columns of a tile
     const int ntn = (int)((a.n + half_n - 1) / half_n);
     const int ntm = QT ? (int)((a.m + BM - 1) / BM) : uniform(find_piece<false>(a.g, BM, 0).total);
-    const int tiles = ntm * ntn * (QT ? a.g.groups : a.splits);
+    const int tiles = ntm * ntn * a.splits * (QT ? a.g.groups : 1);
     const int run_len = (tiles + 7) / 8;
     const bool shared_out = QT && ALONE && a.g.groups > 1 && run_len >= 128;
     struct Tile {
@@ -438,12 +438,13 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
             t->k0 = uniform64((int64_t)t->split * a.ksplit);
             t->klen = uniform64(a.k - t->k0 < a.ksplit ? a.k - t->k0 : a.ksplit);
         } else {  // the reduction goes over a group's rows
-            t->group = uniform(t->split);
-            t->split = 0;
+            t->group = uniform(t->split / a.splits);
+            t->split = uniform(t->split - t->group * a.splits);
             int64_t b = 0, n = a.g.total;
             if (a.g.offset || a.g.count || a.g.groups > 1) group_rows(a.g, t->group, &b, &n);
-            t->row0 = uniform64(b);
-            t->klen = uniform64(n);
+            const int64_t piece = ((n + BK - 1) / BK + a.splits - 1) / a.splits * BK, first = t->split * piece;
+            t->row0 = uniform64(b + (first < n ? first : n));
+            t->klen = uniform64(first >= n ? 0 : n - first < piece ? n - first : piece);
             t->k0 = 0;
             t->m0 = (int64_t)uniform(tm) * BM;
             t->rows = a.m - t->m0;
@@ -1061,7 +1062,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                     if (r >= t.rows) continue;
                     const int64_t row = out0 + r;
                     if (a.splits > 1) {  // partial sums, joined by join_kernel
-                        float* p = a.partial + ((int64_t)t.split * a.g.total + row) * (a.glu ? 2 * np : np);
+                        float* p = a.partial + (t.split * (QT ? a.g.groups * a.m : a.g.total) + row) * (a.glu ? 2 * np : np);
                         if (c0 < np) store_run<8>(p, c0, v0[k], 8, true, true);
                         const int64_t d1 = a.glu ? np + c0 : c1;
                         if (a.glu ? c0 < np : c1 < np) store_run<8>(p, d1, v1[k], 8, true, true);

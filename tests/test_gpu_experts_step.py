@@ -276,11 +276,13 @@ def test_fp8_exact(G, N, K, O, fmt):
     assert torch.equal(cgd.linear(_dev((x.to(q), sc)), _dev((w[0].to(q), ws[0]))), (xd @ wd[0].T).to(BF16))
 
 
-@pytest.mark.parametrize("G,N,K,W", [(17, 900, 2048, 2048), (33, 1500, 1536, 1288), (130, 3000, 520, 1280)])
-def test_weight_gradients_of_many_groups(G, N, K, W):
+@pytest.mark.parametrize("G,N,K,W", [(17, 900, 2048, 2048), (33, 1500, 1536, 1288), (130, 3000, 520, 1280), (1, 20000, 520, 72),
+                                     (3, 5000, 264, 40), (7, 9000, 136, 257), (2, 1100, 64, 8)])
+def test_weight_gradients_of_many_groups_and_of_many_rows(G, N, K, W):
+    """Tiles shared out over the XCDs; a group's rows in pieces (uneven groups: some pieces without rows)."""
     say(f"weight gradients G={G} N={N} K={K} W={W}")
     g = _gen(G)
-    off = _offsets(g, G, N, empty=(1, G - 2))
+    off = _offsets(g, G, N, empty=(1, G - 2) if G > 3 else ())
     x, w, grad = _bf(g, N, K), _bf(g, G, W, K, scale=1 / math.sqrt(K)), _bf(g, N, W)
     gx, gw, gb = cgd.grouped_linear_backward(_dev(grad), _dev(x), _dev(w), _dev(off), bias_grad=True)
     torch.cuda.synchronize()
