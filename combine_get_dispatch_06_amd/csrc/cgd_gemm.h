@@ -382,7 +382,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     constexpr int PASSES = ST == 0 ? 4 : MT > 4 ? MT : MT > 2 ? 2 : 1, IPP = MT / PASSES;
     constexpr int ROWS = WM * IPP * 16;
     // Tiles with a CU to themselves: one block for each CU takes them in turn.
-    constexpr bool ALONE = ST == 0 || BM * BN > 128 * 128;
+    constexpr bool ALONE = ST == 0 || BM * BN > 192 * 128;
     // LDS: ST stages of both operands; or (ST = 0) two of P and three of Q, all
     // 160 KB, the epilogue's rows in two of Q's; or (FP8) two of P, three of Q and
     // of the scales, the epilogue's rows in the last of Q's and behind it.

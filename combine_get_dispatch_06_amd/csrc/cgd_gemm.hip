@@ -11,16 +11,22 @@ namespace cgd {
 // products of few rows keep the tall tile: every group's weights are read anyway,
 // and a group that does not fit one tile reads them twice (16 experts, 64 rows
 // each on average, 7168 -> 2 x 2048: 176 us against 206 with 64 rows a tile).
+// Groups of 49 to 80 rows on average take 192 x 128: uneven ones have a few above
+// 128 rows, whose second tiles would run on their own at the end. Mean of five
+// draws of uneven sizes, 128 and 192 rows a tile: 16 experts as above, 64 rows
+// 198 and 195 us (the worst draw 257 and 205), 32 experts, 2048 -> 2 x 1024 88 and
+// 76; but 40 rows 171 and 178, 128 rows 89 and 95.
 // A reduction is split where even so there were fewer than 512 blocks (two for a CU).
 constexpr int kSplitBlocks = 512;
-static const int kTileRows[3] = {256, 128, 32}, kTileColumns[3] = {256, 128, 128};
+static const int kTileRows[4] = {256, 128, 32, 192}, kTileColumns[4] = {256, 128, 128, 128};
 
 GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, bool grouped) {
     GemmPlan p;
     const int64_t per = grouped ? (g.total + g.groups - 1) / g.groups : g.total;
     const int64_t wide = n * (glu ? 2 : 1);
+    const bool some_longer = grouped && g.offset && per > 48 && per <= 80;
     auto tiles = [&](int t) { return worst_pieces(g, kTileRows[t], grouped) * ((wide + kTileColumns[t] - 1) / kTileColumns[t]); };
-    p.tile = per > 128 && tiles(0) >= 200 ? 0 : grouped || per > 128 ? 1 : 2;
+    p.tile = per > 128 && tiles(0) >= 200 ? 0 : some_longer && !fp8 ? 3 : grouped || per > 128 ? 1 : 2;
     p.splits = 1;
     p.ksplit = k;
     p.partial_bytes = 0;
@@ -125,6 +131,8 @@ hipError_t launch_forward(const GemmArgs& in, const GemmPlan& p, bool fp8, bool 
         err = launch_gemm<256, 256, 2, 2, 0, 128, false, false, false>(a, grouped, stream);
     else if (p.tile == 1)
         err = launch_gemm<128, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
+    else if (p.tile == 3)
+        err = launch_gemm<192, 128, 2, 2, 2, 128, false, false, false>(a, grouped, stream);
     else
         err = launch_gemm<32, 128, 1, 4, 4, 128, false, false, false>(a, grouped, stream);
     if (err == hipSuccess && p.splits > 1) err = launch_join(a, grouped, stream);

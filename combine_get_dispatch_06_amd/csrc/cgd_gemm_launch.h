@@ -19,7 +19,7 @@ hipError_t launch_gemm(const GemmArgs& a, bool grouped, hipStream_t stream) {
     const int64_t tm = QT ? (int64_t)a.g.groups * ((a.m + BM - 1) / BM) : worst_pieces(a.g, BM, grouped);
     int64_t blocks = (tm * tn * a.splits + 7) / 8 * 8;  // 8 runs of tiles, one for each XCD
     // tiles with a CU to themselves: one block for each of the 256 CUs takes them in turn
-    if ((ST == 0 || BM * BN > 128 * 128) && blocks > 256) blocks = 256;
+    if ((ST == 0 || BM * BN > 192 * 128) && blocks > 256) blocks = 256;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((gemm_kernel<BM, BN, WM, WN, ST, RB, QT, PT, FP8>), dim3((unsigned)blocks), dim3(WM * WN * kWave), 0,
                        stream, a);
