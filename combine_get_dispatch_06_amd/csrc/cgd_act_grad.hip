@@ -6,8 +6,11 @@
 // the matrix cores take bf16 pairs (a second bf16 part would double both
 // products for 8 bits that their own bf16 result cannot show).
 // Memory-bound: one pass over grad_out and preact, 16 bytes per lane. A block
-// takes 32 rows of one group and 512 columns; column sums go up through LDS
-// in a fixed order, one fp32 row per block, which a second kernel adds in order.
+// takes 32 rows of one group and 512 columns (short enough for many blocks, long
+// enough that the sums' traffic is a 32nd of the rows'); column sums go up through
+// LDS in a fixed order, one fp32 row per block, which a second kernel adds in order.
+// SwiGLU, 4095 rows, 2048 columns, with the bias gradient: 25 us for 84 MB
+// (3.4 TB/s), 5 us for the sums.
 #include "cgd_gemm_launch.h"
 
 namespace cgd {
@@ -67,42 +70,42 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-        const int i = i0 + 4 * k;
-        if (i >= rows) break;
-        const int64_t row = pc.row0 + i;
-        float d0[8], d1[8];
-        const float(&g)[8] = gs[k];
-        const float(&z)[8] = zs[k];
-        const float(&u)[8] = us[k];
+            const int i = i0 + 4 * k;
+            if (i >= rows) break;
+            const int64_t row = pc.row0 + i;
+            float d0[8], d1[8];
+            const float(&g)[8] = gs[k];
+            const float(&z)[8] = zs[k];
+            const float(&u)[8] = us[k];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            if (glu) {
-                const float s = sigmoid_f(z[q]);
-                d0[q] = g[q] * u[q] * (s + z[q] * s * (1.0f - s));
-                d1[q] = g[q] * z[q] * s;
-            } else {
-                d0[q] = a.act ? g[q] * act_slope(z[q], a.act) : g[q];
-                d1[q] = 0.0f;
+            for (int q = 0; q < 8; ++q) {
+                if (glu) {
+                    const float s = sigmoid_f(z[q]);
+                    d0[q] = g[q] * u[q] * (s + z[q] * s * (1.0f - s));
+                    d1[q] = g[q] * z[q] * s;
+                } else {
+                    d0[q] = a.act ? g[q] * act_slope(z[q], a.act) : g[q];
+                    d1[q] = 0.0f;
+                }
+                if (q < have) {
+                    s0[q] += d0[q];
+                    s1[q] += d1[q];
+                } else {
+                    d0[q] = d1[q] = 0.0f;
+                }
             }
-            if (q < have) {
-                s0[q] += d0[q];
-                s1[q] += d1[q];
-            } else {
-                d0[q] = d1[q] = 0.0f;
+            if (a.d) {
+                uint16_t* o = a.d + row * a.ldd;
+                if (!glu) {  // the pad of a row lies behind its last column
+                    const int room = (int)(pad_end - c < 8 ? pad_end - c : 8);
+                    store_run<8>(o, c, d0, room, false, true);
+                } else {
+                    store_run<8>(o, c, d0, have, false, wide);
+                    store_run<8>(o, a.n + c, d1, have, false, wide);
+                    if (have > 0 && c + 8 >= a.n)
+                        for (int64_t p = width; p < pad_end; ++p) o[p] = 0;
+                }
             }
-        }
-        if (a.d) {
-            uint16_t* o = a.d + row * a.ldd;
-            if (!glu) {  // the pad of a row lies behind its last column
-                const int room = (int)(pad_end - c < 8 ? pad_end - c : 8);
-                store_run<8>(o, c, d0, room, false, true);
-            } else {
-                store_run<8>(o, c, d0, have, false, wide);
-                store_run<8>(o, a.n + c, d1, have, false, wide);
-                if (have > 0 && c + 8 >= a.n)
-                    for (int64_t p = width; p < pad_end; ++p) o[p] = 0;
-            }
-        }
         }
     }
     if (!a.partial) return;
@@ -123,8 +126,9 @@ __global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
 
 // grad_b[e][c]: the partial rows of e's pieces. A block takes 64 columns; its
 // four waves add every fourth piece in order, and their sums in order.
+// `pieces`: how many act_grad_kernel had room for (offsets that overlap ask for more).
 __global__ __launch_bounds__(256) void bias_join_kernel(const Groups g, const float* partial, int64_t width,
-                                                        uint16_t* out) {
+                                                        int pieces, uint16_t* out) {
     __shared__ float sums[4][kWave];
     const int e = blockIdx.y, lane = lane_id(), wave = threadIdx.x / kWave;
     int before = 0, mine = 0;  // pieces of the groups before e, pieces of e
@@ -144,6 +148,8 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const Groups g, const fl
         }
         mine = __shfl(mine, e & (kWave - 1), kWave);
     }
+    before = before < 0 || before > pieces ? pieces : before;
+    mine = mine > pieces - before ? pieces - before : mine;
     const int64_t c = (int64_t)blockIdx.x * kWave + lane;
     float s = 0.0f;
     if (c < width) {
@@ -191,7 +197,7 @@ hipError_t launch_act_grad(const void* grad_out, const void* preact, int act, in
     }
     if (bias_grad)
         hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((width + kWave - 1) / kWave), (unsigned)g.groups), dim3(256), 0,
-                           stream, g, partial, width, static_cast<uint16_t*>(bias_grad));
+                           stream, g, partial, width, (int)pieces, static_cast<uint16_t*>(bias_grad));
     return hipGetLastError();
 }
 

@@ -449,6 +449,13 @@ def test_segments_outside_the_rows_are_cut():
     torch.cuda.synchronize()
     assert (room[:100] == 5.0).all() and (room[200:] == 5.0).all()
     assert not gw[:2].any() and gw[2].any()
+    # segments that overlap: far more pieces than the rows have
+    off = torch.tensor([0, 100] * 64 + [0], dtype=torch.int32)
+    w = _bf(_gen(3), 128, 40, 64)
+    out = cgd.grouped_linear(_dev(x), _dev(w), _dev(off))
+    gx, gw, gb = cgd.grouped_linear_backward(room[100:200], _dev(x), _dev(w), _dev(off), bias_grad=True)
+    torch.cuda.synchronize()
+    assert out.shape == (100, 40) and torch.isfinite(gb.float()).all() and not gb[1].any()
 
 
 def test_refusals():
