@@ -262,11 +262,12 @@ __device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const b
 }
 // Waits until the last matrix instructions have written their results (the
 // compiler does not see them in multiply(), so it inserts no waits of its own).
+__device__ __forceinline__ void keep(float4_t& c) { asm volatile("" : "+a"(c)); }  // there until here
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 // d = p q over 128 of k, not accumulated. It keeps its place among the volatile
 // statements; result_here(d) has to stand between it and the first use of d, with
-// four others or settle() before that. After a use it keeps that in its place.
+// three others or settle() before that. After a use it keeps that in its place.
 __device__ __forceinline__ void product_fp8(float4_t& d, const int8_t_& p, const int8_t_& q) {
     asm volatile("v_mfma_f32_16x16x128_f8f6f4 %0, %1, %2, 0" : "=&v"(d) : "v"(p), "v"(q));
 }
@@ -1041,6 +1042,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
             for (int i = 0; i < IPP; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
+                    if (ST == 0) keep(acc[i0 + i][j]);
                     const int r = (wm * IPP + i) * 16 + li, u = (j / NH * (BN / 2) + column(j, lg)) / 4;
                     *(CGD_LDS(float4_t)*)(st + r * BN + (u ^ key(r)) * 4) = acc[i0 + i][j];
                 }
@@ -1151,6 +1153,64 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         });
     };
 
+    // Four-wave tiles inside the output whose sums are stored as they are, or with a
+    // residual, need no LDS: a lane has 16 neighbouring columns of a row in either
+    // half, or (P transposed) pieces of 4 that the four lanes of a row exchange.
+    auto finish_plain = [&](const Tile& t) {
+        const int lane = afresh(threadIdx.x) & (kWave - 1), li = lane & 15, lg = lane >> 4;
+        const int64_t out0 = (QT ? (int64_t)t.group * a.m + t.m0 : t.row0) + wm * TM + li;
+        const int64_t c0 = t.n0 + wn * (TN / 2) + lg * 16;
+        const int64_t left = t.rows - wm * TM - li;  // of the lane's rows
+        each<MT>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const int64_t at = (out0 + i * 16) * a.n + c0;
+            uint4 w[2][2] = {};
+            if (!PT && a.residual && i * 16 < left) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        w[h][q] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + at + h * (BN / 2) + q * 8);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (ST == 0) keep(acc[i][h * NH + j]);
+                    float4_t x = acc[i][h * NH + j];
+                    if (!PT) {
+                        const uint32_t lo = j & 1 ? w[h][j / 2].z : w[h][j / 2].x, hi = j & 1 ? w[h][j / 2].w : w[h][j / 2].y;
+                        if (a.residual) x += float4_t{bf16_lo(lo), bf16_hi(lo), bf16_lo(hi), bf16_hi(hi)};
+                    }
+                    v[2 * j] = pack_bf16x2(x[0], x[1]);
+                    v[2 * j + 1] = pack_bf16x2(x[2], x[3]);
+                }
+                if (PT) {  // piece j of lane row g <-> piece g of lane row j
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const auto p = __builtin_amdgcn_permlane32_swap(v[q], v[q + 4], false, false);
+                        v[q] = p[0];
+                        v[q + 4] = p[1];
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const auto p = __builtin_amdgcn_permlane16_swap(v[e + q], v[e + q + 2], false, false);
+                            v[e + q] = p[0];
+                            v[e + q + 2] = p[1];
+                        }
+                }
+                if (i * 16 < left) {
+                    uint16_t* o = static_cast<uint16_t*>(a.out) + at + h * (BN / 2);
+                    *reinterpret_cast<uint4*>(o) = uint4{v[0], v[1], v[2], v[3]};
+                    *reinterpret_cast<uint4*>(o + 8) = uint4{v[4], v[5], v[6], v[7]};
+                }
+            }
+        });
+    };
+
     // ---- the block's tiles ----------------------------------------------------
     start(cur);
     start_rest();
@@ -1162,7 +1222,14 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         multiply_tile(uniform((int)((cur.klen + BK - 1) / BK)));
         block_sync();  // every wave is done with LDS, and no load is on its way there
         if (more) start(next);
-        finish(cur);
+        if constexpr (ST == 0) {
+            if (a.splits == 1 && !a.act && !a.glu && !a.preact && !a.out_f32 && wide_n && cur.n0 + BN <= a.n)
+                finish_plain(cur);
+            else
+                finish(cur);
+        } else {
+            finish(cur);
+        }
         if (!more) return;
         sync_lds();
         start_rest();
