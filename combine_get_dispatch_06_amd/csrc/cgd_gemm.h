@@ -1153,30 +1153,32 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         });
     };
 
-    // Four-wave tiles inside the output whose sums are stored as they are, or with a
-    // residual, need no LDS: a lane has 16 neighbouring columns of a row in either
-    // half, or (P transposed) pieces of 4 that the four lanes of a row exchange.
+    // Tiles with a CU to themselves, inside the output, whose sums are stored as they
+    // are or with a residual, need no LDS: a lane has RUN (8 or 16) neighbouring
+    // columns of a row in either half, or (P transposed) four pieces of 4 that the
+    // four lanes of a row exchange.
     auto finish_plain = [&](const Tile& t) {
+        static_assert(!ALONE || (RUN == 16 || (RUN == 8 && !PT)), "runs of whole stores");
         const int lane = afresh(threadIdx.x) & (kWave - 1), li = lane & 15, lg = lane >> 4;
         const int64_t out0 = (QT ? (int64_t)t.group * a.m + t.m0 : t.row0) + wm * TM + li;
-        const int64_t c0 = t.n0 + wn * (TN / 2) + lg * 16;
+        const int64_t c0 = t.n0 + wn * (TN / 2) + lg * RUN;
         const int64_t left = t.rows - wm * TM - li;  // of the lane's rows
         each<MT>([&](auto I) {
             constexpr int i = decltype(I)::value;
             const int64_t at = (out0 + i * 16) * a.n + c0;
-            uint4 w[2][2] = {};
+            uint4 w[2][NH / 2] = {};
             if (!PT && a.residual && i * 16 < left) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < NH / 2; ++q)
                         w[h][q] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) + at + h * (BN / 2) + q * 8);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t v[8];
+                uint32_t v[2 * NH];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < NH; ++j) {
                     if (ST == 0) keep(acc[i][h * NH + j]);
                     float4_t x = acc[i][h * NH + j];
                     if (!PT) {
@@ -1186,7 +1188,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                     v[2 * j] = pack_bf16x2(x[0], x[1]);
                     v[2 * j + 1] = pack_bf16x2(x[2], x[3]);
                 }
-                if (PT) {  // piece j of lane row g <-> piece g of lane row j
+                if constexpr (PT) {  // piece j of lane row g <-> piece g of lane row j
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         const auto p = __builtin_amdgcn_permlane32_swap(v[q], v[q + 4], false, false);
@@ -1204,8 +1206,9 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                 }
                 if (i * 16 < left) {
                     uint16_t* o = static_cast<uint16_t*>(a.out) + at + h * (BN / 2);
-                    *reinterpret_cast<uint4*>(o) = uint4{v[0], v[1], v[2], v[3]};
-                    *reinterpret_cast<uint4*>(o + 8) = uint4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+                    for (int q = 0; q < NH / 2; ++q)
+                        *reinterpret_cast<uint4*>(o + q * 8) = uint4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
                 }
             }
         });
@@ -1222,7 +1225,7 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
         multiply_tile(uniform((int)((cur.klen + BK - 1) / BK)));
         block_sync();  // every wave is done with LDS, and no load is on its way there
         if (more) start(next);
-        if constexpr (ST == 0) {
+        if constexpr (ALONE) {
             if (a.splits == 1 && !a.act && !a.glu && !a.preact && !a.out_f32 && wide_n && cur.n0 + BN <= a.n)
                 finish_plain(cur);
             else

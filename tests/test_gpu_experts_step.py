@@ -249,6 +249,24 @@ def test_fp8_tall_tiles_over_many_steps(K, act, bias, fmt):
     _near(dense, y.cpu(), t.cpu(), BF16, "dense")
 
 
+@pytest.mark.parametrize("T,K,O", [(2100, 384, 6144), (2049, 256, 6152), (2303, 128, 6140)])
+def test_tall_tiles_with_a_residual(T, K, O):
+    """Whole tiles, tiles that stick out below and to the right, rows that are no whole number of stores."""
+    say(f"tall tiles with a residual T={T} K={K} O={O}")
+    g = _gen(T)
+    res = _bf(g, T, O)
+    (xq, xd), (wq, wd) = _fp8_x(g, T, K), _fp8_w(g, (), O, K)
+    room = torch.full((T + 8, O), 7.0, dtype=BF16, device=DEV)
+    cgd.linear(_dev(xq), _dev(wq), residual=_dev(res), out=room[:T])
+    y, _, t, _ = _ref(xd.to(DEV), wd.to(DEV), None, None, O, res.to(DEV), steps=FP8(K))
+    _near(room[:T], y.cpu(), t.cpu(), BF16, "fp8")
+    x, w = _bf(g, T, K), _bf(g, O, K, scale=1 / math.sqrt(K))
+    out = cgd.linear(_dev(x), _dev(w), residual=_dev(res))
+    y, _, t, _ = _ref(x.to(DEV), w.to(DEV), None, None, O, res.to(DEV))
+    _near(out, y.cpu(), t.cpu(), BF16, "bf16")
+    assert (room[T:] == 7.0).all()
+
+
 @pytest.mark.parametrize("G,N,K,O", [(1, 1, 128, 16), (1, 40, 640, 300), (1, 500, 1152, 129), (3, 70, 256, 260),
                                      (16, 900, 2048, 256), (5, 2100, 128, 5900), (5, 2100, 1664, 5900),
                                      (4, 3100, 512, 3333)])
