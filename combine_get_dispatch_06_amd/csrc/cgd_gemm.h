@@ -256,7 +256,8 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 // c += p q^T (16 x 16, 32 of k) with c in accumulation registers. The compiler,
 // given the choice, keeps part of 256 sums in the others and moves them over
 // and back in every step; written out, they stay. Results may be read after
-// settle().
+// settle(): that the compiler puts nothing of its own in between is checked on
+// the generated code (tests/test_products_code.py).
 __device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const bf16x8_t& q) {
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
 }
@@ -829,10 +830,11 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
             if (kt < nk) {
                 step(Const<0>());
                 row(Const<MT - 1>(), Const<0>());
+                settle();  // in both branches: what they give is moved together behind them
             } else {
                 row(Const<MT - 1>(), Const<1>());
+                settle();
             }
-            settle();
             scale(Const<MT - 1>());
 #pragma unroll
             for (int j = 0; j < NT; ++j) add(Const<MT - 1>(), j);
