@@ -24,7 +24,7 @@ def _wait_states(line: str) -> int:
 
 def _listing(src: str, out: str) -> str:
     flags = [f for f in build.HIPCC_FLAGS if f not in ("-shared", "-fPIC")]
-    r = subprocess.run(["hipcc", *flags, f"-I{build.INCLUDE}", f"-I{build.CSRC}", "--cuda-device-only", "-S", src, "-o", out],
+    r = subprocess.run([os.environ.get("HIPCC", "/opt/rocm/bin/hipcc"), *flags, f"-I{build.INCLUDE}", f"-I{build.CSRC}", "--cuda-device-only", "-S", src, "-o", out],
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0, r.stderr
     return open(out).read()
