@@ -1158,7 +1158,8 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // Tiles with a CU to themselves, inside the output, whose sums are stored as they
     // are or with a residual, need no LDS: a lane has RUN (8 or 16) neighbouring
     // columns of a row in either half, or (P transposed) four pieces of 4 that the
-    // four lanes of a row exchange.
+    // four lanes of a row exchange. Through LDS the same took 4 us a tile longer, with
+    // nothing to cover it: 4096 x 2048 -> 7168 with a residual 137 us against 125.
     auto finish_plain = [&](const Tile& t) {
         static_assert(!ALONE || (RUN == 16 || (RUN == 8 && !PT)), "runs of whole stores");
         const int lane = afresh(threadIdx.x) & (kWave - 1), li = lane & 15, lg = lane >> 4;
