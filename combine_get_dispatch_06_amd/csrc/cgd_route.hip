@@ -28,6 +28,7 @@ namespace cgd {
 
 constexpr int kRouteWaves = 4;
 constexpr int kRouteMaxGroups = 64;
+constexpr float kZeroScore = 745.0f;  // exp of less than its negative is zero in 64 bits
 
 // fp32 -> unsigned with the same order; kNone is -inf, and there is nothing below it
 constexpr uint32_t kNone = 0x007FFFFFu;
@@ -339,14 +340,24 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_kernel(const RouteAr
     // weights of the chosen
     const bool chosen = id >= 0 && place < a.K;
     float s = 0.0f;
+    // Renormalised softmax needs no denominator: it cancels. Its exponentials are relative
+    // to the largest chosen logit, which a bias or groups can leave far below the token's
+    // largest (without them that one is chosen): relative to that one they would lose their
+    // bits from 87 below on and be zero at 104. A token whose chosen scores are all zero in
+    // 64 bits, too, has no shares.
+    const bool shares = a.renormalize && !a.sigmoid;
+    const float ref = WIDE && shares ? wave_max(chosen ? x : -INFINITY) : top;
     if (chosen) {
-        // renormalised softmax needs no denominator: it cancels
-        s = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : a.renormalize ? expf(x - top) : expf(x - top) / (float)norm;
+        s = a.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - ref);
+        if (shares)
+            s = top - ref > kZeroScore ? 0.0f : s;
+        else if (!a.sigmoid)
+            s /= (float)norm;
     }
     if (a.renormalize) {
         if (a.sigmoid && wave_max(s) < 1e-30f) {  // scores this small: all of them scaled up by the same factor
             const float best = wave_max(chosen ? x : -INFINITY);
-            s = chosen && best > -745.0f ? expf(x - best) : 0.0f;  // below that they are zero in 64 bits too
+            s = chosen && best > -kZeroScore ? expf(x - best) : 0.0f;
         }
         const float total = wave_sum(s);
         s = total > 0.0f ? s / total : 0.0f;
@@ -415,7 +426,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(const Ro
         ref = wave_max(x);
         by_exp = by_exp || ref < -60.0f;
     }
-    const bool none = ref == -INFINITY || (a.sigmoid && ref < -745.0f);  // zero in 64 bits too
+    // scores that are zero in 64 bits, too, have no gradient (as in the forward direction)
+    const bool none = ref == -INFINITY || (a.sigmoid ? ref < -kZeroScore : top - ref > kZeroScore);
     if (!none && id >= 0) ps = by_exp ? expf(x - ref) : 1.0f / (1.0f + expf(-x));
     float sum = 0.0f;
 #pragma unroll
