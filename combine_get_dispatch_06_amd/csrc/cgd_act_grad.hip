@@ -24,7 +24,7 @@ __device__ __forceinline__ float act_slope(float v, int act) {
         return s + v * s * (1.0f - s);
     }
     if (act == kActGelu)
-        return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) + v * 0.39894228040143268f * __expf(-0.5f * v * v);
+        return normal_cdf(v) + v * 0.39894228040143268f * __expf(-0.5f * v * v);
     return 1.0f;
 }
 

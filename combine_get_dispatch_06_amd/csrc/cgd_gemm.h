@@ -243,7 +243,9 @@ __device__ __forceinline__ void each(F&& f) {
 // ---- activations, in fp32 -------------------------------------------------
 __device__ __forceinline__ float sigmoid_f(float v) { return 1.0f / (1.0f + __expf(-v)); }
 __device__ __forceinline__ float silu_f(float v) { return v * sigmoid_f(v); }
-__device__ __forceinline__ float gelu_f(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
+// the normal distribution, by erfc: 1 + erf cancels for negative v (4 % off at -5)
+__device__ __forceinline__ float normal_cdf(float v) { return 0.5f * erfcf(v * -0.70710678118654752f); }
+__device__ __forceinline__ float gelu_f(float v) { return v * normal_cdf(v); }
 __device__ __forceinline__ float act_f(float v, int act) {
     if (act == kActRelu) return v < 0.0f ? 0.0f : v;  // NaN passes through
     if (act == kActSilu) return silu_f(v);
