@@ -257,9 +257,11 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) { return __uint_as_f
 
 // c += p q^T (16 x 16, 32 of k) with c in accumulation registers. The compiler,
 // given the choice, keeps part of 256 sums in the others and moves them over
-// and back in every step; written out, they stay. Results may be read after
-// settle(): that the compiler puts nothing of its own in between is checked on
-// the generated code (tests/test_products_code.py).
+// and back in every step; written out, and held where they are ahead of the main
+// loop (keep()), they stay. Results may be read after settle(), and no vector
+// instruction may write an operand or a sum within two wait states ahead: the
+// compiler does not see a matrix instruction here, so both are checked on the
+// generated code (tests/test_products_code.py, tests/test_products_operands.py).
 __device__ __forceinline__ void multiply(float4_t& c, const bf16x8_t& p, const bf16x8_t& q) {
     asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(p), "v"(q));
 }
@@ -865,6 +867,10 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
                 else
                     qf[set][n - NT] = q_frag(qbase, ks, n - NT);
             };
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) keep(acc[i][j]);  // where they stay (see multiply())
             wait_loads<PL + 2 * QL>();
             block_barrier();
             each<MT + NT>([&](auto N) { fetch(N, Const<0>(), 0, qslot(0), 0); });
