@@ -216,15 +216,23 @@ class _X:
             H = q.shape[-1]
             if H % 128 or sc.shape != (*q.shape[:-1], H // 128) or sc.device != q.device:
                 raise ValueError("x scales must be [..., in_features / 128] on the codes' device")
-            if ndim == 3 and sc.shape[0] > 1 and sc.stride(0) != sc.shape[1] * sc.stride(1) and sc.numel():
-                raise ValueError("x scales must have one row stride over all experts' buffers")
             self.fmt = SCALE_UE8M0 if sc.dtype == torch.uint8 else SCALE_F32
-            self.st, self.sb = sc.stride(-2), sc.stride(-1)
+            self.st, self.sb = self._strides(sc)
             self.kind, self.t, self.scales = _FP8, q, sc
         else:
             _dev_tensor(x, "x", torch.bfloat16, ndim)
             self.kind, self.t, self.scales = _BF16, x, None
             self.fmt, self.st, self.sb = SCALE_F32, 0, 0
+
+    @staticmethod
+    def _strides(sc) -> tuple:
+        """Row and block stride; a dimension of size 1 has none of its own (whatever torch says)."""
+        rows = [(n, st) for n, st in zip(sc.shape[:-1], sc.stride()) if n > 1]
+        if not rows or not sc.numel():
+            return 0, sc.stride(-1)
+        if len(rows) == 2 and rows[0][1] != rows[1][0] * rows[1][1]:
+            raise ValueError("x scales must have one row stride over all experts' buffers")
+        return rows[-1][1], sc.stride(-1)
 
 
 def _weight(weight, kind: int, lead: tuple, dev, K: int):

@@ -1,0 +1,50 @@
+"""Calls at the edges of what the computing operators document: scales whose
+strides say nothing, more tokens than one launch holds."""
+import pytest
+import torch
+
+import combine_get_dispatch_06_amd as cgd
+from gpu_util import DEV, say
+from test_gpu_products import BF16, _dev, _fp8_w, _fp8_x, _gen
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("fmt", [cgd.SCALE_F32, cgd.SCALE_UE8M0])
+def test_scales_of_one_row(fmt):
+    """The stride of a dimension of size 1 is never stepped over, so it may be anything."""
+    K, O = 384, 40
+    (q, sc), _ = _fp8_x(_gen(1), 1, K, fmt=fmt)
+    x, w = _dev((q, sc)), _dev(_fp8_w(_gen(2), (), O, K)[0])
+    want = cgd.linear(x, w)
+    for st in (1, 1 << 30):
+        odd = torch.as_strided(x[1], (1, K // 128), (st, 1))
+        assert torch.equal(cgd.linear((x[0], odd), w), want), st
+
+
+@pytest.mark.parametrize("fmt", [cgd.SCALE_F32, cgd.SCALE_UE8M0])
+@pytest.mark.parametrize("G,cap", [(5, 1), (1, 5), (1, 1)])
+def test_scales_of_packed_buffers_of_one_row(G, cap, fmt):
+    K, O = 384, 40
+    say(f"packed scales G={G} cap={cap} fmt={fmt}")
+    (q, sc), _ = _fp8_x(_gen(3), G, cap, K, fmt=fmt)
+    x, w = _dev((q, sc)), _dev(_fp8_w(_gen(4), (G,), O, K)[0])
+    cnt = torch.full((G,), cap, dtype=torch.int32, device=DEV)
+    want = cgd.grouped_linear(x, w, cnt)
+    nb = K // 128
+    # column-major within each buffer: with one buffer or one row there is still one row stride
+    turned = x[1].transpose(1, 2).contiguous().transpose(1, 2)
+    assert torch.equal(cgd.grouped_linear((x[0], turned), w, cnt), want)
+    odd = torch.as_strided(x[1], (G, cap, nb), (nb if G > 1 else 1 << 30, nb if cap > 1 else 7, 1))
+    assert torch.equal(cgd.grouped_linear((x[0], odd), w, cnt), want)
+
+
+def test_scales_of_packed_buffers_column_major():
+    """Several rows in several buffers need one row stride."""
+    (q, sc), _ = _fp8_x(_gen(5), 3, 4, 256)
+    x, w = _dev((q, sc)), _dev(_fp8_w(_gen(6), (3,), 16, 256)[0])
+    cnt = torch.full((3,), 4, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        cgd.grouped_linear((x[0], x[1].transpose(1, 2).contiguous().transpose(1, 2)), w, cnt)
+    flat = x[1].view(12, 2).t().contiguous().t().unflatten(0, (3, 4))  # column-major over all rows
+    assert torch.equal(cgd.grouped_linear((x[0], flat), w, cnt), cgd.grouped_linear(x, w, cnt))
