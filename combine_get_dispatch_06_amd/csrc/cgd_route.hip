@@ -477,6 +477,10 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void route_grad_kernel(const Ro
 }
 
 static dim3 route_grid(int64_t T) { return dim3((unsigned)((T + kRouteWaves - 1) / kRouteWaves)); }
+// Tokens of one launch: its work-items, 64 for each token, stay below 2^32.
+constexpr int64_t kRouteTokens = int64_t(1) << 25;
+
+static const void* logits_from(const void* p, int64_t at, int bf16) { return static_cast<const char*>(p) + at * (bf16 ? 2 : 4); }
 
 template <bool WIDE, bool BF16>
 static void route_launch(const RouteArgs& a, hipStream_t stream) {
@@ -491,13 +495,21 @@ static void route_launch(const RouteArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((route_kernel<WIDE, BF16, 8>), grid, block, 0, stream, a);
 }
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
-    if (a.T == 0) return hipSuccess;
-    if (a.bias || a.groups > 1)
-        a.logits_bf16 ? route_launch<true, true>(a, stream) : route_launch<true, false>(a, stream);
-    else
-        a.logits_bf16 ? route_launch<false, true>(a, stream) : route_launch<false, false>(a, stream);
-    return hipGetLastError();
+hipError_t launch_route(const RouteArgs& all, hipStream_t stream) {
+    for (int64_t t = 0; t < all.T; t += kRouteTokens) {
+        RouteArgs a = all;
+        a.T = all.T - t < kRouteTokens ? all.T - t : kRouteTokens;
+        a.logits = logits_from(all.logits, t * a.E, a.logits_bf16);
+        a.topk_idx += t * a.K;
+        a.topk_weights += t * a.K;
+        if (a.bias || a.groups > 1)
+            a.logits_bf16 ? route_launch<true, true>(a, stream) : route_launch<true, false>(a, stream);
+        else
+            a.logits_bf16 ? route_launch<false, true>(a, stream) : route_launch<false, false>(a, stream);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 template <bool BF16>
@@ -513,10 +525,19 @@ static void route_grad_launch(const RouteGradArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((route_grad_kernel<BF16, 8>), grid, block, 0, stream, a);
 }
 
-hipError_t launch_route_grad(const RouteGradArgs& a, hipStream_t stream) {
-    if (a.T == 0) return hipSuccess;
-    a.logits_bf16 ? route_grad_launch<true>(a, stream) : route_grad_launch<false>(a, stream);
-    return hipGetLastError();
+hipError_t launch_route_grad(const RouteGradArgs& all, hipStream_t stream) {
+    for (int64_t t = 0; t < all.T; t += kRouteTokens) {
+        RouteGradArgs a = all;
+        a.T = all.T - t < kRouteTokens ? all.T - t : kRouteTokens;
+        a.logits = logits_from(all.logits, t * a.E, a.logits_bf16);
+        a.grad_logits = const_cast<void*>(logits_from(all.grad_logits, t * a.E, a.logits_bf16));
+        a.topk_idx += t * a.K;
+        a.grad_weights += t * a.K;
+        a.logits_bf16 ? route_grad_launch<true>(a, stream) : route_grad_launch<false>(a, stream);
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
+    return hipSuccess;
 }
 
 hipError_t preload_route() {

@@ -48,3 +48,33 @@ def test_scales_of_packed_buffers_column_major():
         cgd.grouped_linear((x[0], x[1].transpose(1, 2).contiguous().transpose(1, 2)), w, cnt)
     flat = x[1].view(12, 2).t().contiguous().t().unflatten(0, (3, 4))  # column-major over all rows
     assert torch.equal(cgd.grouped_linear((x[0], flat), w, cnt), cgd.grouped_linear(x, w, cnt))
+
+
+@pytest.mark.parametrize("biased", [False, True])
+def test_more_tokens_than_one_launch_holds(biased):
+    """64 work-items for each token, fewer than 2^32 in a launch."""
+    T, E, K = (1 << 26) + 5, 2, 1
+    say(f"route T={T} biased={biased}")
+    l = torch.zeros(T, E, dtype=BF16, device=DEV)
+    l[:, 0] = (torch.arange(T, device=DEV) % 3 - 1).to(BF16)  # -1, 0 (a tie), 1 against 0
+    l[T - 2] = -float("inf")
+    bias = torch.zeros(E, device=DEV) if biased else None
+    idx, w = cgd.route(l, K, bias=bias, renormalize=False, scale=2.0)
+    torch.cuda.synchronize()
+    first = l[:, 0]
+    want = (first < 0).long()
+    want[T - 2] = -1
+    assert torch.equal(idx[:, 0], want)
+    best = 2.0 * torch.sigmoid(first.abs().double())
+    best[T - 2] = 0.0
+    assert ((w[:, 0].double() - best).abs() <= 2.0 ** -20 * best).all()
+    del want, w
+    if not biased:
+        g = cgd.route_backward(torch.ones(T, K, device=DEV), l, idx, renormalize=False)
+        torch.cuda.synchronize()
+        p = torch.sigmoid(first.double())
+        d = p * (1 - p)  # towards the chosen expert
+        d = torch.where(idx[:, 0] == 0, d, -d)
+        d[T - 2] = 0.0
+        for c, want in ((0, d), (1, -d)):
+            assert ((g[:, c].double() - want).abs() <= (2.0 ** -19 + 2.0 ** -8) * want.abs()).all(), c
