@@ -38,7 +38,7 @@ struct ActGradArgs {
     float* partial;  // [piece][width] or null
 };
 
-__global__ __launch_bounds__(256) void act_grad_kernel(const ActGradArgs a) {
+__global__ __launch_bounds__(kActGradThreads) void act_grad_kernel(const ActGradArgs a) {
     __shared__ float sums[2][4][512];
     const Piece pc = find_piece<true>(a.g, kActRows, (int)blockIdx.x);
     if (pc.group < 0) return;
@@ -171,6 +171,8 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const Groups g, const fl
             (uint16_t)pack_bf16x2(((sums[0][lane] + sums[1][lane]) + sums[2][lane]) + sums[3][lane], 0.0f);
 }
 
+int64_t act_grad_blocks(const Groups& g, bool grouped) { return worst_pieces(g, kActRows, grouped); }
+
 size_t act_grad_workspace_bytes(int64_t total, int groups, int64_t width, bool bias_grad) {
     if (!bias_grad) return 0;
     const int64_t pieces = total / kActRows + (groups < total ? groups : total) + 1;
@@ -189,9 +191,9 @@ hipError_t launch_act_grad(const void* grad_out, const void* preact, int act, in
     a.d = static_cast<uint16_t*>(d);
     a.partial = bias_grad ? partial : nullptr;
     const int64_t width = act == kActSwiglu ? 2 * n : n;
-    const int64_t pieces = worst_pieces(g, kActRows, grouped);
+    const int64_t pieces = act_grad_blocks(g, grouped);
     if (pieces > 0) {
-        hipLaunchKernelGGL(act_grad_kernel, dim3((unsigned)pieces, (unsigned)((n + 511) / 512)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(act_grad_kernel, dim3((unsigned)pieces, (unsigned)((n + 511) / 512)), dim3(kActGradThreads), 0, stream, a);
         hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }

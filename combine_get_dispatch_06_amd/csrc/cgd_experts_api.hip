@@ -173,7 +173,9 @@ int backward(const Sizes& s, const void* grad_out, const void* x, const void* w,
         !aligned(grad_w, 16) || !aligned(grad_b, 2))
         return fail(CGD_ERR_INVALID_ARG, "grad_out, x, weight, preact, grad_x and grad_weight must be 16-byte aligned");
     const GradPlan p = grad_plan(s, grad_b != nullptr);
-    if (cgd::grad_blocks(s.g, s.grouped, s.width, s.in) > cgd::kMaxGemmBlocks)
+    // a launch has fewer than 2^32 work-items along a dimension
+    const bool too_many = (p.make_d || grad_b) && cgd::act_grad_blocks(s.g, s.grouped) > UINT32_MAX / cgd::kActGradThreads;
+    if (too_many || cgd::grad_blocks(s.g, s.grouped, s.width, s.in) > cgd::kMaxGemmBlocks)
         return fail(CGD_ERR_INVALID_ARG, "these sizes need more tiles than one launch holds");
     const int rc = check_workspace(workspace, workspace_bytes, p.bytes());
     if (rc) return rc;

@@ -71,6 +71,8 @@ hipError_t launch_weight_grad(const GemmArgs& a, hipStream_t stream);
 
 // d = grad_out * act'(preact), bf16 [total, ldd elements per row], and the
 // sums of d over each group's rows (bf16 [groups, width]); either may be null.
+int64_t act_grad_blocks(const Groups& g, bool grouped);  // launched at most along the rows, kActGradThreads each
+constexpr int kActGradThreads = 256;
 size_t act_grad_workspace_bytes(int64_t total, int groups, int64_t width, bool bias_grad);
 hipError_t launch_act_grad(const void* grad_out, const void* preact, int act, int64_t n, const Groups& g, bool grouped,
                            void* d, int64_t ldd, void* bias_grad, float* partial, hipStream_t stream);

@@ -101,7 +101,8 @@ int cgd_grouped_linear(const void* x, int x_type, const void* x_scales, int64_t 
  *   grad_x = d W, grad_weight = d^T x, grad_bias = sum of d's rows (from fp32).
  * grad_x, grad_weight and grad_bias may each be NULL (not wanted). preact is needed with an
  * activation. The residual's gradient is grad_out. A group without rows gets zero gradients; rows
- * of grad_x that hold no data are left as they were. */
+ * of grad_x that hold no data are left as they were. With an activation, grad_bias or
+ * weight rows that are no multiple of 8, up to about 2^29 rows; what no launch holds is refused. */
 size_t cgd_linear_backward_workspace_bytes(int64_t num_tokens, int64_t in_features, int64_t out_features,
                                            int activation, int bias_grad);
 int cgd_linear_backward(const void* grad_out, const void* x, const void* weight, int64_t num_tokens,
