@@ -11,22 +11,32 @@ namespace cgd {
 // products of few rows keep the tall tile: every group's weights are read anyway,
 // and a group that does not fit one tile reads them twice (16 experts, 64 rows
 // each on average, 7168 -> 2 x 2048: 176 us against 206 with 64 rows a tile).
-// Groups of 49 to 80 rows on average take 192 x 128: uneven ones have a few above
-// 128 rows, whose second tiles would run on their own at the end. Mean of five
-// draws of uneven sizes, 128 and 192 rows a tile: 16 experts as above, 64 rows
-// 198 and 195 us (the worst draw 257 and 205), 32 experts, 2048 -> 2 x 1024 88 and
-// 76; but 40 rows 171 and 178, 128 rows 89 and 95.
+// Where one tile for each group just fills the blocks that run at once (two for a CU:
+// room for fewer than an eighth as many second tiles), the first groups above 128 rows
+// start another round: groups that may be uneven take 192 x 128 there. us with 128 and
+// 192 rows a tile, mean of five draws; the groups' shares are spread by e^0.5, e^0.2:
+//     rows a group              56               64               80               112
+//     16 x 7168 -> 2 x 2048     175 181 165 172  214 189 168 176  271 199 175 184  291 259 291 201
+//     32 x 2048 -> 2 x 1024      84  78  73  75   88  79  73  76   97  90  74  77   94 103  98  77
+//     15 x 7168 -> 2 x 2048     170 176 158 166  190 184 162 171  248 194 171 179  282 257 281 196
+//   more room, 128 rows:
+//     14 x 7168 -> 2 x 2048     163 171 152 161  164 178 157 166  169 188 166 174  273 196 253 191
+//     24 x 4096 -> 2 x 2048     196 203 192 201  195 204 195 204  196 205 200 207  237 215 203 204
+//     8 x 4096 -> 4096           82  97  80  93   84  98  81  96   91  99  83  99
+// (128 rows a group: the first two lines 295 301 300 205 and 95 103 96 82.) Packed
+// buffers say how long a group can be; FP8 has no tile of this shape.
 // A reduction is split where even so there were fewer than 512 blocks (two for a CU).
-constexpr int kSplitBlocks = 512;
+constexpr int kRoundBlocks = 512;
 static const int kTileRows[4] = {256, 128, 32, 192}, kTileColumns[4] = {256, 128, 128, 128};
 
 GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, bool grouped) {
     GemmPlan p;
     const int64_t per = grouped ? (g.total + g.groups - 1) / g.groups : g.total;
     const int64_t wide = n * (glu ? 2 : 1);
-    const bool some_longer = grouped && g.offset && per > 48 && per <= 80;
+    const int64_t one_each = g.groups * ((wide + 127) / 128), room = (kRoundBlocks - one_each % kRoundBlocks) % kRoundBlocks;
+    const bool some_longer = grouped && g.offset && !fp8 && per > 56 && g.total > 128 && room * 8 < one_each;
     auto tiles = [&](int t) { return worst_pieces(g, kTileRows[t], grouped) * ((wide + kTileColumns[t] - 1) / kTileColumns[t]); };
-    p.tile = per > 128 && tiles(0) >= 200 ? 0 : some_longer && !fp8 ? 3 : grouped || per > 128 ? 1 : 2;
+    p.tile = per > 128 && tiles(0) >= 200 ? 0 : some_longer ? 3 : grouped || per > 128 ? 1 : 2;
     p.splits = 1;
     p.ksplit = k;
     p.partial_bytes = 0;
@@ -34,7 +44,7 @@ GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, 
     if (p.tile > 0) {
         const int bk = fp8 ? 128 : 64;
         const int64_t steps = (k + bk - 1) / bk;
-        int64_t s = t > 0 ? kSplitBlocks / t : 1;
+        int64_t s = t > 0 ? kRoundBlocks / t : 1;
         if (s > steps / 4) s = steps / 4;
         if (s > 32) s = 32;
         if (s > 1) {
