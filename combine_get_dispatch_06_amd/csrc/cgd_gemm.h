@@ -426,17 +426,24 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     // Blocks go to the 8 XCDs in turn; each XCD takes one run of consecutive
     // tiles, and within a run 4 row tiles share a column of tiles, so that the
     // tiles in flight on an XCD share operands in its L2. A block takes every
-    // gridDim / 8th tile of its XCD's run. Weight gradients of many groups take as
-    // long a tile as the group has rows: there the XCDs take 16 tiles in turn, which
-    // shares every group out (32 groups of uneven sizes, 16384 rows, 2048 x 4096:
-    // backward 800 us with runs, 747 so).
+    // gridDim / 8th tile of its XCD's run. A tile of a weight gradient takes as long as
+    // its group has rows, so an XCD's run may hold long groups alone: there the XCDs take
+    // 16 tiles in turn (4 or 64 measured up to 20 % more). That costs shared operands, so it
+    // pays with few groups, an XCD's run lying within one or two, or with long runs. Both
+    // gradients in us, in runs and in turn, groups' rows spread by e^0.1 / by e^0.6:
+    //   2 to 15 groups, runs of 64 tiles and more:   10 of 700 rows, 2048 x 2048   149 131 / 159 133
+    //     (4 of 1500, 2048 x 4096  234 201 / 237 209;   15 of 512, 2048 x 2048     204 207 / 213 208)
+    //     shorter runs:  4 of 1024, 2048 x 2048  113 111 / 115 113; 12 of 512, 1024 x 1280 62 79 / 66 83
+    //   16 groups and more, runs of 256 and more:    32 of 512, 2048 x 3200        540 543 / 611 539
+    //     (32 of 512, 4096 x 4096  1250 1313 / 1379 1281)
+    //     shorter runs: 16 of 512, 2048 x 2048   206 222 / 222 224; 24 of 400, the same 235 250 / 262 260
     constexpr int GM = 4;
     const int half_n = a.glu ? BN / 2 : BN;  // output columns of a tile
     const int ntn = (int)((a.n + half_n - 1) / half_n);
     const int ntm = QT ? (int)((a.m + BM - 1) / BM) : uniform(find_piece<false>(a.g, BM, 0).total);
     const int tiles = ntm * ntn * a.splits * (QT ? a.g.groups : 1);
     const int run_len = (tiles + 7) / 8;
-    const bool shared_out = QT && ALONE && a.g.groups > 1 && run_len >= 128;
+    const bool shared_out = QT && ALONE && a.g.groups > 1 && run_len >= (a.g.groups < 16 ? 64 : 256);
     struct Tile {
         int group, split;
         int64_t m0, rows;    // weight gradient: first output row; rows of the tile that exist (may exceed BM)

@@ -74,6 +74,18 @@ def test_tall_tiles_of_uneven_groups(act, O):
         _check(grad[a:z], x[a:z], w[e], None if pre is None else pre[a:z], act, O, gx[a:z], gw[e], gb[e], f"group {e}")
 
 
+# XCDs take a weight gradient's tiles in turn: few groups, many groups; and in runs
+@pytest.mark.parametrize("G,N,K,W", [(33, 600, 2048, 2048), (10, 900, 2048, 2049), (2, 300, 4096, 4104), (16, 500, 2048, 2048)])
+def test_weight_gradients_shared_out(G, N, K, W):
+    say(f"weight gradients G={G} N={N} K={K} W={W}")
+    grad, x, w, _ = _inputs(G, (N,), (G,), K, W, None)
+    off = _offsets(_gen(G), G, N, empty=(1,) if G > 2 else ())
+    gx, gw, gb = cgd.grouped_linear_backward(grad, x, w, off.to(DEV), bias_grad=True)
+    for e in range(G):
+        a, z = int(off[e]), int(off[e + 1])
+        _check(grad[a:z], x[a:z], w[e], None, None, W, gx[a:z], gw[e], gb[e], f"group {e}")
+
+
 # few rows; odd widths; tall tiles; rows in pieces, some without any
 @pytest.mark.parametrize("G,cap,K,O", [(1, 1, 64, 16), (4, 30, 128, 100), (7, 150, 136, 257), (6, 601, 3200, 1664),
                                        (2, 2100, 64, 40), (33, 70, 256, 64)])
