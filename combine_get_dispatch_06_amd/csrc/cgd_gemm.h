@@ -51,11 +51,8 @@
 namespace cgd {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 typedef short short4_t __attribute__((ext_vector_type(4)));
-typedef short short8_t __attribute__((ext_vector_type(8)));
 typedef float float4_t __attribute__((ext_vector_type(4)));
-typedef float float16_t __attribute__((ext_vector_type(16)));
 typedef int int4_t __attribute__((ext_vector_type(4)));
 typedef int int8_t_ __attribute__((ext_vector_type(8)));
 
@@ -391,7 +388,6 @@ __global__ __launch_bounds__(WM* WN* kWave, ST ? 2 : 1) void gemm_kernel(const G
     constexpr int QB = BM * RB, PB = BN * RB;
     constexpr int RPL = 1024 / RB;           // tile rows in one 1-KB load, CPR 16-byte pieces in each
     constexpr int CPR = RB / 16;
-    constexpr int KS = RB / 64;              // matrix instructions along k (bf16) in a stage
     // scales of a stage: one per row, the weights', and a place that is never read
     constexpr int SROWS = BM < 64 ? 64 : BM;
     constexpr int SB = FP8 ? SROWS * 4 + 512 : 0;

@@ -27,7 +27,6 @@
 namespace cgd {
 
 constexpr int kRouteWaves = 4;
-constexpr int kRouteMaxGroups = 64;
 constexpr float kZeroScore = 745.0f;  // exp of less than its negative is zero in 64 bits
 
 // fp32 -> unsigned with the same order; kNone is -inf, and there is nothing below it

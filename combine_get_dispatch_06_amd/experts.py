@@ -94,7 +94,7 @@ def _choice(table: dict, value, name: str) -> int:
 
 
 def _shaped(t, name: str, dtype, shape: tuple, dev) -> torch.Tensor:
-    """A contiguous tensor of this type and shape on the device, 16-byte aligned."""
+    """A contiguous tensor of this type and shape on the device (libcgd checks its alignment)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
