@@ -9,7 +9,11 @@ grouped products and the dense product with its epilogue.
 
 Each has its gradient as a call of its own (route_backward,
 grouped_linear_backward, linear_backward): like dispatch and combine they take
-and give tensors, and record nothing.
+and give tensors, and record nothing. The products' gradients take bf16, a
+gate's float32 ones rounded:
+
+    grad_logits = route_backward(grad_topk_weights, logits, topk_idx, scoring="sigmoid")
+    grad_x, grad_gate, _ = linear_backward(grad_logits.bfloat16(), x, gate)
 
 Like the rest of the package this module only marshals arguments to libcgd
 (include/cgd_experts.h): the kernels run on the caller's current stream of the
@@ -372,8 +376,9 @@ def grouped_linear(x, weight, groups, bias: torch.Tensor | None = None, activati
 def linear_backward(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
                     preact: torch.Tensor | None = None, activation: str | None = None, bias_grad: bool = False):
     """Gradients of linear (bf16): -> (grad_x [T, I], grad_weight like weight,
-    grad_bias [weight rows] or None). grad_out bf16 [T, O]; preact as linear
-    returned it, needed with an activation. The residual's gradient is grad_out."""
+    grad_bias [weight rows] or None). grad_out bf16 [T, O] (a float32 output's,
+    too: a bf16 operand of both products); preact as linear returned it, needed
+    with an activation. The residual's gradient is grad_out."""
     lib = load()
     _dev_tensor(x, "x", torch.bfloat16, 2)
     T, K = x.shape

@@ -1,11 +1,13 @@
 """Calls at the edges of what the computing operators document: scales whose
-strides say nothing, more tokens than one launch holds."""
+strides say nothing, more tokens than one launch holds, a gate's gradient."""
+import math
+
 import pytest
 import torch
 
 import combine_get_dispatch_06_amd as cgd
 from gpu_util import DEV, say
-from test_gpu_products import BF16, _dev, _fp8_w, _fp8_x, _gen
+from test_gpu_products import BF16, F32, _bf, _check_grads, _dev, _fp8_w, _fp8_x, _gen
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +80,18 @@ def test_more_tokens_than_one_launch_holds(biased):
         d[T - 2] = 0.0
         for c, want in ((0, d), (1, -d)):
             assert ((g[:, c].double() - want).abs() <= (2.0 ** -19 + 2.0 ** -8) * want.abs()).all(), c
+
+
+@pytest.mark.parametrize("T,E,K,H", [(1, 8, 2, 64), (300, 256, 8, 512)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_gradient_of_a_gate(T, E, K, H, scoring):
+    """fp32 logits, their gradient rounded to bf16 once: the operand of both products."""
+    say(f"gate gradient T={T} E={E} K={K} H={H} {scoring}")
+    g = _gen(T + E)
+    x, gate = _bf(g, T, H), _bf(g, E, H, scale=2 / math.sqrt(H))
+    logits = cgd.linear(_dev(x), _dev(gate), out_dtype=F32)
+    idx, w = cgd.route(logits, K, scoring=scoring)
+    gl = cgd.route_backward(torch.randn(T, K, generator=g).to(DEV), logits, idx, scoring=scoring)
+    assert gl.dtype == F32
+    gx, gg, _ = cgd.linear_backward(gl.bfloat16(), _dev(x), _dev(gate))
+    _check_grads(gl.cpu(), x, gate, None, None, E, gx, gg, None, True, "gate")
