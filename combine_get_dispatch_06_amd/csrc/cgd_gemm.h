@@ -21,20 +21,22 @@
 // Three main loops:
 //   256 x 256 on four waves (ST = 0): a CU to itself, 256 sums per lane in the
 //     accumulation registers, three slots of Q and two of P in LDS. Operands are
-//     read from LDS half a stage ahead. 32768 x 4096 x 7168 in 1.35 ms (1.42
-//     PFLOP/s); loads half as deep measured 1.43 ms, 32x32 matrix instructions
-//     more (twice the traffic of sums for a product). The chip's power bounds it:
-//     the clock falls to 1.7 GHz with the matrix units 65 % busy.
+//     read from LDS half a stage ahead. 32768 x 4096 x 7168 in 1.33-1.40 ms (1.37-1.45
+//     PFLOP/s); loads half as deep measured 6 % more, 32x32 matrix instructions
+//     more, too (twice the traffic of sums for a product). The chip's power bounds it:
+//     the clock falls to 1.75 GHz with the matrix units 73 % busy and waves waiting a
+//     tenth of the time. Reductions of 8 stages a tile (weight gradients of 32 groups of
+//     512 rows) keep them a third busy: a tile's start and epilogue are not covered.
 //   192 x 256 on eight waves (FP8): a CU to itself, two slots of P and three of Q.
 //     Every 128 of k the products are scaled and added by the vector unit, 96
-//     times four values a lane for 24 matrix instructions, whose time bounds it
-//     with that of the loads (a wave waits a third of the time): 6144 x 8192 x
-//     8192 in 0.38 ms (2.15 PFLOP/s).
+//     times four values a lane for 24 matrix instructions. Matrix units 60 % busy, a
+//     wave waits a third of the time: 6144 x 8192 x 8192 in 0.37 ms (2.2 PFLOP/s).
+//     (The general epilogue spills a few registers, outside the loop.)
 //   smaller tiles: two or more blocks to a CU, ST stages; those of gradients
 //     (RB = 64) read LDS a stage ahead of the matrix instructions: 32.4 us against
 //     35.3 with 128-byte stages (4096 x 1024 x 512, both gradients). Few rows are
 //     bound by the weights' latency and rate: 16 experts of 64 rows, 7168 ->
-//     2 x 2048 in 180 us (5.2 TB/s).
+//     2 x 2048 in 180 us (5.2 TB/s), by the groups' sizes up to 250.
 //
 // Bounds: every global read goes through a buffer descriptor, and each lane's
 // offset is inside its operand or kPastEnd, behind every descriptor's end, where
