@@ -28,7 +28,8 @@ accepts and returns (codes, scales) tuples, and dispatch(..., cast_fp8=fmt)
 casts on the way. Fixed-capacity packed layout (low-latency dispatch):
 low_latency_dispatch / low_latency_combine. The router and the experts'
 products around these calls (route, grouped_linear, linear and their
-gradients) are in experts.py. copy_(dst, src) is libcgd's plain
+gradients) are in experts.py; the norm, the adapters, dropout and combine's
+gradient in layer.py. copy_(dst, src) is libcgd's plain
 16-byte copy, the measured copy ceiling the bandwidths are compared with.
 
 The calls follow the DeepEP-style Buffer API described by the DeepEP Python
@@ -53,7 +54,8 @@ __all__ = ["get_dispatch_layout", "dispatch", "dispatch_plan", "dispatch_apply",
            "layout_and_normal_dispatch_plan", "layout_and_dispatch", "normal_workspace_bytes",
            "layout_and_normal_workspace_bytes", "empty_", "layout_and_dispatch_noalloc", "init",
            "layout_and_normal_dispatch", "route", "route_backward", "linear", "linear_backward", "grouped_linear",
-           "grouped_linear_backward"]
+           "grouped_linear_backward", "rms_norm", "rms_norm_backward", "adapter_linear", "adapter_linear_backward",
+           "dropout", "dropout_backward", "combine_backward"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _BUILT_LIB = os.path.join(_PKG, "libcgd.so")
@@ -90,7 +92,7 @@ def load():
             raise FileNotFoundError(f"CGD_LIBRARY names {_LIB_PATH}, which does not exist")
         from . import build as _build
         _build.build()
-    _lib = _configure_experts(configure(ctypes.CDLL(_LIB_PATH)))
+    _lib = _configure_layer(_configure_experts(configure(ctypes.CDLL(_LIB_PATH))))
     return _lib
 
 
@@ -1326,3 +1328,5 @@ def low_latency_combine(expert_out: torch.Tensor, topk_weights: torch.Tensor, ha
 # The operators that compute around these moves (they use the helpers above).
 from .experts import (configure as _configure_experts, grouped_linear, grouped_linear_backward, linear,  # noqa: E402
                       linear_backward, route, route_backward)
+from .layer import (configure as _configure_layer, adapter_linear, adapter_linear_backward, combine_backward,  # noqa: E402
+                    dropout, dropout_backward, rms_norm, rms_norm_backward)

@@ -9,6 +9,7 @@
 #include <string>
 
 #include "cgd_experts_launch.h"
+#include "cgd_layer_launch.h"
 #include "cgd_launch.h"
 
 namespace {
@@ -1050,6 +1051,10 @@ extern "C" int cgd_init(void) {
     if (err == hipSuccess) err = cgd::preload_gemm_fp8();
     if (err == hipSuccess) err = cgd::preload_gemm_grad();
     if (err == hipSuccess) err = cgd::preload_act_grad();
+    if (err == hipSuccess) err = cgd::preload_norm();
+    if (err == hipSuccess) err = cgd::preload_dropout();
+    if (err == hipSuccess) err = cgd::preload_combine_grad();
+    if (err == hipSuccess) err = cgd::preload_adapters();
     if (err != hipSuccess) return hip_fail(err, "loading the GPU code");
     return CGD_OK;
 }
