@@ -3,12 +3,14 @@
 //   gh[t] = scale[j] b[j]^T grad[t],  grad_x[t] = a[j]^T gh[t]
 //   grad_a[j] = sum over j's tokens of gh x^T,  grad_b[j] = sum of scale grad h^T
 // Tokens are put in order of their adapter first (a stable order: sums do not
-// depend on timing), those without one last; tiles of 16 tokens and up then
-// have one adapter each, and rows are gathered through that order. The products
-// are skinny, a rank is some 8 to 256: what bounds them is reading x and writing
-// out once, so operands go from memory straight into the registers of the matrix
-// instructions, 16 bytes a lane, without LDS in between, and the reduction over
-// in_features is split until the CUs are busy.
+// depend on timing), those without one last; tiles of 16 or 32 tokens then have one
+// adapter each, and rows are gathered through that order. The products are skinny, a
+// rank is some 8 to 256: what bounds them is reading x and writing out once, so the
+// reduction over in_features and the out features are split until the CUs are busy,
+// and loads and stores take 128 bytes of a row at a time.
+// 4093 tokens of 24 requests, rank 64, 7168 -> 4096 with a residual: order 5.7 us, first
+// product 21 (2.8 TB/s), second 25 (2.7 TB/s). Operands loaded the way the matrix
+// instructions want them: 37 and 40; both products in one kernel like that: 73 and more.
 // h and gh are fp32 sums; as operands of the second product they go in as two
 // bf16 parts (v = hi + lo, off by 2^-16 of v at most), which costs matrix
 // instructions that nothing waits for: results are rounded once.
@@ -20,8 +22,11 @@ namespace cgd {
 namespace {
 
 typedef uint32_t uint4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t uint2_t __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ bf16x8_t frag_at(const uint16_t* p) { return *reinterpret_cast<const bf16x8_t*>(p); }
+// LDS is written and read through one type.
+__device__ __forceinline__ void put16(void* p, const uint4& v) { *static_cast<uint4_t*>(p) = uint4_t{v.x, v.y, v.z, v.w}; }
+__device__ __forceinline__ bf16x8_t get16(const void* p) { return __builtin_bit_cast(bf16x8_t, *static_cast<const uint4_t*>(p)); }
 __device__ __forceinline__ bf16x8_t no_frag() { return __builtin_bit_cast(bf16x8_t, uint4_t{0, 0, 0, 0}); }
 __device__ __forceinline__ float4_t mul16(const bf16x8_t& rows, const bf16x8_t& columns, const float4_t& sum) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, columns, sum, 0, 0, 0);
@@ -39,17 +44,29 @@ __device__ __forceinline__ void halves2(float a, float b, uint32_t* hi, uint32_t
 
 // ---- order of the tokens ---------------------------------------------------
 
+// A tile: up to `tile` (16 or 32) tokens in order, all of one adapter (group
+// `adapters`: of none; < 0: no tile). Group g's tiles begin at slot
+// offset[g] / tile + g: as many slots lie between that and the next group's as its
+// tiles need, or one more, which says so. So a group knows its slots without the
+// others' counts. token: past the tile's rows the last of them again.
+constexpr int kTallTile = 32;
+struct Tile {
+    int group, row0, rows, pad;
+    int token[kTallTile];
+};
+
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kWave;
+constexpr int kPlanKept = 8;  // tokens of a lane whose groups stay in registers between the two passes
 
 // Block g finds the tokens of adapter g (g = adapters: those without one): how
 // many come before them, and in a second pass their places. No block waits for
 // another. Each wave has a run of tokens, so the order within a group is the
 // tokens' own.
-__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_t* __restrict__ index, int tokens, int adapters,
-                                                                    int32_t* __restrict__ offset, int32_t* __restrict__ order) {
-    __shared__ int32_t less_of[kPlanWaves], same_of[kPlanWaves];
-    const int mine = blockIdx.x, lane = lane_id(), wave = threadIdx.x / kWave;
+__device__ __forceinline__ void plan_group(const int64_t* __restrict__ index, int tokens, int adapters, int mine,
+                                           int32_t* __restrict__ offset, int32_t* __restrict__ order, Tile* __restrict__ tiles, int tile,
+                                           int32_t* less_of, int32_t* same_of) {
+    const int lane = lane_id(), wave = threadIdx.x / kWave;
     const int run = (tokens + kPlanThreads - 1) / kPlanThreads * kWave;
     const int t0 = wave * run, t1 = t0 + run < tokens ? t0 + run : tokens;
     auto group = [&](int t) {
@@ -57,7 +74,14 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_
         return j >= 0 && j < adapters ? (int)j : adapters;
     };
     int less = 0, same = 0;
-    for (int t = t0 + lane; t < t1; t += 4 * kWave) {
+    int kept[kPlanKept];
+#pragma unroll
+    for (int u = 0; u < kPlanKept; ++u) {
+        kept[u] = t0 + u * kWave + lane < t1 ? group(t0 + u * kWave + lane) : INT32_MAX;
+        less += kept[u] < mine;
+        same += kept[u] == mine;
+    }
+    for (int t = t0 + kPlanKept * kWave + lane; t < t1; t += 4 * kWave) {
         int g[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) g[u] = t + u * kWave < t1 ? group(t + u * kWave) : INT32_MAX;
@@ -77,23 +101,97 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_
         same_of[wave] = same;
     }
     __syncthreads();
-    int first = 0, at = 0;
+    int first = 0, at = 0, all = 0;
     for (int w = 0; w < kPlanWaves; ++w) {
         first += less_of[w];
+        all += same_of[w];
         at += w < wave ? same_of[w] : 0;
     }
     at += first;
+    Tile* const slots = tiles + first / tile + mine;
+    for (int i = threadIdx.x, n = (first + all) / tile + 1 - first / tile; i < n; i += kPlanThreads) {
+        const int left = all - i * tile;
+        slots[i].group = left > 0 ? mine : -1;
+        slots[i].row0 = first + i * tile;
+        slots[i].rows = left < tile ? left : tile;
+    }
     if (threadIdx.x == 0) {
         offset[mine] = first;
         if (mine == adapters) offset[mine + 1] = tokens;
     }
     if (same == 0) return;
-    for (int t = t0; t < t1; t += kWave) {
-        const bool hit = t + lane < t1 && group(t + lane) == mine;
+    auto place = [&](bool hit, int t) {
         const uint64_t hits = ballot(hit);
-        if (hit) order[at + __popcll(hits & lanemask_lt())] = t + lane;
+        if (hit) {
+            const int to = at + __popcll(hits & lanemask_lt()), i = to - first;
+            order[to] = t;
+            slots[i / tile].token[i % tile] = t;
+            if (to == first + all - 1)
+                for (int k = i % tile + 1; k < tile; ++k) slots[i / tile].token[k] = t;
+        }
         at += __popcll(hits);
+    };
+#pragma unroll
+    for (int u = 0; u < kPlanKept; ++u) place(kept[u] == mine, t0 + u * kWave + lane);
+    for (int t = t0 + kPlanKept * kWave; t < t1; t += kWave) place(t + lane < t1 && group(t + lane) == mine, t + lane);
+}
+
+// 64 x 64 of a transpose through LDS, with 256 threads; rows and columns are
+// multiples of 8.
+__device__ __forceinline__ void turn_tile(const uint16_t* from, uint16_t* to, int64_t rows, int64_t columns, int64_t r0, int64_t c0,
+                                          uint16_t (*tile)[66]) {
+    const int tid = threadIdx.x & 255;
+    for (int i = tid; i < 64 * 8; i += 256) {
+        const int r = i / 8, c = i % 8 * 8;
+        if (r0 + r >= rows || c0 + c >= columns) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(from + (r0 + r) * columns + c0 + c);
+        uint32_t* t = reinterpret_cast<uint32_t*>(&tile[r][c]);
+        t[0] = v.x, t[1] = v.y, t[2] = v.z, t[3] = v.w;
     }
+    __syncthreads();
+    for (int i = tid; i < 64 * 8; i += 256) {
+        const int c = i / 8, r = i % 8 * 8;
+        if (c0 + c >= columns || r0 + r >= rows) continue;
+        uint32_t q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = tile[r + 2 * k][c] | (uint32_t)tile[r + 2 * k + 1][c] << 16;
+        *reinterpret_cast<uint4*>(to + (c0 + c) * rows + r0 + r) = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+}
+
+struct PlanArgs {
+    const int64_t* index;
+    int tokens, adapters;
+    int32_t* offset;
+    int32_t* order;
+    Tile* tiles;
+    int tile;
+    // for gradients: transposes of the adapters, four squares of 64 x 64 a block after the groups'
+    const uint16_t* a;   // [adapters][rank][in]
+    const uint16_t* b;   // [adapters][out][rank]
+    uint16_t* turned_a;  // [adapters][in][rank]
+    uint16_t* turned_b;  // [adapters][rank][out]
+    int64_t in, out;
+    int rank;
+    int64_t a_squares, squares;  // of all adapters: a's, then b's
+};
+
+__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const PlanArgs p) {
+    __shared__ int32_t less_of[kPlanWaves], same_of[kPlanWaves];
+    __shared__ uint16_t turned[4][64][66];
+    if ((int)blockIdx.x <= p.adapters) {
+        plan_group(p.index, p.tokens, p.adapters, blockIdx.x, p.offset, p.order, p.tiles, p.tile, less_of, same_of);
+        return;
+    }
+    const int quarter = threadIdx.x / 256;
+    int64_t t = (int64_t)(blockIdx.x - p.adapters - 1) * 4 + quarter;
+    const bool is_a = t < p.a_squares, there = t < p.squares;
+    if (!is_a) t -= p.a_squares;
+    const int64_t rows = is_a ? p.rank : p.out, columns = is_a ? p.in : p.rank;
+    const int64_t across = (columns + 63) / 64, each = across * ((rows + 63) / 64);
+    const int64_t j = t / each, i = t - j * each;
+    turn_tile((is_a ? p.a : p.b) + j * rows * columns, (is_a ? p.turned_a : p.turned_b) + j * rows * columns, there ? rows : 0,
+              columns, i / across * 64, i % across * 64, turned[quarter]);
 }
 
 // ---- the first product: to the rank ------------------------------------------
@@ -101,99 +199,171 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_
 struct ShrinkArgs {
     const uint16_t* x;       // [tokens, in]
     const uint16_t* w;       // [adapters, rank, in]
-    const int32_t* offset;   // [adapters + 2]
-    const int32_t* order;
+    const int64_t* index;    // few tokens: the kernel makes the tiles itself
+    Tile* tiles;             // one for each blockIdx.x
     int64_t tokens, in, piece;  // piece: of `in` for one block, a multiple of 64
     int adapters, rank;
     float* partial;          // [pieces][token in order][rank]
 };
 
-// A block has 16 * MT tokens of one adapter and 16 * NT of the ranks over one
-// piece of the reduction; its four waves take 64 of it in turn (128 bytes of a
-// row at a time) and join their sums through LDS.
-template <int MT, int NT>
-__global__ __launch_bounds__(256) void adapter_shrink_kernel(const ShrinkArgs s) {
-    constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = BN + 4;
-    __shared__ __attribute__((aligned(16))) float sums[4][BM][PITCH];
-    const Groups groups{s.offset, nullptr, 0, s.tokens, s.adapters};
-    const Piece pc = find_piece<true>(groups, BM, (int)blockIdx.x);
-    if (pc.group < 0) return;
-    const int lane = lane_id(), wave = threadIdx.x / kWave, m = lane & 15, g = lane >> 4;
-    const int rows = pc.rows < BM ? (int)pc.rows : BM;
+// The plan of at most kFewTokens tokens, by every block for itself: a lane of its
+// first wave has a token and counts the groups before its own and the tokens before
+// it. Tiles of 16.
+// (128 tokens: the shrink kernel 14.6 us with it, 5.5 and the plan's 3.2 without.)
+constexpr int kFewTokens = 32;
+constexpr int kTile = 16;
+__device__ __forceinline__ void plan_few(const int64_t* index, int tokens, int adapters, int want, Tile& p) {
+    if (threadIdx.x < kWave) {
+        const int t = lane_id();
+        int mine = INT32_MAX;
+        if (t < tokens) {
+            const int64_t j = index[t];
+            mine = j >= 0 && j < adapters ? (int)j : adapters;
+        }
+        int less = 0, before = 0, same = 0;
+        for (int i = 0; i < tokens; ++i) {
+            const int o = __builtin_amdgcn_readlane(mine, i);
+            less += o < mine;
+            same += o == mine;
+            before += o == mine && i < t;
+        }
+        if (t == 0) p.group = -1;
+        __builtin_amdgcn_wave_barrier();
+        const bool here = t < tokens && less / kTile + mine + before / kTile == want;
+        const int i = before % kTile;
+        if (here) p.token[i] = t;
+        if (here && before == same - 1)
+            for (int k = i + 1; k < kTile; ++k) p.token[k] = t;
+        if (here && i == 0) {
+            p.group = mine;
+            p.row0 = less + before;
+            p.rows = same - before < kTile ? same - before : kTile;
+        }
+    }
+    __syncthreads();
+}
+
+// Rows on their way from memory to the matrix instructions. These want 16 rows side
+// by side in neighbouring lanes; loaded like that, every lane's 16 bytes are an
+// access of their own (some 100 cycles for a wave's load, measured). So eight lanes
+// load 128 bytes of one row, and the rows are turned over in LDS of the wave's own:
+// 16-byte piece c of row r lies at c ^ (r % 8), which spreads the 16 rows that an
+// operand takes, and the pieces of a row, over all banks.
+constexpr int kRowBytes = 128;
+__device__ __forceinline__ char* turn_place(char* room, int row, int piece) {
+    return room + row * kRowBytes + (piece ^ (row & 7)) * 16;
+}
+
+// A block has a tile of up to 16 * MT tokens and 16 * NT of the ranks over one piece
+// of the reduction; its four waves take 64 * U of it in turn, the next ones on their
+// way while these are multiplied, and join their sums through LDS.
+template <int MT, int NT, int U, bool FEW>
+__global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs s) {
+    constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = BN + 4, ROWS = BM + BN;
+    constexpr int TURN = ROWS * kRowBytes * U, SUMS = 4 * BM * PITCH * 4;
+    __shared__ __attribute__((aligned(16))) char room[4 * TURN > SUMS ? 4 * TURN : SUMS];
+    __shared__ Tile few;
+    const Tile* tile = &s.tiles[blockIdx.x];
+    if constexpr (FEW) {
+        plan_few(s.index, (int)s.tokens, s.adapters, blockIdx.x, few);
+        if (blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < sizeof(Tile) / 4)
+            reinterpret_cast<int*>(&s.tiles[blockIdx.x])[threadIdx.x] = reinterpret_cast<const int*>(&few)[threadIdx.x];
+        tile = &few;
+    }
+    const int lane = lane_id(), wave = threadIdx.x / kWave, n = lane & 15, g = lane >> 4;
+    const int group = uniform(tile->group), row0 = uniform(tile->row0), rows = uniform(tile->rows);
+    if (group < 0 || group == s.adapters) return;
     const int rank0 = blockIdx.z * BN;
     const int64_t k0 = blockIdx.y * s.piece, k1 = k0 + s.piece < s.in ? k0 + s.piece : s.in;
-    // rows past the tile's tokens, or past the rank, repeat the last: nothing of them is stored
-    const uint16_t* xp[MT];
-    const uint16_t* wp[NT];
+    // a load's eight rows: 8 q + lane / 8 of the tokens, then of the ranks (eight past
+    // the rank: the first again; nothing of them is stored)
+    const int r8 = lane >> 3, c8 = lane & 7;
+    const uint16_t* xp[2 * MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const int r = i * 16 + m < rows ? i * 16 + m : rows - 1;
-        xp[i] = s.x + s.order[pc.row0 + r] * s.in + g * 8;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int r = rank0 + j * 16 + m < s.rank ? rank0 + j * 16 + m : s.rank - 1;
-        wp[j] = s.w + ((int64_t)pc.group * s.rank + r) * s.in + g * 8;
-    }
+    for (int q = 0; q < 2 * MT; ++q) xp[q] = s.x + tile->token[q * 8 + r8] * s.in + k0 + c8 * 8;
+    const uint16_t* const wp = s.w + ((int64_t)group * s.rank + rank0 + r8) * s.in + k0 + c8 * 8;
+    const int64_t next8 = 8 * s.in;
+    char* const mine = room + wave * TURN;
     float4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = float4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = MT * NT > 4 ? 2 : 4;  // units of 64 on their way at a time
-    const int whole = (int)((k1 - k0) / 64), units = (int)((k1 - k0 + 63) / 64);
-    int u = wave;
-    for (; u + 4 * (U - 1) < whole; u += 4 * U) {
-        bf16x8_t xf[U][2][MT], wf[U][2][NT];
+    uint4 stage[U][2 * (MT + NT)];
+    const int span = (int)(k1 - k0), whole = span / (64 * U);
+    auto load = [&](int u) {
 #pragma unroll
-        for (int v = 0; v < U; ++v)
+        for (int v = 0; v < U; ++v) {
+            const int k = (u * U + v) * 64;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t k = k0 + (u + 4 * v) * 64 + h * 32;
+            for (int q = 0; q < 2 * MT; ++q) stage[v][q] = *reinterpret_cast<const uint4*>(xp[q] + k);
 #pragma unroll
-                for (int i = 0; i < MT; ++i) xf[v][h][i] = frag_at(xp[i] + k);
-#pragma unroll
-                for (int j = 0; j < NT; ++j) wf[v][h][j] = frag_at(wp[j] + k);
-            }
-#pragma unroll
-        for (int v = 0; v < U; ++v)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) acc[i][j] = mul16(wf[v][h][j], xf[v][h][i], acc[i][j]);
-    }
-    for (; u < units; u += 4) {
+            for (int q = 0; q < 2 * NT; ++q)
+                stage[v][2 * MT + q] = *reinterpret_cast<const uint4*>(wp + (rank0 + q * 8 < s.rank ? q * next8 : 0) + k);
+        }
+    };
+    auto turn = [&](int v, int q) {
+        put16(turn_place(mine + v * ROWS * kRowBytes, q * 8 + r8, c8), stage[v][q]);
+    };
+    auto multiply = [&](int v) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int64_t k = k0 + u * 64 + h * 32;
-            const bool in = k + g * 8 < k1;
             bf16x8_t xf[MT], wf[NT];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) xf[i] = in ? frag_at(xp[i] + k) : no_frag();
+            for (int i = 0; i < MT; ++i) xf[i] = get16(turn_place(mine + v * ROWS * kRowBytes, i * 16 + n, h * 4 + g));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) wf[j] = in ? frag_at(wp[j] + k) : no_frag();
+            for (int j = 0; j < NT; ++j) wf[j] = get16(turn_place(mine + v * ROWS * kRowBytes, BM + j * 16 + n, h * 4 + g));
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int j = 0; j < NT; ++j) acc[i][j] = mul16(wf[j], xf[i], acc[i][j]);
         }
+    };
+    int u = wave;
+    if (u < whole) load(u);
+    for (; u < whole; u += 4) {
+#pragma unroll
+        for (int v = 0; v < U; ++v)
+#pragma unroll
+            for (int q = 0; q < 2 * (MT + NT); ++q) turn(v, q);
+        __builtin_amdgcn_sched_barrier(0);
+        if (u + 4 < whole) load(u + 4);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int v = 0; v < U; ++v) multiply(v);
+        __builtin_amdgcn_sched_barrier(0);
     }
+    if (u == whole) {  // what is left of the piece is one wave's, with zeros behind it
+        for (int k = whole * U * 64; k < span; k += 64) {
+            const bool in = k + c8 * 8 < span;
+#pragma unroll
+            for (int q = 0; q < 2 * MT; ++q) stage[0][q] = in ? *reinterpret_cast<const uint4*>(xp[q] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 2 * NT; ++q)
+                stage[0][2 * MT + q] = in ? *reinterpret_cast<const uint4*>(wp + (rank0 + q * 8 < s.rank ? q * next8 : 0) + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int q = 0; q < 2 * (MT + NT); ++q) turn(0, q);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+    __syncthreads();
+    float(*sums)[BM][PITCH] = reinterpret_cast<float(*)[BM][PITCH]>(room);
     // a lane has four consecutive ranks of one token
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) *reinterpret_cast<float4_t*>(&sums[wave][i * 16 + m][j * 16 + g * 4]) = acc[i][j];
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<float4_t*>(&sums[wave][i * 16 + n][j * 16 + g * 4]) = acc[i][j];
     __syncthreads();
-    float* out = s.partial + ((int64_t)blockIdx.y * s.tokens + pc.row0) * s.rank;
+    float* out = s.partial + ((int64_t)blockIdx.y * s.tokens + row0) * s.rank + rank0;
     for (int i = threadIdx.x; i < BM * NT * 4; i += 256) {
         const int r = i / (NT * 4), c = i % (NT * 4) * 4;
         if (r >= rows || rank0 + c >= s.rank) continue;
         float4_t v = *reinterpret_cast<const float4_t*>(&sums[0][r][c]);
 #pragma unroll
         for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const float4_t*>(&sums[w][r][c]);
-        *reinterpret_cast<float4_t*>(out + (int64_t)r * s.rank + rank0 + c) = v;
+        *reinterpret_cast<float4_t*>(out + (int64_t)r * s.rank + c) = v;
     }
 }
 
@@ -204,9 +374,8 @@ struct ExpandArgs {
     int pieces;
     const uint16_t* w;       // [adapters, out, rank]
     const float* scale;      // [adapters] or null
-    const int32_t* offset;
-    const int32_t* order;
-    int64_t tokens, width, chunk;  // chunk: of the out features for one block, a multiple of 256
+    const Tile* tiles;
+    int64_t tokens, width, chunk;  // chunk: of the out features for one block, a multiple of 64 for each wave
     int adapters, rank;
     const uint16_t* residual;
     uint16_t* out;           // [tokens, width], or null
@@ -214,109 +383,194 @@ struct ExpandArgs {
     float* scaled;           // joined sums times the scale [token in order][rank], or null
 };
 
-// A block has 16 * NT tokens of one adapter (or of none) and `chunk` out
-// features. Its waves take 64 features at a time: the tile's rows are ordered
-// so that a lane ends up with 16 consecutive features of a token, and the four
-// lanes of a token with a whole 128-byte line.
-template <int NT>
-__global__ __launch_bounds__(256) void adapter_expand_kernel(const ExpandArgs e) {
-    constexpr int BM = 16 * NT;
-    extern __shared__ __attribute__((aligned(16))) uint16_t parts[];  // [hi, lo][token][pitch]
-    const int pitch = e.rank + 8;
-    const Groups groups{e.offset, nullptr, 0, e.tokens, e.adapters + 1};
-    const Piece pc = find_piece<true>(groups, BM, (int)blockIdx.x);
-    if (pc.group < 0) return;
+// A block has a tile of up to 16 * MT tokens and `chunk` out features. KS matrix
+// instructions cover the rank, padded with zeros to 32 * KS, for each of the two
+// parts of h; KS = 0: a rank of up to 16, whose parts lie side by side in one
+// instruction. A wave takes F features at a time: their rows of b, which are one run
+// of memory, come in whole and are turned over in the wave's own LDS, the next F on
+// their way; so do the results, the other way round, so that neighbouring lanes
+// write one token's features.
+template <int MT, int KS>
+__global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(const ExpandArgs e) {
+    constexpr int BM = 16 * MT, RANK = KS ? 32 * KS : 16, PITCH = RANK + 8, KN = KS ? KS : 1;
+    constexpr int F = KS > 4 ? 32 : 64, FT = F / 16, OUT = F + 4, LOADS = F * RANK / 512;  // (a load: 1 KB)
+    constexpr int ROOM = F * RANK * 2, OUT_ROOM = BM * OUT * 4;
+    static_assert(ROOM % 16 == 0 && OUT_ROOM % 16 == 0, "16-byte pieces");
+    __shared__ __attribute__((aligned(16))) uint16_t parts[2][BM][PITCH];
+    __shared__ __attribute__((aligned(16))) char room[4][ROOM > OUT_ROOM ? ROOM : OUT_ROOM];  // b's rows, then the results
+    const Tile* tile = &e.tiles[blockIdx.x];
     const int lane = lane_id(), wave = threadIdx.x / kWave, n = lane & 15, g = lane >> 4;
-    const int rows = pc.rows < BM ? (int)pc.rows : BM;
-    const bool none = pc.group == e.adapters;
-    const float scale = none || !e.scale ? 1.0f : e.scale[pc.group];
-    const int quads = e.rank / 4;
-    for (int i = threadIdx.x; i < BM * quads; i += 256) {
-        const int r = i / quads, c = (i - r * quads) * 4;
-        float4_t v = {0.f, 0.f, 0.f, 0.f};
-        if (r < rows && !none) v = join_pieces(e.partial + (pc.row0 + r) * e.rank + c, e.tokens * e.rank, e.pieces);
-        if (r < rows && blockIdx.y == 0) {
-            if (e.hidden) *reinterpret_cast<float4_t*>(e.hidden + (int64_t)e.order[pc.row0 + r] * e.rank + c) = v;
-            if (e.scaled) *reinterpret_cast<float4_t*>(e.scaled + (pc.row0 + r) * e.rank + c) = v * scale;
+    const int group = uniform(tile->group), row0 = uniform(tile->row0), rows = uniform(tile->rows);
+    if (group < 0) return;
+    const bool none = group == e.adapters, whole = e.width % 8 == 0;
+    const int64_t end = (int64_t)(blockIdx.y + 1) * e.chunk < e.width ? (int64_t)(blockIdx.y + 1) * e.chunk : e.width;
+    // b's rows, PR 16-byte pieces each in LDS (zeros past the rank): a load takes RPL of
+    // them, a lane the piece lp of row lane / PR; piece i lies at i ^ (i / 8 ^ i / 64) % 8
+    constexpr int PR = RANK / 8, RPL = kWave / PR;
+    const int lr = lane / PR, lp = lane % PR;
+    const bool held = lp * 8 < e.rank;
+    const uint16_t* const wp = e.w + ((int64_t)group * e.width + lr) * e.rank + lp * 8;
+    uint4 stage[LOADS];
+    auto load = [&](int64_t o0) {
+        const uint16_t* from = wp + o0 * e.rank;
+        const int64_t next = (int64_t)RPL * e.rank;
+        if (o0 + F <= e.width) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) stage[i] = held ? *reinterpret_cast<const uint4*>(from + i * next) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i)
+                stage[i] = held && o0 + i * RPL + lr < e.width ? *reinterpret_cast<const uint4*>(from + i * next) : make_uint4(0, 0, 0, 0);
         }
-        v *= scale;
-        uint2 hi, lo;
-        halves2(v[0], v[1], &hi.x, &lo.x);
-        halves2(v[2], v[3], &hi.y, &lo.y);
-        *reinterpret_cast<uint2*>(parts + r * pitch + c) = hi;
-        *reinterpret_cast<uint2*>(parts + (BM + r) * pitch + c) = lo;
+    };
+    auto place = [](int i) { return (i ^ (((i >> 3) ^ (i >> 6)) & 7)) * 16; };
+    // the results' lanes: 8 features of token 64 * 8 / F * q + lane / (F / 8)
+    constexpr int LR = F / 8, TOKENS = kWave / LR, Q = BM / TOKENS;
+    const int rt = lane / LR, ro = lane % LR * 8;
+    int64_t at[Q];  // of the lane's features in out and residual, but for o0; < 0: no token
+#pragma unroll
+    for (int q = 0; q < Q; ++q) at[q] = q * TOKENS + rt < rows ? tile->token[q * TOKENS + rt] * e.width + ro : -1;
+    uint4 residual[Q];
+    auto load_residual = [&](int64_t o0) {
+        if (!e.residual || !whole) return;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            residual[q] = make_uint4(0, 0, 0, 0);
+            if (at[q] >= 0 && o0 + ro < e.width) residual[q] = *reinterpret_cast<const uint4*>(e.residual + at[q] + o0);
+        }
+    };
+    int64_t o0 = blockIdx.y * e.chunk + wave * F;
+    const float scale = none || !e.scale ? 1.0f : e.scale[group];
+    if (e.out && o0 < end) {
+        if (!none) load(o0);
+        load_residual(o0);
+    }
+    // the pieces' sums: all of a thread's values of several pieces on their way at a time
+    constexpr int ITEMS = (BM * RANK + 1023) / 1024;
+    float4_t sum[ITEMS];
+    auto item_row = [&](int i) { return (int)(i * 256 + threadIdx.x) / (RANK / 4); };
+    auto item_column = [&](int i) { return (int)(i * 256 + threadIdx.x) % (RANK / 4) * 4; };
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) sum[i] = float4_t{0.f, 0.f, 0.f, 0.f};
+    if (!none) {
+        const float* from[ITEMS];
+#pragma unroll
+        for (int i = 0; i < ITEMS; ++i) {  // (what lies past the tile or the rank reads what is there: its sums are not kept)
+            const int r = item_row(i) < rows ? item_row(i) : rows - 1, c = item_column(i) < e.rank ? item_column(i) : 0;
+            from[i] = e.partial + (int64_t)(row0 + r) * e.rank + c;
+        }
+        const int64_t next = e.tokens * e.rank;
+        constexpr int AT_ONCE = ITEMS > 2 ? 2 : 4;
+        int p = 0;
+        for (; p + AT_ONCE <= e.pieces; p += AT_ONCE) {
+            float4_t v[AT_ONCE][ITEMS];
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u)
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i) v[u][i] = *reinterpret_cast<const float4_t*>(from[i] + (p + u) * next);
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u)
+#pragma unroll
+                for (int i = 0; i < ITEMS; ++i) sum[i] += v[u][i];
+        }
+        for (; p < e.pieces; ++p)
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i) sum[i] += *reinterpret_cast<const float4_t*>(from[i] + p * next);
+    }
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+        const int r = item_row(i), c = item_column(i);
+        if (r >= BM) break;  // (a small tile of a small rank has fewer values than threads)
+        const bool in = r < rows && c < e.rank;
+        const float4_t v = in ? sum[i] : float4_t{0.f, 0.f, 0.f, 0.f}, k = v * scale;
+        if (in && blockIdx.y == 0) {
+            if (e.hidden) *reinterpret_cast<float4_t*>(e.hidden + (int64_t)tile->token[r] * e.rank + c) = v;
+            if (e.scaled) *reinterpret_cast<float4_t*>(e.scaled + (int64_t)(row0 + r) * e.rank + c) = k;
+        }
+        uint32_t h[2], l[2];
+        halves2(k[0], k[1], &h[0], &l[0]);
+        halves2(k[2], k[3], &h[1], &l[1]);
+        *reinterpret_cast<uint2_t*>(&parts[0][r][c]) = uint2_t{h[0], h[1]};
+        *reinterpret_cast<uint2_t*>(&parts[1][r][c]) = uint2_t{l[0], l[1]};
     }
     if (!e.out) return;
-    __syncthreads();
-    int64_t token[NT];
+    sync_lds();
+    char* const mine = room[wave];
+    float(*const results)[OUT] = reinterpret_cast<float(*)[OUT]>(mine);
+    for (; o0 < end; o0 += 4 * F) {
+        float4_t acc[MT][FT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) token[t] = t * 16 + n < rows ? e.order[pc.row0 + t * 16 + n] : -1;
-    const bool whole = e.width % 8 == 0, dual = e.rank % 32 == 0;
-    const int eighths = e.rank / 8;  // 16-byte pieces of a row of w
-    const int64_t end = (int64_t)(blockIdx.y + 1) * e.chunk < e.width ? (int64_t)(blockIdx.y + 1) * e.chunk : e.width;
-    for (int64_t o0 = blockIdx.y * e.chunk + wave * 64; o0 < end; o0 += 256) {
-        float4_t acc[4][NT];
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) acc[p][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+            for (int p = 0; p < FT; ++p) acc[t][p] = float4_t{0.f, 0.f, 0.f, 0.f};
         if (!none) {
-            const uint16_t* wp[4];
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {  // row n of tile p is feature (n / 4) * 16 + p * 4 + n % 4
-                const int64_t o = o0 + (n >> 2) * 16 + p * 4 + (n & 3);
-                wp[p] = e.w + ((int64_t)pc.group * e.width + (o < e.width ? o : e.width - 1)) * e.rank;
-            }
-            if (dual) {
-                for (int k = 0; k < e.rank; k += 32) {
-                    bf16x8_t wf[4];
+            for (int i = 0; i < LOADS; ++i) put16(mine + place(i * 64 + lane), stage[i]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (o0 + 4 * F < end) load(o0 + 4 * F);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) wf[p] = frag_at(wp[p] + k + g * 8);
+            for (int k = 0; k < KN; ++k) {
+                const int piece = KS ? k * 4 + g : g & 1;
+                bf16x8_t wf[FT];
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const bf16x8_t hi = frag_at(parts + (t * 16 + n) * pitch + k + g * 8);
-                        const bf16x8_t lo = frag_at(parts + (BM + t * 16 + n) * pitch + k + g * 8);
+                for (int p = 0; p < FT; ++p)
+                    wf[p] = get16(mine + place((p * 16 + n) * PR + piece));
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) acc[p][t] = mul16(wf[p], lo, mul16(wf[p], hi, acc[p][t]));
-                    }
-                }
-            } else {  // the two parts one after the other along the reduction: a row of w twice
-                for (int k = 0; k < 2 * eighths; k += 4) {
-                    const int piece = k + g, part = piece >= eighths;
-                    const int at = piece - part * eighths;
-                    const bool in = piece < 2 * eighths;
-                    bf16x8_t wf[4];
+                for (int t = 0; t < MT; ++t) {
+                    if constexpr (KS > 0) {
+                        const bf16x8_t hi = get16(&parts[0][t * 16 + n][k * 32 + g * 8]), lo = get16(&parts[1][t * 16 + n][k * 32 + g * 8]);
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) wf[p] = in ? frag_at(wp[p] + at * 8) : no_frag();
+                        for (int p = 0; p < FT; ++p) acc[t][p] = mul16(wf[p], lo, mul16(wf[p], hi, acc[t][p]));
+                    } else {
+                        const bf16x8_t h = get16(&parts[g >> 1][t * 16 + n][(g & 1) * 8]);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const bf16x8_t h = in ? frag_at(parts + (part * BM + t * 16 + n) * pitch + at * 8) : no_frag();
-#pragma unroll
-                        for (int p = 0; p < 4; ++p) acc[p][t] = mul16(wf[p], h, acc[p][t]);
+                        for (int p = 0; p < FT; ++p) acc[t][p] = mul16(wf[p], h, acc[t][p]);
                     }
                 }
             }
         }
-        const int64_t o = o0 + g * 16;
+        // a lane has four consecutive features of one token; b's rows are in registers by now
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if (token[t] < 0 || o >= e.width) continue;
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int have = (int)(e.width - o - q * 8 < 8 ? e.width - o - q * 8 : 8);
-                if (have <= 0) continue;
-                float v[8] = {acc[2 * q][t][0], acc[2 * q][t][1], acc[2 * q][t][2], acc[2 * q][t][3],
-                              acc[2 * q + 1][t][0], acc[2 * q + 1][t][1], acc[2 * q + 1][t][2], acc[2 * q + 1][t][3]};
-                const int64_t at = token[t] * e.width + o + q * 8;
+            for (int p = 0; p < FT; ++p) *reinterpret_cast<float4_t*>(&results[t * 16 + n][p * 16 + g * 4]) = acc[t][p];
+        __builtin_amdgcn_wave_barrier();
+        const int64_t o = o0 + ro;
+        const int have = (int)(e.width - o < 8 ? e.width - o : 8);
+        uint4 now[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) now[q] = residual[q];
+        if (o0 + 4 * F < end) load_residual(o0 + 4 * F);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const float4_t lo = *reinterpret_cast<const float4_t*>(&results[q * TOKENS + rt][ro]);
+            const float4_t hi = *reinterpret_cast<const float4_t*>(&results[q * TOKENS + rt][ro + 4]);
+            if (at[q] < 0 || have <= 0) continue;
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            if (whole) {
+                if (e.residual) {
+                    const uint32_t r[4] = {now[q].x, now[q].y, now[q].z, now[q].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[2 * i] += bf16_lo(r[i]);
+                        v[2 * i + 1] += bf16_hi(r[i]);
+                    }
+                }
+                store_run<8>(e.out, at[q] + o0, v, 8, false, true);
+            } else {
                 if (e.residual) {
                     float r[8];
-                    load_run<8>(e.residual + at, have, whole, r);
+                    load_run<8>(e.residual + at[q] + o0, have, false, r);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[i] += r[i];
                 }
-                store_run<8>(e.out, at, v, have, false, whole);
+                store_run<8>(e.out, at[q] + o0, v, have, false, false);
             }
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -436,58 +690,30 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
     }
 }
 
-// ---- transposes of the adapters: [rows][columns] -> [columns][rows] ---------------
-
-// 64 x 64 at a time through LDS; rows and columns are multiples of 8. Blocks past
-// a_blocks are b's.
-__global__ __launch_bounds__(256) void adapter_turn_kernel(const uint16_t* a, const uint16_t* b, uint16_t* at, uint16_t* bt,
-                                                           int64_t in, int64_t out, int rank, int a_blocks) {
-    __shared__ uint16_t tile[64][66];
-    const bool is_a = (int)blockIdx.x < a_blocks;
-    const int64_t rows = is_a ? rank : out, columns = is_a ? in : rank;
-    const int across = (int)((columns + 63) / 64);
-    const int block = is_a ? blockIdx.x : blockIdx.x - a_blocks;
-    const int64_t r0 = (int64_t)(block / across) * 64, c0 = (int64_t)(block % across) * 64;
-    const uint16_t* from = (is_a ? a : b) + (int64_t)blockIdx.y * rows * columns;
-    uint16_t* to = (is_a ? at : bt) + (int64_t)blockIdx.y * rows * columns;
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int r = i / 8, c = i % 8 * 8;
-        if (r0 + r >= rows || c0 + c >= columns) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(from + (r0 + r) * columns + c0 + c);
-        uint32_t* t = reinterpret_cast<uint32_t*>(&tile[r][c]);
-        t[0] = v.x, t[1] = v.y, t[2] = v.z, t[3] = v.w;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 64 * 8; i += 256) {
-        const int c = i / 8, r = i % 8 * 8;
-        if (c0 + c >= columns || r0 + r >= rows) continue;
-        uint32_t q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = tile[r + 2 * k][c] | (uint32_t)tile[r + 2 * k + 1][c] << 16;
-        *reinterpret_cast<uint4*>(to + (c0 + c) * rows + r0 + r) = make_uint4(q[0], q[1], q[2], q[3]);
-    }
-}
-
 // ---- host --------------------------------------------------------------------
 
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Room {  // places in the workspace
-    size_t offset, order, partial, scaled, turned_a, turned_b, bytes;
+    size_t offset, order, tiles, partial, scaled, turned_a, turned_b, bytes;
 };
 
-int shrink_tiles(int64_t tokens) { return tokens >= 1024 ? 2 : 1; }
-int64_t shrink_piece(int64_t tokens, int adapters, int rank, int64_t in) {
-    const int bm = 16 * shrink_tiles(tokens);
-    const int64_t tiles = (tokens + bm - 1) / bm * ((rank + 63) / 64);
-    int64_t pieces = 512 / (tiles > 0 ? tiles : 1);
+bool few(int64_t tokens) { return tokens <= kFewTokens; }
+int tile_tokens(int64_t tokens) { return tokens >= 1024 ? kTallTile : kTile; }
+int64_t tile_slots(int64_t tokens, int adapters) { return tokens / tile_tokens(tokens) + adapters + 1; }
+
+// Pieces of the reduction: until there are some two blocks for a CU, of at least
+// 64 for each of a block's waves.
+int64_t shrink_piece(int64_t tokens, int rank, int64_t in) {
+    const int64_t tiles = (tokens + tile_tokens(tokens) - 1) / tile_tokens(tokens) * ((rank + 63) / 64);
+    int64_t pieces = (rank > 32 ? 768 : 640) / (tiles > 0 ? tiles : 1);
     if (pieces > in / 256) pieces = in / 256;
     if (pieces > 32) pieces = 32;
     if (pieces < 1) pieces = 1;
     return ((in + pieces - 1) / pieces + 63) / 64 * 64;
 }
-int64_t piece_count(int64_t tokens, int adapters, int rank, int64_t in) {
-    const int64_t p = shrink_piece(tokens, adapters, rank, in);
+int64_t piece_count(int64_t tokens, int rank, int64_t in) {
+    const int64_t p = shrink_piece(tokens, rank, in);
     return (in + p - 1) / p;
 }
 
@@ -495,58 +721,82 @@ Room room_for(int64_t tokens, int adapters, int rank, int64_t in, int64_t out, b
     Room r;
     r.offset = 0;
     r.order = padded(((size_t)adapters + 2) * 4);
-    r.partial = r.order + padded((size_t)tokens * 4);
-    r.scaled = r.partial + padded((size_t)piece_count(tokens, adapters, rank, grad ? out : in) * tokens * rank * 4);
+    r.tiles = r.order + padded((size_t)tokens * 4);
+    r.partial = r.tiles + padded((size_t)tile_slots(tokens, adapters) * sizeof(Tile));
+    r.scaled = r.partial + padded((size_t)piece_count(tokens, rank, grad ? out : in) * tokens * rank * 4);
     r.turned_a = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
     r.turned_b = r.turned_a + (grad ? padded((size_t)adapters * rank * in * 2) : 0);
     r.bytes = r.turned_b + (grad ? padded((size_t)adapters * rank * out * 2) : 0);
     return r;
 }
 
-hipError_t plan(const int64_t* index, int64_t tokens, int adapters, int32_t* offset, int32_t* order, hipStream_t stream) {
-    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)adapters + 1), dim3(kPlanThreads), 0, stream, index, (int)tokens,
-                       adapters, offset, order);
+hipError_t plan(const PlanArgs& p, hipStream_t stream) {
+    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)(p.adapters + 1 + (p.squares + 3) / 4)), dim3(kPlanThreads), 0, stream, p);
     return hipGetLastError();
 }
 
-hipError_t shrink(const ShrinkArgs& s, hipStream_t stream) {
-    const int mt = shrink_tiles(s.tokens), nt = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : 4;
-    const Groups g{s.offset, nullptr, 0, s.tokens, s.adapters};
-    const dim3 grid((unsigned)worst_pieces(g, 16 * mt, true), (unsigned)((s.in + s.piece - 1) / s.piece), (unsigned)((s.rank + 16 * nt - 1) / (16 * nt)));
-#define CGD_SHRINK(M, N) hipLaunchKernelGGL((adapter_shrink_kernel<M, N>), grid, dim3(256), 0, stream, s)
-    if (mt == 1 && nt == 1)
-        CGD_SHRINK(1, 1);
-    else if (mt == 1 && nt == 2)
-        CGD_SHRINK(1, 2);
-    else if (mt == 1)
-        CGD_SHRINK(1, 4);
-    else if (nt == 1)
-        CGD_SHRINK(2, 1);
-    else if (nt == 2)
-        CGD_SHRINK(2, 2);
+// own_plan: few tokens, and the kernel makes the tiles itself.
+hipError_t shrink(const ShrinkArgs& s, bool own_plan, hipStream_t stream) {
+    const int nt = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : 4;
+    const dim3 grid((unsigned)tile_slots(s.tokens, s.adapters), (unsigned)((s.in + s.piece - 1) / s.piece), (unsigned)((s.rank + 16 * nt - 1) / (16 * nt)));
+#define CGD_SHRINK(M, N, F) hipLaunchKernelGGL((adapter_shrink_kernel<M, N, (M + N <= 3 ? 2 : 1), F>), grid, dim3(256), 0, stream, s)
+#define CGD_SHRINK_RANK(M, F)  \
+    do {                       \
+        if (nt == 1)           \
+            CGD_SHRINK(M, 1, F); \
+        else if (nt == 2)      \
+            CGD_SHRINK(M, 2, F); \
+        else                   \
+            CGD_SHRINK(M, 4, F); \
+    } while (0)
+    if (own_plan)
+        CGD_SHRINK_RANK(1, true);
+    else if (tile_tokens(s.tokens) == kTile)
+        CGD_SHRINK_RANK(1, false);
     else
-        CGD_SHRINK(2, 4);
+        CGD_SHRINK_RANK(2, false);
+#undef CGD_SHRINK_RANK
 #undef CGD_SHRINK
     return hipGetLastError();
 }
 
+template <int MT>
+void expand_rank(const ExpandArgs& e, const dim3& grid, hipStream_t stream) {
+#define CGD_EXPAND(K) hipLaunchKernelGGL((adapter_expand_kernel<MT, K>), grid, dim3(256), 0, stream, e)
+    if (e.rank <= 16)
+        CGD_EXPAND(0);
+    else if (e.rank <= 32)
+        CGD_EXPAND(1);
+    else if (e.rank <= 64)
+        CGD_EXPAND(2);
+    else if (e.rank <= 128)
+        CGD_EXPAND(4);
+    else
+        CGD_EXPAND(8);
+#undef CGD_EXPAND
+}
+
 hipError_t expand(const ExpandArgs& in, hipStream_t stream) {
     ExpandArgs e = in;
-    const int nt = e.tokens >= 2048 && e.rank <= 128 ? 4 : e.tokens >= 512 ? 2 : 1;  // (at most 64 KB of LDS)
-    const Groups g{e.offset, nullptr, 0, e.tokens, e.adapters + 1};
-    const int64_t tiles = worst_pieces(g, 16 * nt, true), steps = e.out ? (e.width + 255) / 256 : 1;
-    int64_t chunks = (1024 + tiles - 1) / tiles;
+    const int tile = tile_tokens(e.tokens), step = e.rank <= 128 ? 256 : 128;  // features of a block's waves at a time
+    const int64_t tiles = (e.tokens + tile - 1) / tile, steps = e.out ? (e.width + step - 1) / step : 1;
+    int64_t chunks = ((e.rank > 32 ? 384 : 640) + tiles - 1) / tiles;
     if (chunks > steps) chunks = steps;
-    e.chunk = (steps + chunks - 1) / chunks * 256;
-    const dim3 grid((unsigned)tiles, (unsigned)((steps * 256 + e.chunk - 1) / e.chunk));
-    const size_t lds = (size_t)2 * 16 * nt * (e.rank + 8) * 2;
-    if (nt == 4)
-        hipLaunchKernelGGL(adapter_expand_kernel<4>, grid, dim3(256), lds, stream, e);
-    else if (nt == 2)
-        hipLaunchKernelGGL(adapter_expand_kernel<2>, grid, dim3(256), lds, stream, e);
+    e.chunk = (steps + chunks - 1) / chunks * step;
+    const dim3 grid((unsigned)tile_slots(e.tokens, e.adapters), (unsigned)((steps * step + e.chunk - 1) / e.chunk));
+    if (tile == kTile)
+        expand_rank<1>(e, grid, stream);
     else
-        hipLaunchKernelGGL(adapter_expand_kernel<1>, grid, dim3(256), lds, stream, e);
+        expand_rank<2>(e, grid, stream);
     return hipGetLastError();
+}
+
+// The two products; the pieces of the first are set here.
+hipError_t products(ShrinkArgs s, ExpandArgs e, bool own_plan, hipStream_t stream) {
+    s.piece = shrink_piece(s.tokens, s.rank, s.in);
+    e.pieces = (int)((s.in + s.piece - 1) / s.piece);
+    const hipError_t err = shrink(s, own_plan, stream);
+    return err == hipSuccess ? expand(e, stream) : err;
 }
 
 }  // namespace
@@ -562,17 +812,18 @@ hipError_t launch_adapters(const AdapterArgs& p, void* workspace, hipStream_t st
     if (p.tokens == 0) return hipSuccess;
     char* ws = static_cast<char*>(workspace);
     const Room room = room_for(p.tokens, p.adapters, p.rank, p.in, p.out_features, false);
+    const bool own_plan = few(p.tokens);
     int32_t* offset = reinterpret_cast<int32_t*>(ws + room.offset);
     int32_t* order = reinterpret_cast<int32_t*>(ws + room.order);
+    Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
     float* partial = reinterpret_cast<float*>(ws + room.partial);
-    hipError_t err = plan(p.index, p.tokens, p.adapters, offset, order, stream);
-    if (err != hipSuccess) return err;
-    const int64_t piece = shrink_piece(p.tokens, p.adapters, p.rank, p.in);
-    err = shrink(ShrinkArgs{p.x, p.a, offset, order, p.tokens, p.in, piece, p.adapters, p.rank, partial}, stream);
-    if (err != hipSuccess) return err;
-    return expand(ExpandArgs{partial, (int)((p.in + piece - 1) / piece), p.b, p.scale, offset, order, p.tokens, p.out_features, 0,
-                             p.adapters, p.rank, p.residual, p.out, p.hidden, nullptr},
-                  stream);
+    if (!own_plan) {
+        const hipError_t err = plan(PlanArgs{p.index, (int)p.tokens, p.adapters, offset, order, tiles, tile_tokens(p.tokens), nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, 0}, stream);
+        if (err != hipSuccess) return err;
+    }
+    return products(ShrinkArgs{p.x, p.a, p.index, tiles, p.tokens, p.in, 0, p.adapters, p.rank, partial},
+                    ExpandArgs{partial, 0, p.b, p.scale, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, p.residual, p.out, p.hidden, nullptr},
+                    own_plan, stream);
 }
 
 hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipStream_t stream) {
@@ -582,22 +833,22 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
     int32_t* order = reinterpret_cast<int32_t*>(ws + room.order);
     float* partial = reinterpret_cast<float*>(ws + room.partial);
     float* scaled = reinterpret_cast<float*>(ws + room.scaled);
+    Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
     uint16_t* at = reinterpret_cast<uint16_t*>(ws + room.turned_a);
     uint16_t* bt = reinterpret_cast<uint16_t*>(ws + room.turned_b);
-    hipError_t err = plan(p.index, p.tokens, p.adapters, offset, order, stream);
+    const bool through = p.tokens && (p.grad_x || p.grad_a);  // gh is needed
+    const int64_t down = (p.rank + 63) / 64;
+    const int64_t a_squares = through && p.grad_x ? p.adapters * down * ((p.in + 63) / 64) : 0;
+    const int64_t b_squares = through ? p.adapters * down * ((p.out_features + 63) / 64) : 0;
+    hipError_t err = plan(PlanArgs{p.index, (int)p.tokens, p.adapters, offset, order, tiles, tile_tokens(p.tokens), p.a, p.b, at, bt, p.in, p.out_features, p.rank, a_squares,
+                                   a_squares + b_squares},
+                          stream);
     if (err != hipSuccess) return err;
-    if (p.tokens && (p.grad_x || p.grad_a)) {
-        const int64_t down = (p.rank + 63) / 64;
-        const int64_t a_blocks = p.grad_x ? down * ((p.in + 63) / 64) : 0, b_blocks = down * ((p.out_features + 63) / 64);
-        hipLaunchKernelGGL(adapter_turn_kernel, dim3((unsigned)(a_blocks + b_blocks), (unsigned)p.adapters), dim3(256), 0, stream,
-                           p.a, p.b, at, bt, p.in, p.out_features, p.rank, (int)a_blocks);
-        if ((err = hipGetLastError()) != hipSuccess) return err;
-        const int64_t piece = shrink_piece(p.tokens, p.adapters, p.rank, p.out_features);
-        err = shrink(ShrinkArgs{p.grad, bt, offset, order, p.tokens, p.out_features, piece, p.adapters, p.rank, partial}, stream);
-        if (err != hipSuccess) return err;
-        err = expand(ExpandArgs{partial, (int)((p.out_features + piece - 1) / piece), at, p.scale, offset, order, p.tokens, p.in, 0,
-                                p.adapters, p.rank, nullptr, p.grad_x, nullptr, p.grad_a ? scaled : nullptr},
-                     stream);
+    if (through) {
+        err = products(ShrinkArgs{p.grad, bt, p.index, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, partial},
+                       ExpandArgs{partial, 0, at, p.scale, tiles, p.tokens, p.in, 0, p.adapters, p.rank, nullptr, p.grad_x, nullptr,
+                                  p.grad_a ? scaled : nullptr},
+                       false, stream);
         if (err != hipSuccess) return err;
     }
     if (p.grad_a || p.grad_b) {
