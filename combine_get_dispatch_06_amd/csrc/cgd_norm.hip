@@ -10,51 +10,55 @@
 // Memory-bound: every input is read once into registers and every output written
 // once; a row's sums go over its lanes with shuffles and, where a row has more
 // than a wave, over its waves through LDS.
-#include "cgd_device.h"
+#include "cgd_gemm.h"
 #include "cgd_layer_launch.h"
 
 namespace cgd {
 
 namespace {
 
-// Sum of v over the LANES lanes (16, 32, 64) or all LANES threads of the block
-// that hold a row; every one of them gets it. `slot`: LDS, one float per wave.
-template <int LANES>
-__device__ __forceinline__ float row_sum(float v, float* slot) {
-#pragma unroll
-    for (int d = (LANES < kWave ? LANES : kWave) / 2; d; d >>= 1) v += __shfl_xor(v, d, kWave);
-    if constexpr (LANES > kWave) {
-        const int wave = threadIdx.x / kWave;
-        if (lane_id() == 0) slot[wave] = v;
-        __syncthreads();
-        v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < LANES / kWave; ++w) v += slot[w];
-    }
-    return v;
-}
+// The lanes that hold a row: LANES neighbours (16, 32, 64) of a block of 256, or
+// (0) a whole block of `threads`, a multiple of 64.
+constexpr int kMaxWaves = 16;
 
-// The same of two values.
-template <int LANES>
-__device__ __forceinline__ void row_sums(float& a, float& b, float (*slot)[2]) {
+// The value of the lane N places on, around a row of 16 lanes: within the vector unit,
+// where a shuffle through LDS is some ten times as late.
+template <int N>
+__device__ __forceinline__ float turned16(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float sum16(float v) {  // the same bits in all 16 lanes: addition commutes
+    v += turned16<8>(v);
+    v += turned16<4>(v);
+    v += turned16<2>(v);
+    return v + turned16<1>(v);
+}
+__device__ __forceinline__ float max16(float v) {
+    v = fmaxf(v, turned16<8>(v));
+    v = fmaxf(v, turned16<4>(v));
+    v = fmaxf(v, turned16<2>(v));
+    return fmaxf(v, turned16<1>(v));
+}
+__device__ __forceinline__ float of_lane(float v, int lane) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); }
+
+// Sums of N values over a row; every lane of it gets them. `slot`: LDS, for blocks.
+template <int LANES, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], int threads, float (*slot)[N]) {
 #pragma unroll
-    for (int d = (LANES < kWave ? LANES : kWave) / 2; d; d >>= 1) {
-        a += __shfl_xor(a, d, kWave);
-        b += __shfl_xor(b, d, kWave);
+    for (int i = 0; i < N; ++i) {
+        v[i] = sum16(v[i]);
+        if constexpr (LANES == 32) v[i] += __shfl_xor(v[i], 16, kWave);
+        if constexpr (LANES == 0 || LANES == 64) v[i] = (of_lane(v[i], 0) + of_lane(v[i], 16)) + (of_lane(v[i], 32) + of_lane(v[i], 48));
     }
-    if constexpr (LANES > kWave) {
-        const int wave = threadIdx.x / kWave;
-        if (lane_id() == 0) {
-            slot[wave][0] = a;
-            slot[wave][1] = b;
-        }
-        __syncthreads();
-        a = b = 0.0f;
+    if constexpr (LANES == 0) {
+        const int wave = threadIdx.x / kWave, waves = threads / kWave;
+        if (lane_id() == 0)
 #pragma unroll
-        for (int w = 0; w < LANES / kWave; ++w) {
-            a += slot[w][0];
-            b += slot[w][1];
-        }
+            for (int i = 0; i < N; ++i) slot[wave][i] = v[i];
+        sync_lds();
+        const int from = lane_id() & (kMaxWaves - 1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = of_lane(sum16(from < waves ? slot[from][i] : 0.0f), 0);
     }
 }
 
@@ -65,7 +69,6 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&v)[8]) {
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
-__device__ __forceinline__ uint4 vec_at(const uint16_t* p, int64_t v) { return reinterpret_cast<const uint4*>(p)[v]; }
 
 __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&out)[8]) {
     if (f32) {
@@ -77,77 +80,87 @@ __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&o
     }
 }
 
-// LANES threads hold a row, V 16-byte vectors each; a block has THREADS threads.
-template <int THREADS, int LANES, int V>
-__global__ __launch_bounds__(THREADS) void norm_kernel(const NormArgs a) {
-    __shared__ float slot[THREADS / kWave];
+// V 16-byte vectors a lane, R rows one after the other (their loads together).
+template <int LANES, int V, int R>
+__global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(const NormArgs a, int threads) {
+    __shared__ float slot[kMaxWaves][1];
     const int nvec = a.width / 8;
-    const int64_t row = (int64_t)blockIdx.x * (THREADS / LANES) + threadIdx.x / LANES;
-    const int l = threadIdx.x % LANES;
-    if (LANES <= kWave && row >= a.rows) return;  // (a row of a whole block always exists)
-    const int64_t base = row * nvec;
-    uint4 xs[V], rs[V];
+    constexpr int GROUPS = LANES ? 256 / LANES : 1;
+    const int step = LANES ? LANES : threads;
+    const int l = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
+    const int64_t row0 = (int64_t)blockIdx.x * (GROUPS * R) + (LANES ? threadIdx.x / (LANES ? LANES : 1) : 0);
+    uint4 xs[R][V], rs[R][V];
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        const int v = l + u * LANES;
-        xs[u] = rs[u] = make_uint4(0, 0, 0, 0);
-        if (v < nvec) {
-            xs[u] = vec_at(a.x, base + v);
-            if (a.residual) rs[u] = vec_at(a.residual, base + v);
+    for (int k = 0; k < R; ++k) {
+        const int64_t row = row0 + k * GROUPS, base = row * nvec;
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            const int v = l + u * step;
+            xs[k][u] = rs[k][u] = make_uint4(0, 0, 0, 0);
+            if (v < nvec && row < a.rows) {
+                xs[k][u] = reinterpret_cast<const uint4*>(a.x)[base + v];
+                if (a.residual) rs[k][u] = reinterpret_cast<const uint4*>(a.residual)[base + v];
+            }
         }
     }
-    float s[V][8];
-    float ss = 0.0f;
+    float w[V][8];
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        float r[8];
-        unpack8(xs[u], s[u]);
-        unpack8(rs[u], r);
+    for (int u = 0; u < V; ++u) weight8(a.weight, a.weight_f32, l + u * step < nvec ? l + u * step : 0, w[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (a.residual) s[u][i] += r[i];
-            ss = __builtin_fmaf(s[u][i], s[u][i], ss);
+    for (int k = 0; k < R; ++k) {
+        const int64_t row = row0 + k * GROUPS, base = row * nvec;
+        float s[V][8];
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int u = 0; u < V; ++u) {
+            float r[8];
+            unpack8(xs[k][u], s[u]);
+            unpack8(rs[k][u], r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (a.residual) s[u][i] += r[i];
+                ss[0] = __builtin_fmaf(s[u][i], s[u][i], ss[0]);
+            }
         }
-    }
-    const float r = rsqrtf(row_sum<LANES>(ss, slot) / (float)a.width + a.eps);
+        row_sums<LANES>(ss, threads, slot);
+        const float r = rsqrtf(ss[0] / (float)a.width + a.eps);
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-        const int v = l + u * LANES;
-        const bool in = v < nvec;
-        if (in && a.sum) reinterpret_cast<uint4*>(a.sum)[base + v] = pack8(s[u]);
-        float y[8];
-        float w[8];
-        if (in) weight8(a.weight, a.weight_f32, v, w);
-        float m = 0.0f;
+        for (int u = 0; u < V; ++u) {
+            const int v = l + u * step;
+            const bool in = v < nvec && row < a.rows;
+            if (in && a.sum) reinterpret_cast<uint4*>(a.sum)[base + v] = pack8(s[u]);
+            float y[8];
+            float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            y[i] = in ? s[u][i] * r * w[i] : 0.0f;
-            m = fmaxf(m, fabsf(y[i]));
-        }
-        if (in && a.y) reinterpret_cast<uint4*>(a.y)[base + v] = pack8(y);
-        if (a.codes) {  // 16 lanes hold a block of 128: all of them are in the row or none
-            const Fp8Scale sc = fp8_block_scale(group16_max(m), a.format);
-            if (in) {
-                uint2 q;
-                q.x = pack_e4m3x4(y[0] * sc.mul, y[1] * sc.mul, y[2] * sc.mul, y[3] * sc.mul);
-                q.y = pack_e4m3x4(y[4] * sc.mul, y[5] * sc.mul, y[6] * sc.mul, y[7] * sc.mul);
-                reinterpret_cast<uint2*>(a.codes)[base + v] = q;
-                if ((v & 15) == 0) {
-                    const int64_t at = (base + v) / 16;
-                    if (a.format == 2)
-                        static_cast<uint8_t*>(a.scales)[at] = (uint8_t)sc.ue8m0;
-                    else
-                        static_cast<float*>(a.scales)[at] = sc.scale;
+            for (int i = 0; i < 8; ++i) {
+                y[i] = s[u][i] * r * w[u][i];
+                m = fmaxf(m, fabsf(y[i]));
+            }
+            if (in && a.y) reinterpret_cast<uint4*>(a.y)[base + v] = pack8(y);
+            if (a.codes) {  // 16 lanes hold a block of 128: all of them are in the row or none
+                const Fp8Scale sc = fp8_block_scale(max16(m), a.format);
+                if (in) {
+                    uint2 q;
+                    q.x = pack_e4m3x4(y[0] * sc.mul, y[1] * sc.mul, y[2] * sc.mul, y[3] * sc.mul);
+                    q.y = pack_e4m3x4(y[4] * sc.mul, y[5] * sc.mul, y[6] * sc.mul, y[7] * sc.mul);
+                    reinterpret_cast<uint2*>(a.codes)[base + v] = q;
+                    if ((v & 15) == 0) {
+                        const int64_t at = (base + v) / 16;
+                        if (a.format == 2)
+                            static_cast<uint8_t*>(a.scales)[at] = (uint8_t)sc.ue8m0;
+                        else
+                            static_cast<float*>(a.scales)[at] = sc.scale;
+                    }
                 }
             }
         }
     }
 }
 
-template <int THREADS, int LANES, int V>
-hipError_t norm_rows(const NormArgs& all, hipStream_t stream) {
-    constexpr int kRows = THREADS / LANES;
-    const int64_t most = kMaxWorkItems / LANES;  // whole blocks of rows
+template <int LANES, int V, int R = 1>
+hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
+    const int rows = LANES ? 256 / (LANES ? LANES : 1) * R : 1;
+    const int64_t most = kMaxWorkItems / threads * rows;
     for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
         NormArgs a = all;
         a.rows = all.rows - r0 < most ? all.rows - r0 : most;
@@ -160,66 +173,77 @@ hipError_t norm_rows(const NormArgs& all, hipStream_t stream) {
             a.codes += at;
             a.scales = static_cast<char*>(a.scales) + at / kFp8Block * (a.format == 2 ? 1 : 4);
         }
-        hipLaunchKernelGGL((norm_kernel<THREADS, LANES, V>), dim3((unsigned)((a.rows + kRows - 1) / kRows)), dim3(THREADS), 0, stream, a);
+        hipLaunchKernelGGL((norm_kernel<LANES, V, R>), dim3((unsigned)((a.rows + rows - 1) / rows)), dim3((unsigned)threads), 0, stream, a, threads);
     }
     return hipGetLastError();
 }
 
-// Gradient. A block takes every gridDim.x-th group of rows and keeps the
-// weight's gradient of its columns in registers: one row of sums a block.
-template <int THREADS, int LANES, int V>
-__global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormGradArgs a) {
-    constexpr int kRows = THREADS / LANES;
-    __shared__ float slot[2][THREADS / kWave][2];
+// Gradient. A block takes every gridDim.x-th group of rows and keeps the weight's gradient of its columns in registers: one row of sums a
+// block. Two blocks share a CU, so that one loads while the other adds up: 45 us for
+// 4095 x 7168 where one with its next row on the way took 52.
+template <int LANES, int V>
+__global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void norm_grad_kernel(const NormGradArgs a, int threads) {
+    constexpr int GROUPS = LANES ? 256 / LANES : 1;
+    constexpr bool KEPT = V < 4;  // room for the weights in registers
+    __shared__ float slot[2][kMaxWaves][2];
     const int nvec = a.width / 8;
-    const int l = threadIdx.x % LANES;
+    const int step = LANES ? LANES : threads;
+    const int l = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
     float w[V][8], dw[V][8];
 #pragma unroll
     for (int u = 0; u < V; ++u) {
+        if (KEPT) weight8(a.weight, a.weight_f32, l + u * step < nvec ? l + u * step : 0, w[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[u][i] = dw[u][i] = 0.0f;
-        if (l + u * LANES < nvec) weight8(a.weight, a.weight_f32, l + u * LANES, w[u]);
+        for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
     }
     int turn = 0;
     const float mean = 1.0f / (float)a.width;
-    for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < a.rows; row0 += (int64_t)gridDim.x * kRows) {
-        const int64_t row = row0 + threadIdx.x / LANES;
-        const bool there = LANES > kWave || row < a.rows;
+    int64_t row0 = (int64_t)blockIdx.x * GROUPS;
+    const int mine = LANES ? threadIdx.x / (LANES ? LANES : 1) : 0;
+    for (; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t row = row0 + mine;
+        const bool there = row < a.rows;
         const int64_t base = row * nvec;
-        uint4 xs[V], gs[V], ds[V];
+        uint4 x4[V], g4[V], d4[V];
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int v = l + u * LANES;
-            xs[u] = gs[u] = ds[u] = make_uint4(0, 0, 0, 0);
+            const int v = l + u * step;
+            x4[u] = g4[u] = d4[u] = make_uint4(0, 0, 0, 0);
             if (there && v < nvec) {
-                xs[u] = vec_at(a.x, base + v);
-                gs[u] = vec_at(a.grad, base + v);
-                if (a.grad_sum) ds[u] = vec_at(a.grad_sum, base + v);
+                x4[u] = reinterpret_cast<const uint4*>(a.x)[base + v];
+                g4[u] = reinterpret_cast<const uint4*>(a.grad)[base + v];
+                if (a.grad_sum) d4[u] = reinterpret_cast<const uint4*>(a.grad_sum)[base + v];
             }
         }
-        float ss = 0.0f, gx = 0.0f;
+        if constexpr (!KEPT) {
+            const int again = afresh(l);
+#pragma unroll
+            for (int u = 0; u < V; ++u) weight8(a.weight, a.weight_f32, again + u * step < nvec ? again + u * step : 0, w[u]);
+        }
+        float sums[2] = {0.0f, 0.0f};  // of s^2, of g s
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             float x[8], g[8];
-            unpack8(xs[u], x);
-            unpack8(gs[u], g);
+            unpack8(x4[u], x);
+            unpack8(g4[u], g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                ss = __builtin_fmaf(x[i], x[i], ss);
-                gx = __builtin_fmaf(g[i] * w[u][i], x[i], gx);
+                sums[0] = __builtin_fmaf(x[i], x[i], sums[0]);
+                sums[1] = __builtin_fmaf(g[i] * w[u][i], x[i], sums[1]);
             }
         }
-        row_sums<LANES>(ss, gx, slot[turn]);  // (two sets of slots: a wave may be one row ahead, not two)
+        // two sets of slots: a wave may be one row ahead of another's reads, not two
+        row_sums<LANES>(sums, threads, slot[turn]);
         turn ^= 1;
-        const float r = rsqrtf(ss * mean + a.eps);
-        const float c = gx * r * r * mean;  // times s: h mean(g h)
+        const float r = rsqrtf(sums[0] * mean + a.eps);
+        const float c = sums[1] * r * r * mean;  // times s: h mean(g h)
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int v = l + u * LANES;
+            const int v = l + u * step;
             float x[8], g[8], d[8];
-            unpack8(xs[u], x);
-            unpack8(gs[u], g);
-            unpack8(ds[u], d);
+            unpack8(x4[u], x);
+            unpack8(g4[u], g);
+            unpack8(d4[u], d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (there) dw[u][i] = __builtin_fmaf(g[i] * r, x[i], dw[u][i]);  // (r of no row may be infinite)
@@ -230,30 +254,29 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const NormGradArgs a
         }
     }
     if (!a.partial) return;
-    if constexpr (LANES <= kWave) {  // the block's groups of lanes, in order
-        __shared__ float part[THREADS][9];
-        float* out = a.partial + (int64_t)blockIdx.x * a.width;
+    float* const out = a.partial + (int64_t)blockIdx.x * a.width;
+    if constexpr (LANES > 0) {  // the block's groups of lanes, in order
+        __shared__ float part[256][9];
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 8; ++i) part[threadIdx.x][i] = dw[u][i];
             __syncthreads();
-            for (int c = threadIdx.x; c < LANES * 8; c += THREADS) {
+            for (int c = threadIdx.x; c < LANES * 8; c += 256) {
                 float s = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kRows; ++k) s += part[k * LANES + c / 8][c % 8];
+                for (int k = 0; k < GROUPS; ++k) s += part[k * LANES + c / 8][c % 8];
                 if (c + u * LANES * 8 < a.width) out[c + u * LANES * 8] = s;
             }
         }
     } else {
-        float4* out = reinterpret_cast<float4*>(a.partial + (int64_t)blockIdx.x * a.width);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
-            const int v = l + u * LANES;
+            const int v = l + u * step;
             if (v >= nvec) continue;
-            out[2 * v] = make_float4(dw[u][0], dw[u][1], dw[u][2], dw[u][3]);
-            out[2 * v + 1] = make_float4(dw[u][4], dw[u][5], dw[u][6], dw[u][7]);
+            reinterpret_cast<float4*>(out)[2 * v] = make_float4(dw[u][0], dw[u][1], dw[u][2], dw[u][3]);
+            reinterpret_cast<float4*>(out)[2 * v + 1] = make_float4(dw[u][4], dw[u][5], dw[u][6], dw[u][7]);
         }
     }
 }
@@ -285,40 +308,44 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* partial,
         static_cast<uint16_t*>(out)[c] = (uint16_t)pack_bf16x2(s, 0.0f);
 }
 
-template <int THREADS, int LANES, int V>
-void norm_grad_rows(const NormGradArgs& a, int64_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL((norm_grad_kernel<THREADS, LANES, V>), dim3((unsigned)blocks), dim3(THREADS), 0, stream, a);
+template <int LANES, int V>
+void norm_grad_rows(const NormGradArgs& a, int64_t blocks, int threads, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_grad_kernel<LANES, V>), dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, a, threads);
 }
 
-// Threads that hold a row of the gradient, and a block's threads.
-int grad_lanes(int width) { return width <= 128 ? 16 : width <= 256 ? 32 : width <= 2048 ? 64 : width <= 8192 ? 512 : 1024; }
-int grad_threads(int width) { return width <= 2048 ? 256 : width <= 8192 ? 512 : 1024; }
+// Threads of a block that holds a row with V vectors a lane.
+int row_threads(int width, int v) { return (width / 8 + kWave * v - 1) / (kWave * v) * kWave; }
+
+constexpr int kRowsTogether = 2;  // of small widths, where there are many
+// Vectors a lane of a row that has a block. Few rows get as many threads as they have
+// vectors; otherwise two vectors leave fewest lanes without one (4096 x 7168: 47 us;
+// four 53), and the gradient has room for one in 64 registers.
+int forward_vectors(int64_t rows, int width) { return width <= 8192 ? (rows <= 512 ? 1 : 2) : width <= 16384 && rows <= 512 ? 2 : 4; }
+int gradient_vectors(int width) { return width <= 8192 ? 1 : width <= 16384 ? 2 : 4; }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     if (a.rows == 0) return hipSuccess;
     const int w = a.width;
-    if (w <= 128) return norm_rows<256, 16, 1>(a, stream);
-    if (w <= 256) return norm_rows<256, 32, 1>(a, stream);
-    if (w <= 512) return norm_rows<256, 64, 1>(a, stream);
-    if (w <= 1024) return norm_rows<256, 64, 2>(a, stream);
-    if (w <= 2048) return norm_rows<256, 256, 1>(a, stream);
-    if (a.rows <= 512) {  // few rows: more threads for each
-        if (w <= 8192) return norm_rows<1024, 1024, 1>(a, stream);
-        if (w <= 16384) return norm_rows<1024, 1024, 2>(a, stream);
-        return norm_rows<1024, 1024, 4>(a, stream);
+    if (w <= 512) {  // several rows a block; many rows: two at a time
+        const int lanes = w <= 128 ? 16 : w <= 256 ? 32 : 64;
+        const bool many = a.rows * lanes >= int64_t(256) * 2048 * kRowsTogether;
+        if (lanes == 16) return many ? norm_rows<16, 1, kRowsTogether>(a, 256, stream) : norm_rows<16, 1>(a, 256, stream);
+        if (lanes == 32) return many ? norm_rows<32, 1, kRowsTogether>(a, 256, stream) : norm_rows<32, 1>(a, 256, stream);
+        return many ? norm_rows<64, 1, kRowsTogether>(a, 256, stream) : norm_rows<64, 1>(a, 256, stream);
     }
-    if (w <= 4096) return norm_rows<256, 256, 2>(a, stream);
-    if (w <= 8192) return norm_rows<256, 256, 4>(a, stream);
-    if (w <= 16384) return norm_rows<512, 512, 4>(a, stream);
-    return norm_rows<1024, 1024, 4>(a, stream);
+    if (w <= 1024) return norm_rows<64, 2>(a, 256, stream);
+    const int v = forward_vectors(a.rows, w);
+    const int threads = row_threads(w, v);
+    if (v == 1) return norm_rows<0, 1>(a, threads, stream);
+    if (v == 2) return norm_rows<0, 2>(a, threads, stream);
+    return norm_rows<0, 4>(a, threads, stream);
 }
 
 int64_t norm_grad_blocks(int64_t rows, int width) {
-    const int per = grad_threads(width) / grad_lanes(width);
-    const int64_t groups = (rows + per - 1) / per;
-    const int64_t most = width <= 2048 ? 1024 : width <= 8192 ? 512 : 256;
+    const int per = width <= 128 ? 16 : width <= 256 ? 8 : width <= 1024 ? 4 : 1;  // rows at a time
+    const int64_t groups = (rows + per - 1) / per, most = width <= 1024 ? 1024 : 512;
     return groups < most ? groups : most;
 }
 
@@ -326,24 +353,21 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
     const int w = a.width;
     const int64_t blocks = norm_grad_blocks(a.rows, w);
     if (blocks > 0) {
+        const int v = gradient_vectors(w);
         if (w <= 128)
-            norm_grad_rows<256, 16, 1>(a, blocks, stream);
+            norm_grad_rows<16, 1>(a, blocks, 256, stream);
         else if (w <= 256)
-            norm_grad_rows<256, 32, 1>(a, blocks, stream);
+            norm_grad_rows<32, 1>(a, blocks, 256, stream);
         else if (w <= 512)
-            norm_grad_rows<256, 64, 1>(a, blocks, stream);
+            norm_grad_rows<64, 1>(a, blocks, 256, stream);
         else if (w <= 1024)
-            norm_grad_rows<256, 64, 2>(a, blocks, stream);
-        else if (w <= 2048)
-            norm_grad_rows<256, 64, 4>(a, blocks, stream);
-        else if (w <= 4096)
-            norm_grad_rows<512, 512, 1>(a, blocks, stream);
-        else if (w <= 8192)
-            norm_grad_rows<512, 512, 2>(a, blocks, stream);
-        else if (w <= 16384)
-            norm_grad_rows<1024, 1024, 2>(a, blocks, stream);
+            norm_grad_rows<64, 2>(a, blocks, 256, stream);
+        else if (v == 1)
+            norm_grad_rows<0, 1>(a, blocks, row_threads(w, 1), stream);
+        else if (v == 2)
+            norm_grad_rows<0, 2>(a, blocks, row_threads(w, 2), stream);
         else
-            norm_grad_rows<1024, 1024, 4>(a, blocks, stream);
+            norm_grad_rows<0, 4>(a, blocks, row_threads(w, 4), stream);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
     }

@@ -22,7 +22,7 @@ import ctypes
 import torch
 
 from . import DispatchHandle, PackedHandle, _check, _dev_tensor, _fp8_empty, load
-from .experts import _BF16, _Current, _F32, _ptr, _result, _shaped, _stream, _workspace
+from .experts import _BF16, _F32, _ptr, _result, _shaped, _workspace
 
 __all__ = ["rms_norm", "rms_norm_backward", "adapter_linear", "adapter_linear_backward", "dropout", "dropout_backward",
            "combine_backward"]
@@ -54,24 +54,49 @@ def configure(lib):
     return lib
 
 
+# The smallest of these calls take longer on the host than on the GPU, so a tensor that
+# is as it should be is told by the fewest questions (a device by its number), and
+# the device is only changed where it has to be.
+_BFLOAT16, _FLOAT32 = torch.bfloat16, torch.float32
+_Tensor = torch.Tensor
+
+
+def _like(t, name: str, dtype, shape, dev: int):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()):
+        _shaped(t, name, dtype, tuple(shape), torch.device("cuda", dev))  # says what is wrong
+
+
+def _bf16(t, name: str, ndim: int) -> int:
+    """The device of a contiguous bf16 tensor (ndim 0: of any dimensions, but one at least)."""
+    if not (isinstance(t, _Tensor) and t.is_cuda and t.dtype is _BFLOAT16 and t.is_contiguous() and t.dim() == (ndim or t.dim() or 1)):
+        _dev_tensor(t, name, _BFLOAT16, ndim or max(1, t.dim() if isinstance(t, _Tensor) else 1))
+    return t.get_device()
+
+
+def _call(name: str, dev: int, *args):
+    """A call of the library on the device's current stream."""
+    before = torch._C._cuda_getDevice()
+    if before != dev:
+        torch.cuda.set_device(dev)
+    try:
+        status = getattr(load(), name)(*args, torch._C._cuda_getCurrentRawStream(dev))
+    finally:
+        if before != dev:
+            torch.cuda.set_device(before)
+    if status:
+        _check(name, status)
+
+
 # ---------------------------------------------------------------------------
 # Norm
 # ---------------------------------------------------------------------------
 
-def _rows(x, name: str):
-    """-> (rows, hidden) of a bf16 tensor whose last dimension is normed."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    _dev_tensor(x, name, torch.bfloat16, max(1, x.dim()))
-    H = x.shape[-1]
-    return (x.numel() // H if H else 0), H
-
-
-def _norm_weight(weight, H: int, dev) -> int:
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.bfloat16, torch.float32):
+def _norm_weight(weight, H: int, dev: int) -> int:
+    dtype = weight.dtype if isinstance(weight, _Tensor) else None
+    if dtype is not _BFLOAT16 and dtype is not _FLOAT32:
         raise TypeError("weight must be a bfloat16 or float32 tensor")
-    _shaped(weight, "weight", weight.dtype, (H,), dev)
-    return _F32 if weight.dtype == torch.float32 else _BF16
+    _like(weight, "weight", dtype, (H,), dev)
+    return _F32 if dtype is _FLOAT32 else _BF16
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
@@ -85,31 +110,35 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     (bf16 tensor, FP8 tuple), e.g. for a gate beside the dispatch. sum is s in bf16,
     the residual stream; y is made from s before that rounding. sum_out, if given,
     receives it and may be residual or x itself."""
-    lib = load()
-    n, H = _rows(x, "x")
-    dev = x.device
+    dev = _bf16(x, "x", 0)
+    shape = x.shape
+    H = shape[-1]
+    n = x.numel() // H if H else 0
     wtype = _norm_weight(weight, H, dev)
+    y = q = sc = total = None
     if residual is not None:
-        _shaped(residual, "residual", torch.bfloat16, tuple(x.shape), dev)
-    if return_bf16 and cast_fp8 is None:
-        raise ValueError("return_bf16 goes with cast_fp8")
-    if cast_fp8 is not None and H % 128:
-        raise ValueError(f"an FP8 output needs a last dimension that is a multiple of 128 (got {H})")
+        _like(residual, "residual", _BFLOAT16, shape, dev)
     if sum_out is not None:
         if residual is None:
             raise ValueError("sum_out goes with residual")
-        _result(sum_out, torch.bfloat16, tuple(x.shape), dev, weight, *([x] if sum_out.data_ptr() != x.data_ptr() else []),
-                over=residual)
-    with _Current(dev):
-        y = torch.empty_like(x) if cast_fp8 is None or return_bf16 else None
-        total = sum_out if sum_out is not None else None if residual is None else torch.empty_like(x)
-        q = sc = None
-        if cast_fp8 is not None:
-            q, sc = _fp8_empty(n, H, cast_fp8, dev)
-            q, sc = q.view(x.shape), sc.view(*x.shape[:-1], H // 128)
-        _check("cgd_rms_norm",
-               lib.cgd_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), wtype, eps, n, H, _ptr(y), _ptr(q), _ptr(sc),
-                                0 if cast_fp8 is None else cast_fp8, _ptr(total), _stream(dev)))
+        total = _result(sum_out, _BFLOAT16, tuple(shape), x.device, weight, *([x] if sum_out.data_ptr() != x.data_ptr() else []),
+                        over=residual)
+    elif residual is not None:
+        total = torch.empty_like(x)
+    if cast_fp8 is None:
+        if return_bf16:
+            raise ValueError("return_bf16 goes with cast_fp8")
+        y = torch.empty_like(x)
+    else:
+        if H % 128:
+            raise ValueError(f"an FP8 output needs a last dimension that is a multiple of 128 (got {H})")
+        if return_bf16:
+            y = torch.empty_like(x)
+        q, sc = _fp8_empty(n, H, cast_fp8, x.device)
+        if len(shape) != 2:
+            q, sc = q.view(shape), sc.view(*shape[:-1], H // 128)
+    _call("cgd_rms_norm", dev, x.data_ptr(), _ptr(residual), weight.data_ptr(), wtype, eps, n, H, _ptr(y), _ptr(q), _ptr(sc),
+          cast_fp8 or 0, _ptr(total))
     out = y if q is None else (y, (q, sc)) if return_bf16 else (q, sc)
     return out if residual is None else (out, total)
 
@@ -120,20 +149,19 @@ def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     sum that rms_norm returned, whose gradient is that of both terms): -> (grad_x
     bf16 like x, grad_weight like weight). grad_sum, what reaches the residual
     stream on its other way, is added to grad_x. All bf16 but a float32 weight's."""
-    lib = load()
-    n, H = _rows(x, "x")
-    dev = x.device
+    dev = _bf16(x, "x", 0)
+    shape = x.shape
+    H = shape[-1]
+    n = x.numel() // H if H else 0
     wtype = _norm_weight(weight, H, dev)
-    _shaped(grad_y, "grad_y", torch.bfloat16, tuple(x.shape), dev)
+    _like(grad_y, "grad_y", _BFLOAT16, shape, dev)
     if grad_sum is not None:
-        _shaped(grad_sum, "grad_sum", torch.bfloat16, tuple(x.shape), dev)
-    with _Current(dev):
-        gx, gw = torch.empty_like(x), torch.empty_like(weight)
-        nbytes = lib.cgd_rms_norm_backward_workspace_bytes(n, H)
-        wk = _workspace(nbytes, dev)
-        _check("cgd_rms_norm_backward",
-               lib.cgd_rms_norm_backward(_ptr(grad_y), _ptr(x), _ptr(weight), wtype, eps, n, H, _ptr(grad_sum), _ptr(gx),
-                                         _ptr(gw), _ptr(wk), nbytes, _stream(dev)))
+        _like(grad_sum, "grad_sum", _BFLOAT16, shape, dev)
+    gx, gw = torch.empty_like(x), torch.empty_like(weight)
+    nbytes = load().cgd_rms_norm_backward_workspace_bytes(n, H)
+    wk = _workspace(nbytes, x.device)
+    _call("cgd_rms_norm_backward", dev, grad_y.data_ptr(), x.data_ptr(), weight.data_ptr(), wtype, eps, n, H, _ptr(grad_sum),
+          gx.data_ptr(), gw.data_ptr(), _ptr(wk), nbytes)
     return gx, gw
 
 
@@ -142,19 +170,18 @@ def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
 # ---------------------------------------------------------------------------
 
 def _adapters(x, a, b, adapter_idx, scale):
-    """-> (T, J, R, I, O, device)."""
-    _dev_tensor(x, "x", torch.bfloat16, 2)
-    dev = x.device
+    """-> (T, J, R, I, O, the device's number)."""
+    dev = _bf16(x, "x", 2)
     T, I = x.shape
-    _dev_tensor(a, "a", torch.bfloat16, 3)
-    _dev_tensor(b, "b", torch.bfloat16, 3)
-    J, R = a.shape[:2]
+    _bf16(a, "a", 3)
+    _bf16(b, "b", 3)
+    J, R, _ = a.shape
     O = b.shape[1]
-    _shaped(a, "a", torch.bfloat16, (J, R, I), dev)
-    _shaped(b, "b", torch.bfloat16, (J, O, R), dev)
-    _shaped(adapter_idx, "adapter_idx", torch.int64, (T,), dev)
+    _like(a, "a", _BFLOAT16, (J, R, I), dev)
+    _like(b, "b", _BFLOAT16, (J, O, R), dev)
+    _like(adapter_idx, "adapter_idx", torch.int64, (T,), dev)
     if scale is not None:
-        _shaped(scale, "scale", torch.float32, (J,), dev)
+        _like(scale, "scale", _FLOAT32, (J,), dev)
     return T, J, R, I, O, dev
 
 
@@ -172,21 +199,18 @@ def adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_id
     With return_hidden -> (out, hidden float32 [T, R]: a[j] @ x[t]), which
     adapter_linear_backward takes. out, if given, shares no memory with an input,
     but may be residual itself."""
-    lib = load()
     T, J, R, I, O, dev = _adapters(x, a, b, adapter_idx, scale)
     if residual is not None:
-        _shaped(residual, "residual", torch.bfloat16, (T, O), dev)
-    with _Current(dev):
-        if out is None:
-            out = torch.empty((T, O), dtype=torch.bfloat16, device=dev)
-        else:
-            _result(out, torch.bfloat16, (T, O), dev, x, a, b, adapter_idx, scale, over=residual)
-        hidden = torch.empty((T, R), dtype=torch.float32, device=dev) if return_hidden else None
-        nbytes = lib.cgd_adapter_linear_workspace_bytes(T, J, R, I, O)
-        wk = _workspace(nbytes, dev)
-        _check("cgd_adapter_linear",
-               lib.cgd_adapter_linear(_ptr(x), _ptr(a), _ptr(b), _ptr(scale), _ptr(adapter_idx), T, J, R, I, O,
-                                      _ptr(residual), _ptr(out), _ptr(hidden), _ptr(wk), nbytes, _stream(dev)))
+        _like(residual, "residual", _BFLOAT16, (T, O), dev)
+    if out is None:
+        out = x.new_empty((T, O)) if residual is None else torch.empty_like(residual)
+    else:
+        _result(out, _BFLOAT16, (T, O), x.device, x, a, b, adapter_idx, scale, over=residual)
+    hidden = torch.empty((T, R), dtype=_FLOAT32, device=x.device) if return_hidden else None
+    nbytes = load().cgd_adapter_linear_workspace_bytes(T, J, R, I, O)
+    wk = _workspace(nbytes, x.device)
+    _call("cgd_adapter_linear", dev, x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), adapter_idx.data_ptr(), T, J, R, I, O,
+          _ptr(residual), out.data_ptr(), _ptr(hidden), _ptr(wk), nbytes)
     return (out, hidden) if return_hidden else out
 
 
@@ -197,18 +221,14 @@ def adapter_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, a: torch.Te
     zeros, a token without an adapter a zero row. The residual's gradient is
     grad_out; the shared projection's grad_x comes from linear_backward and adds to
     this one. O has to be a multiple of 8."""
-    lib = load()
     T, J, R, I, O, dev = _adapters(x, a, b, adapter_idx, scale)
-    _shaped(grad_out, "grad_out", torch.bfloat16, (T, O), dev)
-    _shaped(hidden, "hidden", torch.float32, (T, R), dev)
-    with _Current(dev):
-        gx, ga, gb = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
-        nbytes = lib.cgd_adapter_linear_backward_workspace_bytes(T, J, R, I, O)
-        wk = _workspace(nbytes, dev)
-        _check("cgd_adapter_linear_backward",
-               lib.cgd_adapter_linear_backward(_ptr(grad_out), _ptr(x), _ptr(a), _ptr(b), _ptr(scale), _ptr(adapter_idx),
-                                               _ptr(hidden), T, J, R, I, O, _ptr(gx), _ptr(ga), _ptr(gb), _ptr(wk),
-                                               nbytes, _stream(dev)))
+    _like(grad_out, "grad_out", _BFLOAT16, (T, O), dev)
+    _like(hidden, "hidden", _FLOAT32, (T, R), dev)
+    gx, ga, gb = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
+    nbytes = load().cgd_adapter_linear_backward_workspace_bytes(T, J, R, I, O)
+    wk = _workspace(nbytes, x.device)
+    _call("cgd_adapter_linear_backward", dev, grad_out.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale),
+          adapter_idx.data_ptr(), hidden.data_ptr(), T, J, R, I, O, gx.data_ptr(), ga.data_ptr(), gb.data_ptr(), _ptr(wk), nbytes)
     return gx, ga, gb
 
 
@@ -228,27 +248,21 @@ def dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual: torch.Te
     replayed with new numbers; `offset` is added to it. Calls of one seed need
     offsets of their own (a layer's number, a step's). A dropped element is 0 even
     where x is infinite or NaN. out may be x or residual itself."""
-    lib = load()
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    _dev_tensor(x, "x", torch.bfloat16, x.dim())
-    dev = x.device
-    shape = tuple(x.shape)
-    if residual is not None:
-        _shaped(residual, "residual", torch.bfloat16, shape, dev)
+    if not (isinstance(x, _Tensor) and x.is_cuda and x.dtype is _BFLOAT16 and x.is_contiguous()):
+        _dev_tensor(x, "x", _BFLOAT16, x.dim() if isinstance(x, _Tensor) else 1)
+    dev = x.get_device()
     state = None
     if isinstance(seed, torch.Tensor):
-        state, seed = _shaped(seed, "seed", torch.int64, (2,), dev), 0
-    for name, v in (("seed", seed), ("offset", offset)):
-        if not isinstance(v, int) or not 0 <= v < 1 << 64:
-            raise ValueError(f"{name} must be an integer in [0, 2^64) (got {v!r})")
-    with _Current(dev):
-        if out is None:
-            out = torch.empty_like(x)
-        else:
-            _result(out, torch.bfloat16, shape, dev, state, *([x] if out.data_ptr() != x.data_ptr() else []), over=residual)
-        _check("cgd_dropout",
-               lib.cgd_dropout(_ptr(x), _ptr(residual), x.numel(), p, seed, offset, _ptr(state), _ptr(out), _stream(dev)))
+        state, seed = _shaped(seed, "seed", torch.int64, (2,), x.device), 0
+    if not (isinstance(seed, int) and 0 <= seed < 1 << 64 and isinstance(offset, int) and 0 <= offset < 1 << 64):
+        raise ValueError(f"seed and offset must be integers in [0, 2^64) (got {seed!r}, {offset!r})")
+    if residual is not None:
+        _like(residual, "residual", _BFLOAT16, x.shape, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _result(out, _BFLOAT16, tuple(x.shape), x.device, state, *([x] if out.data_ptr() != x.data_ptr() else []), over=residual)
+    _call("cgd_dropout", dev, x.data_ptr(), _ptr(residual), x.numel(), p, seed, offset, _ptr(state), out.data_ptr())
     return out
 
 
@@ -272,27 +286,25 @@ def combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, handle, t
     without a row). Rows that hold no token are left as they were (in a new tensor:
     undefined). out, if given, receives grad_expert_out and shares no memory with
     an input."""
-    lib = load()
     packed = isinstance(handle, PackedHandle)
     if not packed and not isinstance(handle, DispatchHandle):
         raise TypeError("handle must be a DispatchHandle or a PackedHandle")
-    _dev_tensor(expert_out, "expert_out", torch.bfloat16, 3 if packed else 2)
-    dev = expert_out.device
-    H = expert_out.shape[-1]
-    cap = expert_out.shape[0] * expert_out.shape[1] if packed else expert_out.shape[0]
-    if packed and expert_out.shape[:2] != (handle.num_experts, handle.expert_capacity):
+    dev = _bf16(expert_out, "expert_out", 3 if packed else 2)
+    shape = expert_out.shape
+    H = shape[-1]
+    cap = shape[0] * shape[1] if packed else shape[0]
+    if packed and shape[:2] != (handle.num_experts, handle.expert_capacity):
         raise ValueError("expert_out must be [num_experts, expert_capacity, hidden]")
-    T, K = handle.dst_row.shape
-    _shaped(handle.dst_row, "handle.dst_row", torch.int32, (T, K), dev)
-    _shaped(grad_out, "grad_out", torch.bfloat16, (T, H), dev)
-    _shaped(topk_weights, "topk_weights", torch.float32, (T, K), dev)
-    with _Current(dev):
-        if out is None:
-            out = torch.empty_like(expert_out)
-        else:
-            _result(out, torch.bfloat16, tuple(expert_out.shape), dev, grad_out, expert_out, handle.dst_row, topk_weights)
-        gw = torch.empty((T, K), dtype=torch.float32, device=dev)
-        _check("cgd_combine_backward",
-               lib.cgd_combine_backward(_ptr(grad_out), _ptr(expert_out), cap, H, _ptr(handle.dst_row), _ptr(topk_weights),
-                                        T, K, _ptr(out), _ptr(gw), _stream(dev)))
+    dst = handle.dst_row
+    T, K = dst.shape
+    _like(dst, "handle.dst_row", torch.int32, (T, K), dev)
+    _like(grad_out, "grad_out", _BFLOAT16, (T, H), dev)
+    _like(topk_weights, "topk_weights", _FLOAT32, (T, K), dev)
+    if out is None:
+        out = torch.empty_like(expert_out)
+    else:
+        _result(out, _BFLOAT16, tuple(shape), expert_out.device, grad_out, expert_out, dst, topk_weights)
+    gw = torch.empty_like(topk_weights)
+    _call("cgd_combine_backward", dev, grad_out.data_ptr(), expert_out.data_ptr(), cap, H, dst.data_ptr(), topk_weights.data_ptr(),
+          T, K, out.data_ptr(), gw.data_ptr())
     return out, gw
