@@ -206,38 +206,59 @@ struct ShrinkArgs {
     float* partial;          // [pieces][token in order][rank]
 };
 
-// The plan of at most kFewTokens tokens, by every block for itself: a lane of its
-// first wave has a token and counts the groups before its own and the tokens before
-// it. Tiles of 16.
-// (128 tokens: the shrink kernel 14.6 us with it, 5.5 and the plan's 3.2 without.)
-constexpr int kFewTokens = 32;
+// Tile `want` of at most kFewTokens tokens, by the first wave of every block for
+// itself: its lanes hold all tokens' groups, a ballot for 64 of them counts those
+// before a group, and as the groups' first slots ascend, ten such counts find the
+// slot's group among 512. Saves the plan's launch (4 us of a call with 128 tokens).
+constexpr int kFewTokens = 512;
 constexpr int kTile = 16;
 __device__ __forceinline__ void plan_few(const int64_t* index, int tokens, int adapters, int want, Tile& p) {
+    constexpr int CHUNKS = kFewTokens / kWave;
     if (threadIdx.x < kWave) {
-        const int t = lane_id();
-        int mine = INT32_MAX;
-        if (t < tokens) {
-            const int64_t j = index[t];
-            mine = j >= 0 && j < adapters ? (int)j : adapters;
+        const int lane = lane_id();
+        int of[CHUNKS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            of[c] = INT32_MAX;
+            if (c * kWave + lane < tokens) {
+                const int64_t j = index[c * kWave + lane];
+                of[c] = j >= 0 && j < adapters ? (int)j : adapters;
+            }
         }
-        int less = 0, before = 0, same = 0;
-        for (int i = 0; i < tokens; ++i) {
-            const int o = __builtin_amdgcn_readlane(mine, i);
-            less += o < mine;
-            same += o == mine;
-            before += o == mine && i < t;
+        auto before = [&](int group) {
+            int n = 0;
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+                if (c * kWave < tokens) n += __popcll(ballot(of[c] < group));
+            return n;
+        };
+        int group = 0;  // the last one whose slots begin at `want` or before it
+        for (int hi = adapters; group < hi;) {
+            const int mid = (group + hi + 1) / 2;
+            if (before(mid) / kTile + mid <= want)
+                group = mid;
+            else
+                hi = mid - 1;
         }
-        if (t == 0) p.group = -1;
-        __builtin_amdgcn_wave_barrier();
-        const bool here = t < tokens && less / kTile + mine + before / kTile == want;
-        const int i = before % kTile;
-        if (here) p.token[i] = t;
-        if (here && before == same - 1)
-            for (int k = i + 1; k < kTile; ++k) p.token[k] = t;
-        if (here && i == 0) {
-            p.group = mine;
-            p.row0 = less + before;
-            p.rows = same - before < kTile ? same - before : kTile;
+        const int first = before(group), skip = (want - first / kTile - group) * kTile;
+        const int left = before(group + 1) - first - skip, rows = left < kTile ? left : kTile;
+        if (lane == 0) {
+            p.group = left > 0 ? group : -1;
+            p.row0 = first + skip;
+            p.rows = rows;
+        }
+        int seen = -skip;  // of the tile's tokens
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            if (c * kWave >= tokens) break;
+            const uint64_t hits = ballot(of[c] == group);
+            const int at = seen + __popcll(hits & lanemask_lt());
+            if (of[c] == group && at >= 0 && at < rows) {
+                p.token[at] = c * kWave + lane;
+                if (at == rows - 1)
+                    for (int k = rows; k < kTile; ++k) p.token[k] = c * kWave + lane;
+            }
+            seen += __popcll(hits);
         }
     }
     __syncthreads();
@@ -369,6 +390,8 @@ __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs
 
 // ---- the second product: from the rank ----------------------------------------
 
+constexpr int kMostPieces = 16;  // of the first product's reduction
+
 struct ExpandArgs {
     const float* partial;    // [pieces][token in order][rank]
     int pieces;
@@ -460,22 +483,19 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
             from[i] = e.partial + (int64_t)(row0 + r) * e.rank + c;
         }
         const int64_t next = e.tokens * e.rank;
-        constexpr int AT_ONCE = ITEMS > 2 ? 2 : 4;
-        int p = 0;
-        for (; p + AT_ONCE <= e.pieces; p += AT_ONCE) {
+        constexpr int AT_ONCE = ITEMS > 2 ? 2 : ITEMS > 1 ? 4 : kMostPieces;
+        for (int p = 0; p < e.pieces; p += AT_ONCE) {
             float4_t v[AT_ONCE][ITEMS];
 #pragma unroll
             for (int u = 0; u < AT_ONCE; ++u)
 #pragma unroll
-                for (int i = 0; i < ITEMS; ++i) v[u][i] = *reinterpret_cast<const float4_t*>(from[i] + (p + u) * next);
+                for (int i = 0; i < ITEMS; ++i) v[u][i] = *reinterpret_cast<const float4_t*>(from[i] + (p + u < e.pieces ? p + u : 0) * next);
 #pragma unroll
             for (int u = 0; u < AT_ONCE; ++u)
 #pragma unroll
-                for (int i = 0; i < ITEMS; ++i) sum[i] += v[u][i];
+                for (int i = 0; i < ITEMS; ++i)
+                    if (p + u < e.pieces) sum[i] += v[u][i];
         }
-        for (; p < e.pieces; ++p)
-#pragma unroll
-            for (int i = 0; i < ITEMS; ++i) sum[i] += *reinterpret_cast<const float4_t*>(from[i] + p * next);
     }
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
@@ -708,7 +728,7 @@ int64_t shrink_piece(int64_t tokens, int rank, int64_t in) {
     const int64_t tiles = (tokens + tile_tokens(tokens) - 1) / tile_tokens(tokens) * ((rank + 63) / 64);
     int64_t pieces = (rank > 32 ? 768 : 640) / (tiles > 0 ? tiles : 1);
     if (pieces > in / 256) pieces = in / 256;
-    if (pieces > 32) pieces = 32;
+    if (pieces > kMostPieces) pieces = kMostPieces;
     if (pieces < 1) pieces = 1;
     return ((in + pieces - 1) / pieces + 63) / 64 * 64;
 }

@@ -22,7 +22,7 @@ import ctypes
 import torch
 
 from . import DispatchHandle, PackedHandle, _check, _dev_tensor, _fp8_empty, load
-from .experts import _BF16, _F32, _ptr, _result, _shaped, _workspace
+from .experts import _BF16, _F32, _ptr, _shaped
 
 __all__ = ["rms_norm", "rms_norm_backward", "adapter_linear", "adapter_linear_backward", "dropout", "dropout_backward",
            "combine_backward"]
@@ -73,6 +73,21 @@ def _bf16(t, name: str, ndim: int) -> int:
     return t.get_device()
 
 
+def _out(out, name: str, shape, dev: int, inputs, over=()):
+    """The caller's bf16 output: it shares no memory with the inputs (contiguous), which
+    other blocks still read while it is written, but may be one of `over` itself."""
+    _like(out, name, _BFLOAT16, shape, dev)
+    begin = out.data_ptr()
+    end = begin + out.nbytes
+    for t in inputs:
+        if t is not None and t.data_ptr() < end and begin < t.data_ptr() + t.nbytes:
+            raise ValueError(f"{name} shares memory with an input")
+    for t in over:
+        if t is not None and t.data_ptr() != begin and t.data_ptr() < end and begin < t.data_ptr() + t.nbytes:
+            raise ValueError(f"{name} shares memory with an input")
+    return out
+
+
 def _call(name: str, dev: int, *args):
     """A call of the library on the device's current stream."""
     before = torch._C._cuda_getDevice()
@@ -121,8 +136,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     if sum_out is not None:
         if residual is None:
             raise ValueError("sum_out goes with residual")
-        total = _result(sum_out, _BFLOAT16, tuple(shape), x.device, weight, *([x] if sum_out.data_ptr() != x.data_ptr() else []),
-                        over=residual)
+        total = _out(sum_out, "sum_out", shape, dev, (weight,), over=(x, residual))
     elif residual is not None:
         total = torch.empty_like(x)
     if cast_fp8 is None:
@@ -159,7 +173,7 @@ def rms_norm_backward(grad_y: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
         _like(grad_sum, "grad_sum", _BFLOAT16, shape, dev)
     gx, gw = torch.empty_like(x), torch.empty_like(weight)
     nbytes = load().cgd_rms_norm_backward_workspace_bytes(n, H)
-    wk = _workspace(nbytes, x.device)
+    wk = x.new_empty(nbytes // 2) if nbytes else None
     _call("cgd_rms_norm_backward", dev, grad_y.data_ptr(), x.data_ptr(), weight.data_ptr(), wtype, eps, n, H, _ptr(grad_sum),
           gx.data_ptr(), gw.data_ptr(), _ptr(wk), nbytes)
     return gx, gw
@@ -173,12 +187,13 @@ def _adapters(x, a, b, adapter_idx, scale):
     """-> (T, J, R, I, O, the device's number)."""
     dev = _bf16(x, "x", 2)
     T, I = x.shape
-    _bf16(a, "a", 3)
-    _bf16(b, "b", 3)
-    J, R, _ = a.shape
-    O = b.shape[1]
-    _like(a, "a", _BFLOAT16, (J, R, I), dev)
-    _like(b, "b", _BFLOAT16, (J, O, R), dev)
+    if _bf16(a, "a", 3) != dev or _bf16(b, "b", 3) != dev:
+        raise ValueError("a and b must be on x's device")
+    J, R, in_a = a.shape
+    in_b, O, out_r = b.shape
+    if in_a != I or in_b != J or out_r != R:
+        raise ValueError(f"a must be [num_adapters, rank, {I}] and b [num_adapters, out_features, rank] "
+                         f"(got {tuple(a.shape)} and {tuple(b.shape)})")
     _like(adapter_idx, "adapter_idx", torch.int64, (T,), dev)
     if scale is not None:
         _like(scale, "scale", _FLOAT32, (J,), dev)
@@ -205,10 +220,10 @@ def adapter_linear(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter_id
     if out is None:
         out = x.new_empty((T, O)) if residual is None else torch.empty_like(residual)
     else:
-        _result(out, _BFLOAT16, (T, O), x.device, x, a, b, adapter_idx, scale, over=residual)
+        _out(out, "out", (T, O), dev, (x, a, b, adapter_idx, scale), over=(residual,))
     hidden = torch.empty((T, R), dtype=_FLOAT32, device=x.device) if return_hidden else None
     nbytes = load().cgd_adapter_linear_workspace_bytes(T, J, R, I, O)
-    wk = _workspace(nbytes, x.device)
+    wk = x.new_empty(nbytes // 2) if nbytes else None  # (bf16 elements; nothing of it outlives the call)
     _call("cgd_adapter_linear", dev, x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale), adapter_idx.data_ptr(), T, J, R, I, O,
           _ptr(residual), out.data_ptr(), _ptr(hidden), _ptr(wk), nbytes)
     return (out, hidden) if return_hidden else out
@@ -226,7 +241,7 @@ def adapter_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, a: torch.Te
     _like(hidden, "hidden", _FLOAT32, (T, R), dev)
     gx, ga, gb = torch.empty_like(x), torch.empty_like(a), torch.empty_like(b)
     nbytes = load().cgd_adapter_linear_backward_workspace_bytes(T, J, R, I, O)
-    wk = _workspace(nbytes, x.device)
+    wk = x.new_empty(nbytes // 2)
     _call("cgd_adapter_linear_backward", dev, grad_out.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(scale),
           adapter_idx.data_ptr(), hidden.data_ptr(), T, J, R, I, O, gx.data_ptr(), ga.data_ptr(), gb.data_ptr(), _ptr(wk), nbytes)
     return gx, ga, gb
@@ -261,7 +276,7 @@ def dropout(x: torch.Tensor, p: float, seed, offset: int = 0, residual: torch.Te
     if out is None:
         out = torch.empty_like(x)
     else:
-        _result(out, _BFLOAT16, tuple(x.shape), x.device, state, *([x] if out.data_ptr() != x.data_ptr() else []), over=residual)
+        _out(out, "out", x.shape, dev, (state,), over=(x, residual))
     _call("cgd_dropout", dev, x.data_ptr(), _ptr(residual), x.numel(), p, seed, offset, _ptr(state), out.data_ptr())
     return out
 
@@ -303,7 +318,7 @@ def combine_backward(grad_out: torch.Tensor, expert_out: torch.Tensor, handle, t
     if out is None:
         out = torch.empty_like(expert_out)
     else:
-        _result(out, _BFLOAT16, tuple(shape), expert_out.device, grad_out, expert_out, dst, topk_weights)
+        _out(out, "out", shape, dev, (grad_out, expert_out, dst, topk_weights))
     gw = torch.empty_like(topk_weights)
     _call("cgd_combine_backward", dev, grad_out.data_ptr(), expert_out.data_ptr(), cap, H, dst.data_ptr(), topk_weights.data_ptr(),
           T, K, out.data_ptr(), gw.data_ptr())
