@@ -8,9 +8,10 @@
 // belongs to the probability that is used, so the expectation is exact.
 // A dropped element is 0 whatever it held, infinities and NaN included.
 // The gradient is the same call on the gradient.
-// Memory-bound: 4096 x 7168 with a residual 28 us (6.2 TB/s); the generator's 20 wide
-// multiplications a vector fit beside the loads (one vector a thread 29, four 29,
-// non-temporal accesses 29-31).
+// Memory-bound: 4096 x 7168 with a residual 29 us (6.0 TB/s) with non-temporal loads, 33
+// without; stores are ordinary ones (non-temporal 29, too): what comes next reads them.
+// The generator's 20 wide multiplications a vector fit beside the loads (one vector
+// a thread, or four: 1 us more).
 #include "cgd_device.h"
 #include "cgd_layer_launch.h"
 
@@ -48,7 +49,9 @@ __device__ __forceinline__ uint32_t drop2(uint32_t x, uint32_t u, uint32_t r, bo
 }
 
 // U vectors a thread; vector `first` + i of the tensor is vector i here.
-template <int U>
+// FAR: more than the Infinity Cache keeps, so the inputs are not worth a place there.
+constexpr int64_t kFarBytes = int64_t(160) << 20;
+template <int U, bool FAR>
 __global__ __launch_bounds__(kDropThreads) void dropout_kernel(const DropoutArgs a, int64_t first) {
     uint64_t seed = a.seed, offset = a.offset;
     if (a.state) {
@@ -63,8 +66,10 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(const DropoutArgs
         const int64_t v = v0 + u * kDropThreads;
         x[u] = r[u] = make_uint4(0, 0, 0, 0);
         if (v < whole) {
-            x[u] = reinterpret_cast<const uint4*>(a.x)[v];
-            if (a.residual) r[u] = reinterpret_cast<const uint4*>(a.residual)[v];
+            const uint4* xv = reinterpret_cast<const uint4*>(a.x) + v;
+            const uint4* rv = reinterpret_cast<const uint4*>(a.residual) + v;
+            x[u] = FAR ? load_nt(xv) : *xv;
+            if (a.residual) r[u] = FAR ? load_nt(rv) : *rv;
         }
     }
     const bool add = a.residual != nullptr;
@@ -102,14 +107,17 @@ hipError_t launch_dropout(const DropoutArgs& a, hipStream_t stream) {
     for (int64_t v = 0; v < vectors; v += most) {
         const int64_t n = vectors - v < most ? vectors - v : most;
         const int64_t blocks = (n + kDropThreads * U - 1) / (kDropThreads * U);
-        hipLaunchKernelGGL(dropout_kernel<U>, dim3((unsigned)blocks), dim3(kDropThreads), 0, stream, a, v);
+        if (a.n * (a.residual ? 6 : 4) > kFarBytes)
+            hipLaunchKernelGGL((dropout_kernel<U, true>), dim3((unsigned)blocks), dim3(kDropThreads), 0, stream, a, v);
+        else
+            hipLaunchKernelGGL((dropout_kernel<U, false>), dim3((unsigned)blocks), dim3(kDropThreads), 0, stream, a, v);
     }
     return hipGetLastError();
 }
 
 hipError_t preload_dropout() {
     hipFuncAttributes at;
-    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&dropout_kernel<kDropVectors>));
+    return hipFuncGetAttributes(&at, reinterpret_cast<const void*>(&dropout_kernel<kDropVectors, false>));
 }
 
 }  // namespace cgd

@@ -70,6 +70,24 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
     return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// FAR: what the call touches does not fit the Infinity Cache, so nothing of it is worth
+// keeping there: non-temporal accesses. 4096 x 7168 with residual and FP8 (265 MB)
+// 46.7 us against 54, its gradient (235 MB) 42.6 against 48.8; 131040 x 128 (67 MB) 13.6
+// against 11.8.
+constexpr int64_t kFarBytes = int64_t(160) << 20;
+template <bool FAR>
+__device__ __forceinline__ uint4 take(const uint4* p) {
+    if constexpr (FAR) return load_nt(p);
+    return *p;
+}
+template <bool FAR, typename T>
+__device__ __forceinline__ void put(T* p, const T& v) {
+    if constexpr (FAR)
+        store_nt(p, v);
+    else
+        *p = v;
+}
+
 __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&out)[8]) {
     if (f32) {
         const float4 a = static_cast<const float4*>(w)[2 * v], b = static_cast<const float4*>(w)[2 * v + 1];
@@ -81,7 +99,7 @@ __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&o
 }
 
 // V 16-byte vectors a lane, R rows one after the other (their loads together).
-template <int LANES, int V, int R>
+template <int LANES, int V, int R, bool FAR>
 __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(const NormArgs a, int threads) {
     __shared__ float slot[kMaxWaves][1];
     const int nvec = a.width / 8;
@@ -98,8 +116,8 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(const NormArgs
             const int v = l + u * step;
             xs[k][u] = rs[k][u] = make_uint4(0, 0, 0, 0);
             if (v < nvec && row < a.rows) {
-                xs[k][u] = reinterpret_cast<const uint4*>(a.x)[base + v];
-                if (a.residual) rs[k][u] = reinterpret_cast<const uint4*>(a.residual)[base + v];
+                xs[k][u] = take<FAR>(reinterpret_cast<const uint4*>(a.x) + base + v);
+                if (a.residual) rs[k][u] = take<FAR>(reinterpret_cast<const uint4*>(a.residual) + base + v);
             }
         }
     }
@@ -128,7 +146,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(const NormArgs
         for (int u = 0; u < V; ++u) {
             const int v = l + u * step;
             const bool in = v < nvec && row < a.rows;
-            if (in && a.sum) reinterpret_cast<uint4*>(a.sum)[base + v] = pack8(s[u]);
+            if (in && a.sum) put<FAR>(reinterpret_cast<uint4*>(a.sum) + base + v, pack8(s[u]));
             float y[8];
             float m = 0.0f;
 #pragma unroll
@@ -136,14 +154,14 @@ __global__ __launch_bounds__(LANES ? 256 : 1024) void norm_kernel(const NormArgs
                 y[i] = s[u][i] * r * w[u][i];
                 m = fmaxf(m, fabsf(y[i]));
             }
-            if (in && a.y) reinterpret_cast<uint4*>(a.y)[base + v] = pack8(y);
+            if (in && a.y) put<FAR>(reinterpret_cast<uint4*>(a.y) + base + v, pack8(y));
             if (a.codes) {  // 16 lanes hold a block of 128: all of them are in the row or none
                 const Fp8Scale sc = fp8_block_scale(max16(m), a.format);
                 if (in) {
                     uint2 q;
                     q.x = pack_e4m3x4(y[0] * sc.mul, y[1] * sc.mul, y[2] * sc.mul, y[3] * sc.mul);
                     q.y = pack_e4m3x4(y[4] * sc.mul, y[5] * sc.mul, y[6] * sc.mul, y[7] * sc.mul);
-                    reinterpret_cast<uint2*>(a.codes)[base + v] = q;
+                    put<FAR>(reinterpret_cast<uint2*>(a.codes) + base + v, q);
                     if ((v & 15) == 0) {
                         const int64_t at = (base + v) / 16;
                         if (a.format == 2)
@@ -161,6 +179,7 @@ template <int LANES, int V, int R = 1>
 hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
     const int rows = LANES ? 256 / (LANES ? LANES : 1) * R : 1;
     const int64_t most = kMaxWorkItems / threads * rows;
+    const bool far = all.rows * all.width * (all.residual ? 8 : 4) > kFarBytes;  // (FP8 outputs: as if bf16)
     for (int64_t r0 = 0; r0 < all.rows; r0 += most) {
         NormArgs a = all;
         a.rows = all.rows - r0 < most ? all.rows - r0 : most;
@@ -173,7 +192,11 @@ hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
             a.codes += at;
             a.scales = static_cast<char*>(a.scales) + at / kFp8Block * (a.format == 2 ? 1 : 4);
         }
-        hipLaunchKernelGGL((norm_kernel<LANES, V, R>), dim3((unsigned)((a.rows + rows - 1) / rows)), dim3((unsigned)threads), 0, stream, a, threads);
+        const dim3 grid((unsigned)((a.rows + rows - 1) / rows)), block((unsigned)threads);
+        if (far)
+            hipLaunchKernelGGL((norm_kernel<LANES, V, R, true>), grid, block, 0, stream, a, threads);
+        else
+            hipLaunchKernelGGL((norm_kernel<LANES, V, R, false>), grid, block, 0, stream, a, threads);
     }
     return hipGetLastError();
 }
@@ -181,7 +204,7 @@ hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
 // Gradient. A block takes every gridDim.x-th group of rows and keeps the weight's gradient of its columns in registers: one row of sums a
 // block. Two blocks share a CU, so that one loads while the other adds up: 45 us for
 // 4095 x 7168 where one with its next row on the way took 52.
-template <int LANES, int V>
+template <int LANES, int V, bool FAR>
 __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void norm_grad_kernel(const NormGradArgs a, int threads) {
     constexpr int GROUPS = LANES ? 256 / LANES : 1;
     constexpr bool KEPT = V < 4;  // room for the weights in registers
@@ -210,9 +233,9 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
             const int v = l + u * step;
             x4[u] = g4[u] = d4[u] = make_uint4(0, 0, 0, 0);
             if (there && v < nvec) {
-                x4[u] = reinterpret_cast<const uint4*>(a.x)[base + v];
-                g4[u] = reinterpret_cast<const uint4*>(a.grad)[base + v];
-                if (a.grad_sum) d4[u] = reinterpret_cast<const uint4*>(a.grad_sum)[base + v];
+                x4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.x) + base + v);
+                g4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad) + base + v);
+                if (a.grad_sum) d4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad_sum) + base + v);
             }
         }
         if constexpr (!KEPT) {
@@ -310,7 +333,10 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* partial,
 
 template <int LANES, int V>
 void norm_grad_rows(const NormGradArgs& a, int64_t blocks, int threads, hipStream_t stream) {
-    hipLaunchKernelGGL((norm_grad_kernel<LANES, V>), dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, a, threads);
+    if (a.rows * a.width * (a.grad_sum ? 8 : 6) > kFarBytes)
+        hipLaunchKernelGGL((norm_grad_kernel<LANES, V, true>), dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, a, threads);
+    else
+        hipLaunchKernelGGL((norm_grad_kernel<LANES, V, false>), dim3((unsigned)blocks), dim3((unsigned)threads), 0, stream, a, threads);
 }
 
 // Threads of a block that holds a row with V vectors a lane.
