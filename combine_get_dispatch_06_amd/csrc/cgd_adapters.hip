@@ -73,28 +73,22 @@ __device__ __forceinline__ void plan_group(const int64_t* __restrict__ index, in
         const int64_t j = index[t];
         return j >= 0 && j < adapters ? (int)j : adapters;
     };
-    int less = 0, same = 0;
+    int less = 0, same = 0;  // of the wave's tokens
+    auto count = [&](int g) {
+        less += __popcll(ballot(g < mine));
+        same += __popcll(ballot(g == mine));
+    };
     int kept[kPlanKept];
 #pragma unroll
-    for (int u = 0; u < kPlanKept; ++u) {
-        kept[u] = t0 + u * kWave + lane < t1 ? group(t0 + u * kWave + lane) : INT32_MAX;
-        less += kept[u] < mine;
-        same += kept[u] == mine;
-    }
-    for (int t = t0 + kPlanKept * kWave + lane; t < t1; t += 4 * kWave) {
+    for (int u = 0; u < kPlanKept; ++u) kept[u] = t0 + u * kWave + lane < t1 ? group(t0 + u * kWave + lane) : INT32_MAX;
+#pragma unroll
+    for (int u = 0; u < kPlanKept; ++u) count(kept[u]);
+    for (int t = t0 + kPlanKept * kWave; t < t1; t += 4 * kWave) {
         int g[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) g[u] = t + u * kWave < t1 ? group(t + u * kWave) : INT32_MAX;
+        for (int u = 0; u < 4; ++u) g[u] = t + u * kWave + lane < t1 ? group(t + u * kWave + lane) : INT32_MAX;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            less += g[u] < mine;
-            same += g[u] == mine;
-        }
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-        less += __shfl_xor(less, d, kWave);
-        same += __shfl_xor(same, d, kWave);
+        for (int u = 0; u < 4; ++u) count(g[u]);
     }
     if (lane == 0) {
         less_of[wave] = less;
@@ -136,69 +130,17 @@ __device__ __forceinline__ void plan_group(const int64_t* __restrict__ index, in
     for (int t = t0 + kPlanKept * kWave; t < t1; t += kWave) place(t + lane < t1 && group(t + lane) == mine, t + lane);
 }
 
-// 64 x 64 of a transpose through LDS, with 256 threads; rows and columns are
-// multiples of 8.
-__device__ __forceinline__ void turn_tile(const uint16_t* from, uint16_t* to, int64_t rows, int64_t columns, int64_t r0, int64_t c0,
-                                          uint16_t (*tile)[66]) {
-    const int tid = threadIdx.x & 255;
-    for (int i = tid; i < 64 * 8; i += 256) {
-        const int r = i / 8, c = i % 8 * 8;
-        if (r0 + r >= rows || c0 + c >= columns) continue;
-        const uint4 v = *reinterpret_cast<const uint4*>(from + (r0 + r) * columns + c0 + c);
-        uint32_t* t = reinterpret_cast<uint32_t*>(&tile[r][c]);
-        t[0] = v.x, t[1] = v.y, t[2] = v.z, t[3] = v.w;
-    }
-    __syncthreads();
-    for (int i = tid; i < 64 * 8; i += 256) {
-        const int c = i / 8, r = i % 8 * 8;
-        if (c0 + c >= columns || r0 + r >= rows) continue;
-        uint32_t q[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = tile[r + 2 * k][c] | (uint32_t)tile[r + 2 * k + 1][c] << 16;
-        *reinterpret_cast<uint4*>(to + (c0 + c) * rows + r0 + r) = make_uint4(q[0], q[1], q[2], q[3]);
-    }
-}
-
-struct PlanArgs {
-    const int64_t* index;
-    int tokens, adapters;
-    int32_t* offset;
-    int32_t* order;
-    Tile* tiles;
-    int tile;
-    // for gradients: transposes of the adapters, four squares of 64 x 64 a block after the groups'
-    const uint16_t* a;   // [adapters][rank][in]
-    const uint16_t* b;   // [adapters][out][rank]
-    uint16_t* turned_a;  // [adapters][in][rank]
-    uint16_t* turned_b;  // [adapters][rank][out]
-    int64_t in, out;
-    int rank;
-    int64_t a_squares, squares;  // of all adapters: a's, then b's
-};
-
-__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const PlanArgs p) {
+__global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_t* index, int tokens, int adapters, int32_t* offset,
+                                                                    int32_t* order, Tile* tiles, int tile) {
     __shared__ int32_t less_of[kPlanWaves], same_of[kPlanWaves];
-    __shared__ uint16_t turned[4][64][66];
-    if ((int)blockIdx.x <= p.adapters) {
-        plan_group(p.index, p.tokens, p.adapters, blockIdx.x, p.offset, p.order, p.tiles, p.tile, less_of, same_of);
-        return;
-    }
-    const int quarter = threadIdx.x / 256;
-    int64_t t = (int64_t)(blockIdx.x - p.adapters - 1) * 4 + quarter;
-    const bool is_a = t < p.a_squares, there = t < p.squares;
-    if (!is_a) t -= p.a_squares;
-    const int64_t rows = is_a ? p.rank : p.out, columns = is_a ? p.in : p.rank;
-    const int64_t across = (columns + 63) / 64, each = across * ((rows + 63) / 64);
-    const int64_t j = t / each, i = t - j * each;
-    turn_tile((is_a ? p.a : p.b) + j * rows * columns, (is_a ? p.turned_a : p.turned_b) + j * rows * columns, there ? rows : 0,
-              columns, i / across * 64, i % across * 64, turned[quarter]);
+    plan_group(index, tokens, adapters, blockIdx.x, offset, order, tiles, tile, less_of, same_of);
 }
 
 // ---- the first product: to the rank ------------------------------------------
 
 struct ShrinkArgs {
     const uint16_t* x;       // [tokens, in]
-    const uint16_t* w;       // [adapters, rank, in]
+    const uint16_t* w;       // [adapters, rank, in]; TURNED: [adapters, in, rank]
     const int64_t* index;    // few tokens: the kernel makes the tiles itself
     Tile* tiles;             // one for each blockIdx.x
     int64_t tokens, in, piece;  // piece: of `in` for one block, a multiple of 64
@@ -277,8 +219,9 @@ __device__ __forceinline__ char* turn_place(char* room, int row, int piece) {
 
 // A block has a tile of up to 16 * MT tokens and 16 * NT of the ranks over one piece
 // of the reduction; its four waves take 64 * U of it in turn, the next ones on their
-// way while these are multiplied, and join their sums through LDS.
-template <int MT, int NT, int U, bool FEW>
+// way while these are multiplied, and join their sums through LDS. TURNED: w's rows are
+// those of the reduction, and the LDS transposing read makes the operand.
+template <int MT, int NT, int U, bool FEW, bool TURNED>
 __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs s) {
     constexpr int BM = 16 * MT, BN = 16 * NT, PITCH = BN + 4, ROWS = BM + BN;
     constexpr int TURN = ROWS * kRowBytes * U, SUMS = 4 * BM * PITCH * 4;
@@ -302,8 +245,15 @@ __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs
     const uint16_t* xp[2 * MT];
 #pragma unroll
     for (int q = 0; q < 2 * MT; ++q) xp[q] = s.x + tile->token[q * 8 + r8] * s.in + k0 + c8 * 8;
-    const uint16_t* const wp = s.w + ((int64_t)group * s.rank + rank0 + r8) * s.in + k0 + c8 * 8;
-    const int64_t next8 = 8 * s.in;
+    constexpr int WP = 2 * NT, WR = kWave / WP;  // TURNED: 16-byte pieces of a row, rows of a load
+    const int wr = lane / WP, wc = lane % WP;
+    const uint16_t* const wp = TURNED ? s.w + ((int64_t)group * s.in + k0 + wr) * s.rank + rank0 + (rank0 + wc * 8 < s.rank ? wc * 8 : 0)
+                                      : s.w + ((int64_t)group * s.rank + rank0 + r8) * s.in + k0 + c8 * 8;
+    auto w_at = [&](int k, int q) {
+        return reinterpret_cast<const uint4*>(TURNED ? wp + (int64_t)(k + q * WR) * s.rank : wp + (rank0 + q * 8 < s.rank ? q * 8 * s.in : 0) + k);
+    };
+    // 32 bytes of each of four rows at a time
+    auto turned_place = [](int row, int piece) { return row * (BN * 2) + (piece ^ (NT == 4 ? (row & 3) << 1 : 0)) * 16; };
     char* const mine = room + wave * TURN;
     float4_t acc[MT][NT];
 #pragma unroll
@@ -320,11 +270,15 @@ __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs
             for (int q = 0; q < 2 * MT; ++q) stage[v][q] = *reinterpret_cast<const uint4*>(xp[q] + k);
 #pragma unroll
             for (int q = 0; q < 2 * NT; ++q)
-                stage[v][2 * MT + q] = *reinterpret_cast<const uint4*>(wp + (rank0 + q * 8 < s.rank ? q * next8 : 0) + k);
+                stage[v][2 * MT + q] = *w_at(k, q);
         }
     };
     auto turn = [&](int v, int q) {
-        put16(turn_place(mine + v * ROWS * kRowBytes, q * 8 + r8, c8), stage[v][q]);
+        char* at = mine + v * ROWS * kRowBytes;
+        if (TURNED && q >= 2 * MT)
+            put16(at + BM * kRowBytes + turned_place((q - 2 * MT) * WR + wr, wc), stage[v][q]);
+        else
+            put16(turn_place(at, q * 8 + r8, c8), stage[v][q]);
     };
     auto multiply = [&](int v) {
 #pragma unroll
@@ -333,7 +287,14 @@ __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs
 #pragma unroll
             for (int i = 0; i < MT; ++i) xf[i] = get16(turn_place(mine + v * ROWS * kRowBytes, i * 16 + n, h * 4 + g));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) wf[j] = get16(turn_place(mine + v * ROWS * kRowBytes, BM + j * 16 + n, h * 4 + g));
+            for (int j = 0; j < NT; ++j) {
+                char* at = mine + v * ROWS * kRowBytes;
+                if constexpr (TURNED)
+                    wf[j] = turned((const CGD_LDS(char)*)(at + BM * kRowBytes + turned_place(h * 32 + g * 8 + (n >> 2), j * 2 + (n >> 1 & 1)) + (n & 1) * 8),
+                                   4 * BN * 2);
+                else
+                    wf[j] = get16(turn_place(at, BM + j * 16 + n, h * 4 + g));
+            }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -361,7 +322,7 @@ __global__ __launch_bounds__(256, 3) void adapter_shrink_kernel(const ShrinkArgs
             for (int q = 0; q < 2 * MT; ++q) stage[0][q] = in ? *reinterpret_cast<const uint4*>(xp[q] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int q = 0; q < 2 * NT; ++q)
-                stage[0][2 * MT + q] = in ? *reinterpret_cast<const uint4*>(wp + (rank0 + q * 8 < s.rank ? q * next8 : 0) + k) : make_uint4(0, 0, 0, 0);
+                stage[0][2 * MT + q] = (TURNED ? k + q * WR + wr < span : in) ? *w_at(k, q) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int q = 0; q < 2 * (MT + NT); ++q) turn(0, q);
             __builtin_amdgcn_sched_barrier(0);
@@ -395,7 +356,7 @@ constexpr int kMostPieces = 16;  // of the first product's reduction
 struct ExpandArgs {
     const float* partial;    // [pieces][token in order][rank]
     int pieces;
-    const uint16_t* w;       // [adapters, out, rank]
+    const uint16_t* w;       // [adapters, width, rank]; TURNED: [adapters, rank, width]
     const float* scale;      // [adapters] or null
     const Tile* tiles;
     int64_t tokens, width, chunk;  // chunk: of the out features for one block, a multiple of 64 for each wave
@@ -413,7 +374,7 @@ struct ExpandArgs {
 // of memory, come in whole and are turned over in the wave's own LDS, the next F on
 // their way; so do the results, the other way round, so that neighbouring lanes
 // write one token's features.
-template <int MT, int KS>
+template <int MT, int KS, bool TURNED>
 __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(const ExpandArgs e) {
     constexpr int BM = 16 * MT, RANK = KS ? 32 * KS : 16, PITCH = RANK + 8, KN = KS ? KS : 1;
     constexpr int F = KS > 4 ? 32 : 64, FT = F / 16, OUT = F + 4, LOADS = F * RANK / 512;  // (a load: 1 KB)
@@ -427,26 +388,31 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
     if (group < 0) return;
     const bool none = group == e.adapters, whole = e.width % 8 == 0;
     const int64_t end = (int64_t)(blockIdx.y + 1) * e.chunk < e.width ? (int64_t)(blockIdx.y + 1) * e.chunk : e.width;
-    // b's rows, PR 16-byte pieces each in LDS (zeros past the rank): a load takes RPL of
-    // them, a lane the piece lp of row lane / PR; piece i lies at i ^ (i / 8 ^ i / 64) % 8
-    constexpr int PR = RANK / 8, RPL = kWave / PR;
+    // w in LDS: rows of PR 16-byte pieces, RPL of them a load, the lane piece lp of row
+    // lane / PR. A row is a feature's ranks (zeros past the rank; piece i of all lies at
+    // i ^ (i / 8 ^ i / 64) % 8) or, TURNED, a rank's features, where the transposing read
+    // takes 32 bytes of each of four rows at a time.
+    constexpr int PR = TURNED ? F / 8 : RANK / 8, RPL = kWave / PR;
     const int lr = lane / PR, lp = lane % PR;
-    const bool held = lp * 8 < e.rank;
-    const uint16_t* const wp = e.w + ((int64_t)group * e.width + lr) * e.rank + lp * 8;
+    const int64_t pitch = TURNED ? e.width : e.rank;
+    const uint16_t* const wp = e.w + (int64_t)group * e.width * e.rank + lr * pitch + lp * 8;
     uint4 stage[LOADS];
     auto load = [&](int64_t o0) {
-        const uint16_t* from = wp + o0 * e.rank;
-        const int64_t next = (int64_t)RPL * e.rank;
-        if (o0 + F <= e.width) {
+        const uint16_t* from = wp + (TURNED ? o0 : o0 * e.rank);
+        const int64_t next = RPL * pitch;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) stage[i] = held ? *reinterpret_cast<const uint4*>(from + i * next) : make_uint4(0, 0, 0, 0);
-        } else {
-#pragma unroll
-            for (int i = 0; i < LOADS; ++i)
-                stage[i] = held && o0 + i * RPL + lr < e.width ? *reinterpret_cast<const uint4*>(from + i * next) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < LOADS; ++i) {
+            const bool in = TURNED ? i * RPL + lr < e.rank && o0 + lp * 8 < e.width : lp * 8 < e.rank && o0 + i * RPL + lr < e.width;
+            stage[i] = in ? *reinterpret_cast<const uint4*>(from + i * next) : make_uint4(0, 0, 0, 0);
         }
     };
-    auto place = [](int i) { return (i ^ (((i >> 3) ^ (i >> 6)) & 7)) * 16; };
+    auto place = [](int i) {
+        if constexpr (TURNED) {
+            const int row = i / PR;
+            return (i ^ ((row << 1 & 6) & (PR - 1))) * 16;
+        }
+        return (i ^ (((i >> 3) ^ (i >> 6)) & 7)) * 16;
+    };
     // the results' lanes: 8 features of token 64 * 8 / F * q + lane / (F / 8)
     constexpr int LR = F / 8, TOKENS = kWave / LR, Q = BM / TOKENS;
     const int rt = lane / LR, ro = lane % LR * 8;
@@ -534,8 +500,12 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
                 const int piece = KS ? k * 4 + g : g & 1;
                 bf16x8_t wf[FT];
 #pragma unroll
-                for (int p = 0; p < FT; ++p)
-                    wf[p] = get16(mine + place((p * 16 + n) * PR + piece));
+                for (int p = 0; p < FT; ++p) {
+                    if constexpr (TURNED)
+                        wf[p] = turned((const CGD_LDS(char)*)(mine + place((piece * 8 + (n >> 2)) * PR + p * 2 + (n >> 1 & 1)) + (n & 1) * 8), 4 * F * 2);
+                    else
+                        wf[p] = get16(mine + place((p * 16 + n) * PR + piece));
+                }
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     if constexpr (KS > 0) {
@@ -634,28 +604,48 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < 8; ++c) acc[r][c] = float4_t{0.f, 0.f, 0.f, 0.f};
-    for (int p0 = begin + wave * 32; p0 < end; p0 += NW * 32) {
-        const int p = p0 + g * 8;
+    // 32 tokens on their way: past the last one it is loaded again, and nothing of it multiplied
+    struct Step {
         uint4 row[8];
+        float v[RT][8];
+    };
+    const uint16_t* const from = wide + (col < width ? col : 0);
+    int rank_at[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) rank_at[r] = rank0 + r * 16 + n < w.rank ? rank0 + r * 16 + n : w.rank - 1;
+    auto load = [&](Step& s, int p0) {
+        const int p = p0 + g * 8;
         int token[8];
+        if (p0 + 32 <= end) {
+            __builtin_memcpy(token, w.order + p, sizeof(token));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) token[i] = p + i < end ? w.order[p + i] : -1;
+            for (int i = 0; i < 8; ++i) token[i] = w.order[p + i < end ? p + i : end - 1];
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            row[i] = token[i] >= 0 && col < width ? *reinterpret_cast<const uint4*>(wide + token[i] * width + col) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < 8; ++i) s.row[i] = *reinterpret_cast<const uint4*>(from + token[i] * width);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float* at = thin + (int64_t)(!is_a ? token[i] : p + i < end ? p + i : end - 1) * w.rank;
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s.v[r][i] = at[rank_at[r]];
+        }
+    };
+    auto multiply = [&](Step& s, int p0) {
+        if (p0 + 32 > end)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p0 + g * 8 + i >= end) {
+                    s.row[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) s.v[r][i] = 0.0f;
+                }
         bf16x8_t hi[RT], lo[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const int k = rank0 + r * 16 + n;
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int64_t at = is_a ? p + i : token[i];
-                v[i] = token[i] >= 0 && k < w.rank ? thin[at * w.rank + k] * scale : 0.0f;
-            }
             uint32_t h[4], l[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) halves2(v[2 * i], v[2 * i + 1], &h[i], &l[i]);
+            for (int i = 0; i < 4; ++i) halves2(s.v[r][2 * i] * scale, s.v[r][2 * i + 1] * scale, &h[i], &l[i]);
             hi[r] = __builtin_bit_cast(bf16x8_t, uint4_t{h[0], h[1], h[2], h[3]});
             lo[r] = __builtin_bit_cast(bf16x8_t, uint4_t{l[0], l[1], l[2], l[3]});
         }
@@ -664,13 +654,18 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
             uint32_t q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t a = reinterpret_cast<const uint32_t*>(&row[2 * i])[c / 2], b = reinterpret_cast<const uint32_t*>(&row[2 * i + 1])[c / 2];
-                q[i] = c & 1 ? (a >> 16) | (b & 0xFFFF0000u) : (a & 0xFFFFu) | (b << 16);
+                const uint32_t lower = reinterpret_cast<const uint32_t*>(&s.row[2 * i])[c / 2], upper = reinterpret_cast<const uint32_t*>(&s.row[2 * i + 1])[c / 2];
+                q[i] = c & 1 ? (lower >> 16) | (upper & 0xFFFF0000u) : (lower & 0xFFFFu) | (upper << 16);
             }
             const bf16x8_t f = __builtin_bit_cast(bf16x8_t, uint4_t{q[0], q[1], q[2], q[3]});
 #pragma unroll
             for (int r = 0; r < RT; ++r) acc[r][c] = mul16(lo[r], f, mul16(hi[r], f, acc[r][c]));
         }
+    };
+    Step s;
+    for (int p0 = begin + wave * 32; p0 < end; p0 += NW * 32) {
+        load(s, p0);
+        multiply(s, p0);
     }
     // the upper half of the waves that had tokens gives its sums to the lower, until one has them
     const int most = (end - begin + 31) / 32;
@@ -715,7 +710,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Room {  // places in the workspace
-    size_t offset, order, tiles, partial, scaled, turned_a, turned_b, bytes;
+    size_t offset, order, tiles, partial, scaled, bytes;
 };
 
 bool few(int64_t tokens) { return tokens <= kFewTokens; }
@@ -744,45 +739,34 @@ Room room_for(int64_t tokens, int adapters, int rank, int64_t in, int64_t out, b
     r.tiles = r.order + padded((size_t)tokens * 4);
     r.partial = r.tiles + padded((size_t)tile_slots(tokens, adapters) * sizeof(Tile));
     r.scaled = r.partial + padded((size_t)piece_count(tokens, rank, grad ? out : in) * tokens * rank * 4);
-    r.turned_a = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
-    r.turned_b = r.turned_a + (grad ? padded((size_t)adapters * rank * in * 2) : 0);
-    r.bytes = r.turned_b + (grad ? padded((size_t)adapters * rank * out * 2) : 0);
+    r.bytes = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
     return r;
 }
 
-hipError_t plan(const PlanArgs& p, hipStream_t stream) {
-    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)(p.adapters + 1 + (p.squares + 3) / 4)), dim3(kPlanThreads), 0, stream, p);
+hipError_t plan(const int64_t* index, int64_t tokens, int adapters, int32_t* offset, int32_t* order, Tile* tiles, hipStream_t stream) {
+    hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)adapters + 1), dim3(kPlanThreads), 0, stream, index, (int)tokens, adapters, offset,
+                       order, tiles, tile_tokens(tokens));
     return hipGetLastError();
 }
 
 // own_plan: few tokens, and the kernel makes the tiles itself.
-hipError_t shrink(const ShrinkArgs& s, bool own_plan, hipStream_t stream) {
+template <int MT, bool FEW, bool TURNED>
+void shrink_rank(const ShrinkArgs& s, hipStream_t stream) {
     const int nt = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : 4;
     const dim3 grid((unsigned)tile_slots(s.tokens, s.adapters), (unsigned)((s.in + s.piece - 1) / s.piece), (unsigned)((s.rank + 16 * nt - 1) / (16 * nt)));
-#define CGD_SHRINK(M, N, F) hipLaunchKernelGGL((adapter_shrink_kernel<M, N, (M + N <= 3 ? 2 : 1), F>), grid, dim3(256), 0, stream, s)
-#define CGD_SHRINK_RANK(M, F)  \
-    do {                       \
-        if (nt == 1)           \
-            CGD_SHRINK(M, 1, F); \
-        else if (nt == 2)      \
-            CGD_SHRINK(M, 2, F); \
-        else                   \
-            CGD_SHRINK(M, 4, F); \
-    } while (0)
-    if (own_plan)
-        CGD_SHRINK_RANK(1, true);
-    else if (tile_tokens(s.tokens) == kTile)
-        CGD_SHRINK_RANK(1, false);
+#define CGD_SHRINK(N) hipLaunchKernelGGL((adapter_shrink_kernel<MT, N, (MT + N <= 3 ? 2 : 1), FEW, TURNED>), grid, dim3(256), 0, stream, s)
+    if (nt == 1)
+        CGD_SHRINK(1);
+    else if (nt == 2)
+        CGD_SHRINK(2);
     else
-        CGD_SHRINK_RANK(2, false);
-#undef CGD_SHRINK_RANK
+        CGD_SHRINK(4);
 #undef CGD_SHRINK
-    return hipGetLastError();
 }
 
-template <int MT>
+template <int MT, bool TURNED>
 void expand_rank(const ExpandArgs& e, const dim3& grid, hipStream_t stream) {
-#define CGD_EXPAND(K) hipLaunchKernelGGL((adapter_expand_kernel<MT, K>), grid, dim3(256), 0, stream, e)
+#define CGD_EXPAND(K) hipLaunchKernelGGL((adapter_expand_kernel<MT, K, TURNED>), grid, dim3(256), 0, stream, e)
     if (e.rank <= 16)
         CGD_EXPAND(0);
     else if (e.rank <= 32)
@@ -796,8 +780,8 @@ void expand_rank(const ExpandArgs& e, const dim3& grid, hipStream_t stream) {
 #undef CGD_EXPAND
 }
 
-hipError_t expand(const ExpandArgs& in, hipStream_t stream) {
-    ExpandArgs e = in;
+template <bool TURNED>
+void expand(ExpandArgs e, hipStream_t stream) {
     const int tile = tile_tokens(e.tokens), step = e.rank <= 128 ? 256 : 128;  // features of a block's waves at a time
     const int64_t tiles = (e.tokens + tile - 1) / tile, steps = e.out ? (e.width + step - 1) / step : 1;
     int64_t chunks = ((e.rank > 32 ? 384 : 640) + tiles - 1) / tiles;
@@ -805,18 +789,27 @@ hipError_t expand(const ExpandArgs& in, hipStream_t stream) {
     e.chunk = (steps + chunks - 1) / chunks * step;
     const dim3 grid((unsigned)tile_slots(e.tokens, e.adapters), (unsigned)((steps * step + e.chunk - 1) / e.chunk));
     if (tile == kTile)
-        expand_rank<1>(e, grid, stream);
+        expand_rank<1, TURNED>(e, grid, stream);
     else
-        expand_rank<2>(e, grid, stream);
-    return hipGetLastError();
+        expand_rank<2, TURNED>(e, grid, stream);
 }
 
-// The two products; the pieces of the first are set here.
-hipError_t products(ShrinkArgs s, ExpandArgs e, bool own_plan, hipStream_t stream) {
+// The two products; the pieces of the first are set here. TURNED: backwards, where
+// each weight is the other product's.
+template <bool TURNED>
+hipError_t products(ShrinkArgs s, ExpandArgs e, hipStream_t stream) {
     s.piece = shrink_piece(s.tokens, s.rank, s.in);
     e.pieces = (int)((s.in + s.piece - 1) / s.piece);
-    const hipError_t err = shrink(s, own_plan, stream);
-    return err == hipSuccess ? expand(e, stream) : err;
+    if (!TURNED && few(s.tokens))
+        shrink_rank<1, !TURNED, TURNED>(s, stream);
+    else if (tile_tokens(s.tokens) == kTile)
+        shrink_rank<1, false, TURNED>(s, stream);
+    else
+        shrink_rank<2, false, TURNED>(s, stream);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    expand<TURNED>(e, stream);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -832,18 +825,17 @@ hipError_t launch_adapters(const AdapterArgs& p, void* workspace, hipStream_t st
     if (p.tokens == 0) return hipSuccess;
     char* ws = static_cast<char*>(workspace);
     const Room room = room_for(p.tokens, p.adapters, p.rank, p.in, p.out_features, false);
-    const bool own_plan = few(p.tokens);
-    int32_t* offset = reinterpret_cast<int32_t*>(ws + room.offset);
-    int32_t* order = reinterpret_cast<int32_t*>(ws + room.order);
     Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
     float* partial = reinterpret_cast<float*>(ws + room.partial);
-    if (!own_plan) {
-        const hipError_t err = plan(PlanArgs{p.index, (int)p.tokens, p.adapters, offset, order, tiles, tile_tokens(p.tokens), nullptr, nullptr, nullptr, nullptr, 0, 0, 0, 0, 0}, stream);
+    if (!few(p.tokens)) {
+        const hipError_t err = plan(p.index, p.tokens, p.adapters, reinterpret_cast<int32_t*>(ws + room.offset),
+                                    reinterpret_cast<int32_t*>(ws + room.order), tiles, stream);
         if (err != hipSuccess) return err;
     }
-    return products(ShrinkArgs{p.x, p.a, p.index, tiles, p.tokens, p.in, 0, p.adapters, p.rank, partial},
-                    ExpandArgs{partial, 0, p.b, p.scale, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, p.residual, p.out, p.hidden, nullptr},
-                    own_plan, stream);
+    return products<false>(ShrinkArgs{p.x, p.a, p.index, tiles, p.tokens, p.in, 0, p.adapters, p.rank, partial},
+                           ExpandArgs{partial, 0, p.b, p.scale, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, p.residual, p.out,
+                                      p.hidden, nullptr},
+                           stream);
 }
 
 hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipStream_t stream) {
@@ -851,24 +843,16 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
     const Room room = room_for(p.tokens, p.adapters, p.rank, p.in, p.out_features, true);
     int32_t* offset = reinterpret_cast<int32_t*>(ws + room.offset);
     int32_t* order = reinterpret_cast<int32_t*>(ws + room.order);
+    Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
     float* partial = reinterpret_cast<float*>(ws + room.partial);
     float* scaled = reinterpret_cast<float*>(ws + room.scaled);
-    Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
-    uint16_t* at = reinterpret_cast<uint16_t*>(ws + room.turned_a);
-    uint16_t* bt = reinterpret_cast<uint16_t*>(ws + room.turned_b);
-    const bool through = p.tokens && (p.grad_x || p.grad_a);  // gh is needed
-    const int64_t down = (p.rank + 63) / 64;
-    const int64_t a_squares = through && p.grad_x ? p.adapters * down * ((p.in + 63) / 64) : 0;
-    const int64_t b_squares = through ? p.adapters * down * ((p.out_features + 63) / 64) : 0;
-    hipError_t err = plan(PlanArgs{p.index, (int)p.tokens, p.adapters, offset, order, tiles, tile_tokens(p.tokens), p.a, p.b, at, bt, p.in, p.out_features, p.rank, a_squares,
-                                   a_squares + b_squares},
-                          stream);
+    hipError_t err = plan(p.index, p.tokens, p.adapters, offset, order, tiles, stream);
     if (err != hipSuccess) return err;
-    if (through) {
-        err = products(ShrinkArgs{p.grad, bt, p.index, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, partial},
-                       ExpandArgs{partial, 0, at, p.scale, tiles, p.tokens, p.in, 0, p.adapters, p.rank, nullptr, p.grad_x, nullptr,
-                                  p.grad_a ? scaled : nullptr},
-                       false, stream);
+    if (p.tokens && (p.grad_x || p.grad_a)) {
+        err = products<true>(ShrinkArgs{p.grad, p.b, p.index, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, partial},
+                             ExpandArgs{partial, 0, p.a, p.scale, tiles, p.tokens, p.in, 0, p.adapters, p.rank, nullptr, p.grad_x, nullptr,
+                                        p.grad_a ? scaled : nullptr},
+                             stream);
         if (err != hipSuccess) return err;
     }
     if (p.grad_a || p.grad_b) {
@@ -878,10 +862,18 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
 #define CGD_WEIGHTS(RT, NW)                                                                                                    \
     hipLaunchKernelGGL((adapter_weight_kernel<RT, NW>), dim3((unsigned)blocks, (unsigned)p.adapters, (unsigned)((p.rank + 16 * RT - 1) / (16 * RT))), \
                        dim3(NW* kWave), (size_t)NW / 2 * RT * 8 * kWave * 16, stream, w)
-        if (p.rank <= 16)
-            CGD_WEIGHTS(1, 8);
-        else
+        // More waves where an adapter has many tokens. Rank 16, 4095 tokens, 4096 -> 7168, us with
+        // 4, 8 and 16 waves: 16 adapters 26 29 32, four 27 25 24, one 62 49 37; rank 64 with 4 and 8:
+        // 16 adapters 45 64, one 64 48.
+        const bool many = p.tokens >= int64_t(768) * p.adapters;
+        if (p.rank <= 16 && many)
+            CGD_WEIGHTS(1, 16);
+        else if (p.rank <= 16)
+            CGD_WEIGHTS(1, 4);
+        else if (many)
             CGD_WEIGHTS(2, 8);
+        else
+            CGD_WEIGHTS(2, 4);
 #undef CGD_WEIGHTS
         err = hipGetLastError();
     }
