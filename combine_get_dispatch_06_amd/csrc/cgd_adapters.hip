@@ -148,60 +148,73 @@ struct ShrinkArgs {
     float* partial;          // [pieces][token in order][rank]
 };
 
-// Tile `want` of at most kFewTokens tokens, by the first wave of every block for
-// itself: its lanes hold all tokens' groups, a ballot for 64 of them counts those
-// before a group, and as the groups' first slots ascend, ten such counts find the
-// slot's group among 512. Saves the plan's launch (4 us of a call with 128 tokens).
-constexpr int kFewTokens = 512;
+// At most kFewTokens tokens need no plan: a wave holds all their groups, and a ballot
+// for 64 of them counts those before a group. Saves the plan's launch: 4 us, for 2 more
+// of the first product with 128 tokens (and 5 with 512).
+constexpr int kFewTokens = 256;
 constexpr int kTile = 16;
-__device__ __forceinline__ void plan_few(const int64_t* index, int tokens, int adapters, int want, Tile& p) {
-    constexpr int CHUNKS = kFewTokens / kWave;
-    if (threadIdx.x < kWave) {
-        const int lane = lane_id();
-        int of[CHUNKS];
+struct FewTokens {
+    static constexpr int CHUNKS = kFewTokens / kWave;
+    int of[CHUNKS];
+    int tokens;
+    __device__ __forceinline__ FewTokens(const int64_t* index, int n, int adapters) : tokens(n) {
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             of[c] = INT32_MAX;
-            if (c * kWave + lane < tokens) {
-                const int64_t j = index[c * kWave + lane];
+            if (c * kWave + lane_id() < n) {
+                const int64_t j = index[c * kWave + lane_id()];
                 of[c] = j >= 0 && j < adapters ? (int)j : adapters;
             }
         }
-        auto before = [&](int group) {
-            int n = 0;
+    }
+    __device__ __forceinline__ int before(int group) const {
+        int n = 0;
 #pragma unroll
-            for (int c = 0; c < CHUNKS; ++c)
-                if (c * kWave < tokens) n += __popcll(ballot(of[c] < group));
-            return n;
-        };
-        int group = 0;  // the last one whose slots begin at `want` or before it
-        for (int hi = adapters; group < hi;) {
-            const int mid = (group + hi + 1) / 2;
-            if (before(mid) / kTile + mid <= want)
-                group = mid;
-            else
-                hi = mid - 1;
-        }
-        const int first = before(group), skip = (want - first / kTile - group) * kTile;
-        const int left = before(group + 1) - first - skip, rows = left < kTile ? left : kTile;
-        if (lane == 0) {
-            p.group = left > 0 ? group : -1;
-            p.row0 = first + skip;
-            p.rows = rows;
-        }
-        int seen = -skip;  // of the tile's tokens
+        for (int c = 0; c < CHUNKS; ++c)
+            if (c * kWave < tokens) n += __popcll(ballot(of[c] < group));
+        return n;
+    }
+    // to[i] = the group's token number skip + i, for i < rows; -> the last of them, in its lane (-1 elsewhere)
+    __device__ __forceinline__ int list(int group, int skip, int rows, int* to) const {
+        int seen = -skip, last = -1;
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             if (c * kWave >= tokens) break;
             const uint64_t hits = ballot(of[c] == group);
             const int at = seen + __popcll(hits & lanemask_lt());
             if (of[c] == group && at >= 0 && at < rows) {
-                p.token[at] = c * kWave + lane;
-                if (at == rows - 1)
-                    for (int k = rows; k < kTile; ++k) p.token[k] = c * kWave + lane;
+                to[at] = c * kWave + lane_id();
+                if (at == rows - 1) last = to[at];
             }
             seen += __popcll(hits);
         }
+        return last;
+    }
+};
+
+// Tile `want` of a few tokens, by the first wave of every block for itself: the groups'
+// first slots ascend, so ten counts find the slot's group among 512.
+__device__ __forceinline__ void plan_few(const int64_t* index, int tokens, int adapters, int want, Tile& p) {
+    if (threadIdx.x < kWave) {
+        const FewTokens t(index, tokens, adapters);
+        int group = 0;  // the last one whose slots begin at `want` or before it
+        for (int hi = adapters; group < hi;) {
+            const int mid = (group + hi + 1) / 2;
+            if (t.before(mid) / kTile + mid <= want)
+                group = mid;
+            else
+                hi = mid - 1;
+        }
+        const int first = t.before(group), skip = (want - first / kTile - group) * kTile;
+        const int left = t.before(group + 1) - first - skip, rows = left < kTile ? left : kTile;
+        if (lane_id() == 0) {
+            p.group = left > 0 ? group : -1;
+            p.row0 = first + skip;
+            p.rows = rows;
+        }
+        const int last = t.list(group, skip, rows, p.token);
+        if (last >= 0)
+            for (int k = rows; k < kTile; ++k) p.token[k] = last;
     }
     __syncthreads();
 }
@@ -572,6 +585,8 @@ struct AdapterWeightArgs {
     const float* scaled;    // gh [token in order][rank]
     const float* hidden;    // [token][rank]
     const float* scale;
+    const int64_t* index;   // few tokens: the kernel finds its own
+    int tokens;
     const int32_t* offset;
     const int32_t* order;
     int64_t in, out;
@@ -587,9 +602,10 @@ struct AdapterWeightArgs {
 // eight tokens of one column in a lane: a lane loads eight columns of eight
 // tokens, 16 bytes each, and turns that square over in its own registers; the
 // eight matrix tiles it makes have every eighth column each.
-template <int RT, int NW>
+template <int RT, int NW, bool FEW>
 __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const AdapterWeightArgs w) {
     extern __shared__ __attribute__((aligned(16))) float4_t joined[];  // [wave][RT * 8][lane]
+    __shared__ int own[FEW ? kFewTokens : 1], bounds[2];
     const int lane = lane_id(), wave = threadIdx.x / kWave, n = lane & 15, g = lane >> 4;
     const bool is_a = (int)blockIdx.x < w.a_blocks;
     const int64_t width = is_a ? w.in : w.out;
@@ -597,7 +613,20 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
     const uint16_t* wide = is_a ? w.x : w.grad;
     const float* thin = is_a ? w.scaled : w.hidden;
     const int j = blockIdx.y, rank0 = blockIdx.z * 16 * RT;
-    const int begin = w.offset[j], end = w.offset[j + 1];
+    if constexpr (FEW) {
+        if (wave == 0) {
+            const FewTokens t(w.index, w.tokens, w.adapters);
+            const int first = t.before(j), n = t.before(j + 1) - first;
+            t.list(j, 0, n, own);
+            if (lane == 0) {
+                bounds[0] = first;
+                bounds[1] = first + n;
+            }
+        }
+        __syncthreads();
+    }
+    const int begin = FEW ? bounds[0] : w.offset[j], end = FEW ? bounds[1] : w.offset[j + 1];
+    const int* const order = FEW ? own : w.order + begin;  // of the adapter's tokens
     const float scale = !is_a && w.scale ? w.scale[j] : 1.0f;
     float4_t acc[RT][8];
 #pragma unroll
@@ -617,10 +646,10 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
         const int p = p0 + g * 8;
         int token[8];
         if (p0 + 32 <= end) {
-            __builtin_memcpy(token, w.order + p, sizeof(token));
+            __builtin_memcpy(token, order + (p - begin), sizeof(token));
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) token[i] = w.order[p + i < end ? p + i : end - 1];
+            for (int i = 0; i < 8; ++i) token[i] = order[(p + i < end ? p + i : end - 1) - begin];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) s.row[i] = *reinterpret_cast<const uint4*>(from + token[i] * width);
@@ -800,8 +829,8 @@ template <bool TURNED>
 hipError_t products(ShrinkArgs s, ExpandArgs e, hipStream_t stream) {
     s.piece = shrink_piece(s.tokens, s.rank, s.in);
     e.pieces = (int)((s.in + s.piece - 1) / s.piece);
-    if (!TURNED && few(s.tokens))
-        shrink_rank<1, !TURNED, TURNED>(s, stream);
+    if (few(s.tokens))
+        shrink_rank<1, true, TURNED>(s, stream);
     else if (tile_tokens(s.tokens) == kTile)
         shrink_rank<1, false, TURNED>(s, stream);
     else
@@ -846,7 +875,8 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
     Tile* tiles = reinterpret_cast<Tile*>(ws + room.tiles);
     float* partial = reinterpret_cast<float*>(ws + room.partial);
     float* scaled = reinterpret_cast<float*>(ws + room.scaled);
-    hipError_t err = plan(p.index, p.tokens, p.adapters, offset, order, tiles, stream);
+    hipError_t err = hipSuccess;
+    if (!few(p.tokens)) err = plan(p.index, p.tokens, p.adapters, offset, order, tiles, stream);
     if (err != hipSuccess) return err;
     if (p.tokens && (p.grad_x || p.grad_a)) {
         err = products<true>(ShrinkArgs{p.grad, p.b, p.index, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, partial},
@@ -856,24 +886,28 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
         if (err != hipSuccess) return err;
     }
     if (p.grad_a || p.grad_b) {
-        AdapterWeightArgs w{p.x, p.grad, scaled, p.hidden, p.scale, offset, order, p.in, p.out_features, p.adapters, p.rank, 0, p.grad_a, p.grad_b};
+        AdapterWeightArgs w{p.x, p.grad, scaled, p.hidden, p.scale, p.index, (int)p.tokens, offset, order, p.in, p.out_features, p.adapters, p.rank, 0, p.grad_a, p.grad_b};
         w.a_blocks = p.grad_a ? (int)((p.in + 127) / 128) : 0;
         const int blocks = w.a_blocks + (p.grad_b ? (int)((p.out_features + 127) / 128) : 0);
-#define CGD_WEIGHTS(RT, NW)                                                                                                    \
-    hipLaunchKernelGGL((adapter_weight_kernel<RT, NW>), dim3((unsigned)blocks, (unsigned)p.adapters, (unsigned)((p.rank + 16 * RT - 1) / (16 * RT))), \
+#define CGD_WEIGHTS(RT, NW, FEW)                                                                                                    \
+    hipLaunchKernelGGL((adapter_weight_kernel<RT, NW, FEW>), dim3((unsigned)blocks, (unsigned)p.adapters, (unsigned)((p.rank + 16 * RT - 1) / (16 * RT))), \
                        dim3(NW* kWave), (size_t)NW / 2 * RT * 8 * kWave * 16, stream, w)
         // More waves where an adapter has many tokens. Rank 16, 4095 tokens, 4096 -> 7168, us with
         // 4, 8 and 16 waves: 16 adapters 26 29 32, four 27 25 24, one 62 49 37; rank 64 with 4 and 8:
         // 16 adapters 45 64, one 64 48.
         const bool many = p.tokens >= int64_t(768) * p.adapters;
-        if (p.rank <= 16 && many)
-            CGD_WEIGHTS(1, 16);
+        if (few(p.tokens) && p.rank <= 16)
+            CGD_WEIGHTS(1, 4, true);
+        else if (few(p.tokens))
+            CGD_WEIGHTS(2, 4, true);
+        else if (p.rank <= 16 && many)
+            CGD_WEIGHTS(1, 16, false);
         else if (p.rank <= 16)
-            CGD_WEIGHTS(1, 4);
+            CGD_WEIGHTS(1, 4, false);
         else if (many)
-            CGD_WEIGHTS(2, 8);
+            CGD_WEIGHTS(2, 8, false);
         else
-            CGD_WEIGHTS(2, 4);
+            CGD_WEIGHTS(2, 4, false);
 #undef CGD_WEIGHTS
         err = hipGetLastError();
     }

@@ -26,9 +26,9 @@ extern "C" {
  *   codes, scales FP8 e4m3 [num_rows, hidden] and [num_rows, hidden / 128] (fp32, or UE8M0 bytes for
  *                 scale_format 2) out, or NULL: y as cgd_cast_to_fp8 encodes it, but from fp32 values
  *   sum           bf16 [num_rows, hidden] out or NULL: s rounded (y is made from s before that)
- * At least one of y and codes. sum may be x or residual itself, y may be x (or residual, unless sum
- * is); the outputs share no other memory. hidden: a multiple of 8 (FP8: of 128) up to 32768. A row
- * whose squares add up to more than fp32 holds gives zeros. All but scales 16-byte aligned. */
+ * At least one of y and codes. sum may be x or residual itself; the outputs share no other memory.
+ * hidden: a multiple of 8 (FP8: of 128) up to 32768. A finite row whose squares add up to more than
+ * fp32 holds gives zeros. All but scales 16-byte aligned. */
 int cgd_rms_norm(const void* x, const void* residual, const void* weight, int weight_type, float eps, int64_t num_rows,
                  int hidden, void* y, void* codes, void* scales, int scale_format, void* sum, hipStream_t stream);
 
@@ -36,7 +36,7 @@ int cgd_rms_norm(const void* x, const void* residual, const void* weight, int we
  * of both):
  *   grad_y        bf16 [num_rows, hidden]
  *   grad_sum      bf16 [num_rows, hidden] or NULL: what reaches the sum on another way, added
- *   grad_x        bf16 [num_rows, hidden] out or NULL; may be grad_y or grad_sum itself
+ *   grad_x        bf16 [num_rows, hidden] out or NULL
  *   grad_weight   [hidden] of weight_type out or NULL, which needs the workspace */
 size_t cgd_rms_norm_backward_workspace_bytes(int64_t num_rows, int hidden);
 int cgd_rms_norm_backward(const void* grad_y, const void* x, const void* weight, int weight_type, float eps,

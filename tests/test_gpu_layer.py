@@ -168,6 +168,8 @@ def test_norm_special_values():
         x[2] = 0
         x[4, H // 2] = float("nan")
         x[6, 3] = float("inf")
+        big = torch.full((1, H), 1e30, dtype=BF16, device=DEV)  # its squares are more than float32 holds
+        assert (cgd.rms_norm(big, _dev(w)) == 0).all()
         y = cgd.rms_norm(_dev(x), _dev(w)).cpu()
         _, y64, _, ty = _norm64(x, None, w, 1e-6)
         ok = [0, 1, 2, 3, 5, 7]
@@ -258,7 +260,8 @@ SHAPES = [  # T, J, R, I, O, none, runs
     (1, 1, 8, 8, 1, 0.0, 0), (1, 5, 64, 4096, 7168, 0.0, 0), (2, 3, 16, 72, 24, 0.0, 0), (16, 1, 8, 264, 130, 0.0, 0),
     (17, 4, 24, 320, 63, 0.3, 0), (31, 2, 16, 1000, 257, 0.0, 1), (64, 64, 32, 512, 512, 0.1, 0),
     (128, 32, 16, 7168, 256, 0.1, 0), (100, 512, 8, 128, 96, 0.0, 0), (130, 3, 40, 640, 320, 0.5, 7),
-    (300, 8, 64, 1032, 515, 0.1, 9), (513, 2, 128, 264, 264, 0.0, 3), (600, 5, 72, 136, 1003, 0.2, 0),
+    (255, 20, 24, 136, 264, 0.2, 0), (256, 300, 16, 264, 72, 0.1, 0), (256, 2, 32, 128, 128, 0.0, 2), (257, 9, 8, 72, 136, 0.1, 0),
+    (1023, 3, 16, 136, 64, 0.1, 8), (1024, 40, 32, 64, 200, 0.0, 0), (300, 8, 64, 1032, 515, 0.1, 9), (513, 2, 128, 264, 264, 0.0, 3), (600, 5, 72, 136, 1003, 0.2, 0),
     (1030, 7, 16, 2304, 136, 0.1, 0), (1500, 1, 256, 256, 300, 0.0, 1), (2100, 16, 32, 200, 520, 0.05, 30),
     (2500, 3, 136, 328, 72, 0.1, 5), (4093, 8, 64, 448, 264, 0.1, 24)]
 
