@@ -8,9 +8,11 @@
 // rank is some 8 to 256: what bounds them is reading x and writing out once, so the
 // reduction over in_features and the out features are split until the CUs are busy,
 // and loads and stores take 128 bytes of a row at a time.
-// 4093 tokens of 24 requests, rank 64, 7168 -> 4096 with a residual: order 5.7 us, first
-// product 21 (2.8 TB/s), second 25 (2.7 TB/s). Operands loaded the way the matrix
-// instructions want them: 37 and 40; both products in one kernel like that: 73 and more.
+// 4093 tokens of 24 requests, rank 64, 7168 -> 4096 with a residual: order 5.9 us, first
+// product 21 (59 MB of x: 2.8 TB/s), second 26 (67 MB of residual and out: 2.6 TB/s).
+// Operands loaded the way the matrix instructions want them: 37 and 40; both products in
+// one kernel like that: 73 and more. Tiles of one adapter on one XCD, so that its weights
+// come into one L2: 1 us less for the first product, none for the second.
 // h and gh are fp32 sums; as operands of the second product they go in as two
 // bf16 parts (v = hi + lo, off by 2^-16 of v at most), which costs matrix
 // instructions that nothing waits for: results are rounded once.
@@ -602,6 +604,10 @@ struct AdapterWeightArgs {
 // eight tokens of one column in a lane: a lane loads eight columns of eight
 // tokens, 16 bytes each, and turns that square over in its own registers; the
 // eight matrix tiles it makes have every eighth column each.
+// 4095 tokens of 16 adapters, rank 16, 4096 -> 7168: 23 us for 94 MB (4.1 TB/s); grad_a
+// alone takes 15, the chain of a block's waits (its adapter's offset, the order, rows,
+// join). The next tokens on their way, at half as many waves: 23.6; grad_b's blocks in
+// the first product's launch: 42 for both and grad_a, where they take 38 one by one.
 template <int RT, int NW, bool FEW>
 __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const AdapterWeightArgs w) {
     extern __shared__ __attribute__((aligned(16))) float4_t joined[];  // [wave][RT * 8][lane]

@@ -6,7 +6,7 @@
 // wave. The token's gradient row is read by all waves of the block and comes from
 // the caches after the first. Slots without a row have a gradient of 0; rows that
 // no slot names are left as they were.
-// 4096 tokens, top-8, hidden 7168: 189 us for 1.0 GB (5.3 TB/s): what the row copy and
+// 4096 tokens, top-8, hidden 7168: 190 us for 1.0 GB (5.3 TB/s): what the row copy and
 // the combine take together on these rows (98 and 88). In the rows' own order instead,
 // every slot reads the token's gradient once more from the Infinity Cache: 195.
 #include "cgd_device.h"

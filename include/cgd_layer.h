@@ -87,8 +87,9 @@ int cgd_dropout(const void* x, const void* residual, int64_t num_elements, doubl
 /* Gradient of cgd_combine: for every slot (t, k) whose dst_row is a receive row,
  *   grad_expert_out[dst_row] = topk_weights[t, k] * grad_out[t]   (bf16 [recv_capacity, hidden])
  *   grad_topk_weights[t, k]  = <grad_out[t], expert_out[dst_row]> (fp32; 0 for other slots)
- * Receive rows that no slot names are left as they were. grad_expert_out shares no memory with an
- * input. (The gradient of a dispatch is cgd_combine with weights of 1.) */
+ * Receive rows that no slot names are left as they were; no two slots name one row (a dispatch gives
+ * each its own). grad_expert_out shares no memory with an input. (The gradient of a dispatch is
+ * cgd_combine with weights of 1.) */
 int cgd_combine_backward(const void* grad_out, const void* expert_out, int64_t recv_capacity, int hidden,
                          const int32_t* dst_row, const float* topk_weights, int64_t num_tokens, int num_topk,
                          void* grad_expert_out, float* grad_topk_weights, hipStream_t stream);
