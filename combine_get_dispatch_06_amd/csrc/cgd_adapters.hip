@@ -483,7 +483,8 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
         const int r = item_row(i), c = item_column(i);
         if (r >= BM) break;  // (a small tile of a small rank has fewer values than threads)
         const bool in = r < rows && c < e.rank;
-        const float4_t v = in ? sum[i] : float4_t{0.f, 0.f, 0.f, 0.f}, k = v * scale;
+        // (nothing times an infinite scale would be NaN in every feature)
+        const float4_t v = in ? sum[i] : float4_t{0.f, 0.f, 0.f, 0.f}, k = in ? v * scale : v;
         if (in && blockIdx.y == 0) {
             if (e.hidden) *reinterpret_cast<float4_t*>(e.hidden + (int64_t)tile->token[r] * e.rank + c) = v;
             if (e.scaled) *reinterpret_cast<float4_t*>(e.scaled + (int64_t)(row0 + r) * e.rank + c) = k;
@@ -667,6 +668,10 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
         }
     };
     auto multiply = [&](Step& s, int p0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) s.v[r][i] *= scale;
         if (p0 + 32 > end)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -680,7 +685,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
         for (int r = 0; r < RT; ++r) {
             uint32_t h[4], l[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) halves2(s.v[r][2 * i] * scale, s.v[r][2 * i + 1] * scale, &h[i], &l[i]);
+            for (int i = 0; i < 4; ++i) halves2(s.v[r][2 * i], s.v[r][2 * i + 1], &h[i], &l[i]);
             hi[r] = __builtin_bit_cast(bf16x8_t, uint4_t{h[0], h[1], h[2], h[3]});
             lo[r] = __builtin_bit_cast(bf16x8_t, uint4_t{l[0], l[1], l[2], l[3]});
         }

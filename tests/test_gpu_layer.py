@@ -371,6 +371,31 @@ def test_adapters_special_values():
     assert gx.isfinite().all() and ga.isfinite().all() and gb.isfinite().all()
 
 
+@pytest.mark.parametrize("T,R", [(5, 8), (5, 40), (100, 16), (300, 24), (1100, 8), (1100, 72), (4000, 8)])
+def test_adapters_infinite_scale(T, R):
+    """Of positive values an infinite scale makes infinities and no NaN: what a tile is
+    padded with does not meet it. An adapter without tokens has zero gradients all the same."""
+    g = _gen(12)
+    pos = lambda *shape: _dev((torch.rand(shape, generator=g) + 0.5).to(BF16))
+    x, a, b, grad, res = pos(T, 136), pos(3, R, 136), pos(3, 72, R), pos(T, 72), pos(T, 72)
+    idx = torch.randint(2, (T,), generator=g)
+    idx[0] = 0
+    idx[3] = -1
+    idx, inf = _dev(idx), float("inf")
+    runs = []
+    for scale in ([inf, 0.5, inf], [1.0, 0.5, 1.0]):
+        scale = torch.tensor(scale, device=DEV)
+        out, hidden = cgd.adapter_linear(x, a, b, idx, scale=scale, residual=res, return_hidden=True)
+        runs.append((out, hidden, *cgd.adapter_linear_backward(grad, x, a, b, idx, hidden, scale=scale)))
+    (out, hidden, gx, ga, gb), (out1, hidden1, gx1, ga1, gb1) = runs
+    first = idx == 0
+    assert torch.equal(hidden, hidden1) and hidden.isfinite().all()
+    assert (out[first] == inf).all() and torch.equal(out[~first], out1[~first])
+    assert (gx[first] == inf).all() and torch.equal(gx[~first], gx1[~first])
+    assert (ga[0] == inf).all() and torch.equal(ga[1:], ga1[1:])
+    assert (gb[0] == inf).all() and torch.equal(gb[1:], gb1[1:])
+
+
 # ---------------------------------------------------------------------------
 # Dropout
 # ---------------------------------------------------------------------------
