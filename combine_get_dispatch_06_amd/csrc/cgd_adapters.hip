@@ -61,7 +61,7 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kWave;
 constexpr int kPlanKept = 8;  // tokens of a lane whose groups stay in registers between the two passes
 
-// Block g finds the tokens of adapter g (g = adapters: those without one): how
+// Up to kLongPlan tokens: block g finds those of adapter g (g = adapters: of none): how
 // many come before them, and in a second pass their places. No block waits for
 // another. Each wave has a run of tokens, so the order within a group is the
 // tokens' own.
@@ -136,6 +136,160 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int64_
                                                                     int32_t* order, Tile* tiles, int tile) {
     __shared__ int32_t less_of[kPlanWaves], same_of[kPlanWaves];
     plan_group(index, tokens, adapters, blockIdx.x, offset, order, tiles, tile, less_of, same_of);
+}
+
+// Many tokens go in chunks, a block each: the tokens of every group in a chunk are
+// counted, the counts added up over the chunks, and every chunk places its own. The
+// groups' blocks above all read all tokens: us with these and with chunks, 8192 tokens
+// of 64 adapters 6.8 and 12, 16384 13 and 12, 65536 43 and 13; 2^18 of 512 194 and 22.
+// Chunks of 1024 take 17, 16 and 23 for the last three.
+constexpr int64_t kLongPlan = 16384;
+constexpr int kChunkThreads = 256, kChunkKept = 2, kChunkWaves = kChunkThreads / kWave, kChunk = kChunkThreads * kChunkKept;
+constexpr int kMostGroups = 513;  // the adapters', and that of none
+struct ChunkArgs {
+    const int64_t* index;
+    int tokens, adapters, chunks, tile;
+    int32_t* counts;  // [chunks + 1][groups]: of the chunk; then: of those before it, and (last) of all
+    int32_t* offset;
+    int32_t* order;
+    Tile* tiles;
+};
+
+// A chunk's tokens: their groups, and how many of the same wave and group come before
+// each. count: [wave][group] of the block, the waves' counts then.
+struct ChunkTokens {
+    int group[kChunkKept], rank[kChunkKept], t0;
+    __device__ __forceinline__ ChunkTokens(const ChunkArgs& p, volatile int32_t (*count)[kMostGroups]) {
+        const int wave = threadIdx.x / kWave;
+        t0 = blockIdx.x * kChunk + wave * (kChunk / kChunkWaves) + lane_id();
+#pragma unroll
+        for (int u = 0; u < kChunkKept; ++u) {
+            group[u] = 1023;  // no token
+            if (t0 + u * kWave < p.tokens) {
+                const int64_t j = p.index[t0 + u * kWave];
+                group[u] = j >= 0 && j < p.adapters ? (int)j : p.adapters;
+            }
+        }
+        for (int i = lane_id(); i <= p.adapters; i += kWave) count[wave][i] = 0;
+#pragma unroll
+        for (int u = 0; u < kChunkKept; ++u) {
+            uint64_t same = ~uint64_t(0);  // the lanes of the same group, bit by bit of its number
+#pragma unroll
+            for (int b = 0; b < 10; ++b) {
+                const bool set = group[u] >> b & 1;
+                const uint64_t lanes = ballot(set);
+                same &= set ? lanes : ~lanes;
+            }
+            const int before = __popcll(same & lanemask_lt());
+            __builtin_amdgcn_wave_barrier();
+            const int have = group[u] <= p.adapters ? count[wave][group[u]] : 0;
+            rank[u] = have + before;
+            __builtin_amdgcn_wave_barrier();
+            if (before == 0 && group[u] <= p.adapters) count[wave][group[u]] = have + __popcll(same);
+        }
+        __syncthreads();
+    }
+};
+
+__global__ __launch_bounds__(kChunkThreads) void adapter_count_kernel(const ChunkArgs p) {
+    __shared__ int32_t count[kChunkWaves][kMostGroups];
+    const ChunkTokens t(p, count);
+    for (int i = threadIdx.x; i <= p.adapters; i += kChunkThreads) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < kChunkWaves; ++w) n += count[w][i];
+        p.counts[(int64_t)blockIdx.x * (p.adapters + 1) + i] = n;
+    }
+}
+
+__device__ __forceinline__ int sum_up_to_lane(int v) {
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int other = __shfl_up(v, d, kWave);
+        if (lane_id() >= d) v += other;
+    }
+    return v;
+}
+
+// A wave for each group.
+__global__ __launch_bounds__(256) void adapter_sum_kernel(const ChunkArgs p) {
+    const int groups = p.adapters + 1, i = blockIdx.x * 4 + threadIdx.x / kWave;
+    if (i >= groups) return;
+    int sum = 0;
+    for (int c0 = lane_id(); c0 - lane_id() < p.chunks; c0 += 4 * kWave) {
+        int v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = c0 + u * kWave < p.chunks ? p.counts[(int64_t)(c0 + u * kWave) * groups + i] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int to = sum_up_to_lane(v[u]);
+            if (c0 + u * kWave < p.chunks) p.counts[(int64_t)(c0 + u * kWave) * groups + i] = sum + to - v[u];
+            sum += __shfl(to, kWave - 1, kWave);
+        }
+    }
+    if (lane_id() == 0) p.counts[(int64_t)p.chunks * groups + i] = sum;
+}
+
+__global__ __launch_bounds__(kChunkThreads) void adapter_place_kernel(const ChunkArgs p) {
+    constexpr int OWN = (kMostGroups + kChunkThreads - 1) / kChunkThreads;  // groups of a thread
+    __shared__ int32_t count[kChunkWaves][kMostGroups];
+    __shared__ int32_t first[kMostGroups + 1], wave_sum[kChunkWaves];
+    const ChunkTokens t(p, count);
+    const int wave = threadIdx.x / kWave, groups = p.adapters + 1, tile = p.tile, i0 = threadIdx.x * OWN;
+    int all[OWN], before[OWN], sum = 0;
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+        all[k] = before[k] = 0;
+        if (i0 + k < groups) {
+            all[k] = p.counts[(int64_t)p.chunks * groups + i0 + k];
+            before[k] = p.counts[(int64_t)blockIdx.x * groups + i0 + k];
+        }
+        sum += all[k];
+    }
+    const int to = sum_up_to_lane(sum);
+    if (lane_id() == kWave - 1) wave_sum[wave] = to;
+    __syncthreads();
+    int start = to - sum;
+    for (int w = 0; w < wave; ++w) start += wave_sum[w];
+#pragma unroll
+    for (int k = 0; k < OWN; ++k) {
+        const int i = i0 + k;
+        if (i >= groups) break;
+        first[i] = start;
+        int at = start + before[k];
+#pragma unroll
+        for (int w = 0; w < kChunkWaves; ++w) {
+            const int n = count[w][i];
+            count[w][i] = at;
+            at += n;
+        }
+        if (blockIdx.x == 0) {
+            p.offset[i] = start;
+            for (int j = (all[k] + tile - 1) / tile, n = (start + all[k]) / tile + 1 - start / tile; j < n; ++j) p.tiles[start / tile + i + j].group = -1;
+        }
+        start += all[k];
+        if (i == p.adapters) {
+            first[groups] = start;
+            if (blockIdx.x == 0) p.offset[groups] = start;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kChunkKept; ++u) {
+        const int g = t.group[u], token = t.t0 + u * kWave;
+        if (g > p.adapters) continue;
+        const int at = count[wave][g] + t.rank[u], begin = first[g], end = first[g + 1], k = at - begin;
+        Tile& slot = p.tiles[begin / tile + g + k / tile];
+        p.order[at] = token;
+        slot.token[k % tile] = token;
+        if (k % tile == 0) {
+            slot.group = g;
+            slot.row0 = at;
+            slot.rows = end - at < tile ? end - at : tile;
+        }
+        if (at == end - 1)
+            for (int r = k % tile + 1; r < tile; ++r) slot.token[r] = token;
+    }
 }
 
 // ---- the first product: to the rank ------------------------------------------
@@ -750,7 +904,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Room {  // places in the workspace
-    size_t offset, order, tiles, partial, scaled, bytes;
+    size_t offset, order, counts, tiles, partial, scaled, bytes;
 };
 
 bool few(int64_t tokens) { return tokens <= kFewTokens; }
@@ -772,18 +926,28 @@ int64_t piece_count(int64_t tokens, int rank, int64_t in) {
     return (in + p - 1) / p;
 }
 
+int64_t chunk_count(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
+
 Room room_for(int64_t tokens, int adapters, int rank, int64_t in, int64_t out, bool grad) {
     Room r;
     r.offset = 0;
     r.order = padded(((size_t)adapters + 2) * 4);
-    r.tiles = r.order + padded((size_t)tokens * 4);
+    r.counts = r.order + padded((size_t)tokens * 4);
+    r.tiles = r.counts + (tokens > kLongPlan ? padded((size_t)(chunk_count(tokens) + 1) * (adapters + 1) * 4) : 0);
     r.partial = r.tiles + padded((size_t)tile_slots(tokens, adapters) * sizeof(Tile));
     r.scaled = r.partial + padded((size_t)piece_count(tokens, rank, grad ? out : in) * tokens * rank * 4);
     r.bytes = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
     return r;
 }
 
-hipError_t plan(const int64_t* index, int64_t tokens, int adapters, int32_t* offset, int32_t* order, Tile* tiles, hipStream_t stream) {
+hipError_t plan(const int64_t* index, int64_t tokens, int adapters, int32_t* offset, int32_t* order, int32_t* counts, Tile* tiles, hipStream_t stream) {
+    if (tokens > kLongPlan) {
+        const ChunkArgs p{index, (int)tokens, adapters, (int)chunk_count(tokens), tile_tokens(tokens), counts, offset, order, tiles};
+        hipLaunchKernelGGL(adapter_count_kernel, dim3((unsigned)p.chunks), dim3(kChunkThreads), 0, stream, p);
+        hipLaunchKernelGGL(adapter_sum_kernel, dim3((unsigned)(adapters + 4) / 4), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL(adapter_place_kernel, dim3((unsigned)p.chunks), dim3(kChunkThreads), 0, stream, p);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL(adapter_plan_kernel, dim3((unsigned)adapters + 1), dim3(kPlanThreads), 0, stream, index, (int)tokens, adapters, offset,
                        order, tiles, tile_tokens(tokens));
     return hipGetLastError();
@@ -869,7 +1033,8 @@ hipError_t launch_adapters(const AdapterArgs& p, void* workspace, hipStream_t st
     float* partial = reinterpret_cast<float*>(ws + room.partial);
     if (!few(p.tokens)) {
         const hipError_t err = plan(p.index, p.tokens, p.adapters, reinterpret_cast<int32_t*>(ws + room.offset),
-                                    reinterpret_cast<int32_t*>(ws + room.order), tiles, stream);
+                                    reinterpret_cast<int32_t*>(ws + room.order),
+                                    reinterpret_cast<int32_t*>(ws + room.counts), tiles, stream);
         if (err != hipSuccess) return err;
     }
     return products<false>(ShrinkArgs{p.x, p.a, p.index, tiles, p.tokens, p.in, 0, p.adapters, p.rank, partial},
@@ -887,7 +1052,7 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
     float* partial = reinterpret_cast<float*>(ws + room.partial);
     float* scaled = reinterpret_cast<float*>(ws + room.scaled);
     hipError_t err = hipSuccess;
-    if (!few(p.tokens)) err = plan(p.index, p.tokens, p.adapters, offset, order, tiles, stream);
+    if (!few(p.tokens)) err = plan(p.index, p.tokens, p.adapters, offset, order, reinterpret_cast<int32_t*>(ws + room.counts), tiles, stream);
     if (err != hipSuccess) return err;
     if (p.tokens && (p.grad_x || p.grad_a)) {
         err = products<true>(ShrinkArgs{p.grad, p.b, p.index, tiles, p.tokens, p.out_features, 0, p.adapters, p.rank, partial},

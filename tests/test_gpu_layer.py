@@ -263,7 +263,10 @@ SHAPES = [  # T, J, R, I, O, none, runs
     (255, 20, 24, 136, 264, 0.2, 0), (256, 300, 16, 264, 72, 0.1, 0), (256, 2, 32, 128, 128, 0.0, 2), (257, 9, 8, 72, 136, 0.1, 0),
     (1023, 3, 16, 136, 64, 0.1, 8), (1024, 40, 32, 64, 200, 0.0, 0), (300, 8, 64, 1032, 515, 0.1, 9), (513, 2, 128, 264, 264, 0.0, 3), (600, 5, 72, 136, 1003, 0.2, 0),
     (1030, 7, 16, 2304, 136, 0.1, 0), (1500, 1, 256, 256, 300, 0.0, 1), (2100, 16, 32, 200, 520, 0.05, 30),
-    (2500, 3, 136, 328, 72, 0.1, 5), (4093, 8, 64, 448, 264, 0.1, 24)]
+    (2500, 3, 136, 328, 72, 0.1, 5), (4093, 8, 64, 448, 264, 0.1, 24),
+    # many tokens: their order by chunks
+    (8193, 40, 8, 16, 24, 0.1, 0), (16384, 3, 8, 72, 24, 0.1, 0), (16385, 512, 8, 24, 16, 0.1, 0), (20000, 1, 8, 64, 8, 0.3, 0),
+    (33000, 512, 16, 16, 8, 0.9, 40), (70001, 64, 16, 24, 40, 0.05, 500), (300000, 2, 8, 8, 8, 0.5, 0)]
 
 
 @pytest.mark.parametrize("T,J,R,I,O,none,runs", SHAPES)
