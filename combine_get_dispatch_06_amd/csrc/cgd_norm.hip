@@ -207,15 +207,21 @@ hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
 template <int LANES, int V, bool FAR>
 __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void norm_grad_kernel(const NormGradArgs a, int threads) {
     constexpr int GROUPS = LANES ? 256 / LANES : 1;
-    constexpr bool KEPT = V < 4;  // room for the weights in registers
+    constexpr bool KEPT = V < 4;  // room for the weights in registers: four vectors spill (1000 x 32768: 104 us for 60)
     __shared__ float slot[2][kMaxWaves][2];
     const int nvec = a.width / 8;
     const int step = LANES ? LANES : threads;
     const int l = LANES ? threadIdx.x % (LANES ? LANES : 1) : threadIdx.x;
-    float w[V][8], dw[V][8];
+    float w[KEPT ? V : 1][8], dw[V][8];
+    // the weights of vector u of the lane: kept, or loaded again
+    auto weights = [&](int u, int from) -> const float(&)[8] {
+        if constexpr (KEPT) return w[u];
+        weight8(a.weight, a.weight_f32, from + u * step < nvec ? from + u * step : 0, w[0]);
+        return w[0];
+    };
 #pragma unroll
     for (int u = 0; u < V; ++u) {
-        if (KEPT) weight8(a.weight, a.weight_f32, l + u * step < nvec ? l + u * step : 0, w[u]);
+        if constexpr (KEPT) weight8(a.weight, a.weight_f32, l + u * step < nvec ? l + u * step : 0, w[u]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
     }
@@ -235,24 +241,21 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
             if (there && v < nvec) {
                 x4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.x) + base + v);
                 g4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad) + base + v);
-                if (a.grad_sum) d4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad_sum) + base + v);
+                if (KEPT && a.grad_sum) d4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad_sum) + base + v);
             }
         }
-        if constexpr (!KEPT) {
-            const int again = afresh(l);
-#pragma unroll
-            for (int u = 0; u < V; ++u) weight8(a.weight, a.weight_f32, again + u * step < nvec ? again + u * step : 0, w[u]);
-        }
+        const int once = KEPT ? l : afresh(l);
         float sums[2] = {0.0f, 0.0f};  // of s^2, of g s
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             float x[8], g[8];
             unpack8(x4[u], x);
             unpack8(g4[u], g);
+            const float(&wu)[8] = weights(u, once);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sums[0] = __builtin_fmaf(x[i], x[i], sums[0]);
-                sums[1] = __builtin_fmaf(g[i] * w[u][i], x[i], sums[1]);
+                sums[1] = __builtin_fmaf(g[i] * wu[i], x[i], sums[1]);
             }
         }
         // two sets of slots: a wave may be one row ahead of another's reads, not two
@@ -260,17 +263,20 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
         turn ^= 1;
         const float r = rsqrtf(sums[0] * mean + a.eps);
         const float c = sums[1] * r * r * mean;  // times s: h mean(g h)
+        const int twice = KEPT ? l : afresh(l);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
             const int v = l + u * step;
             float x[8], g[8], d[8];
             unpack8(x4[u], x);
             unpack8(g4[u], g);
+            if (!KEPT && a.grad_sum && there && v < nvec) d4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad_sum) + base + v);
             unpack8(d4[u], d);
+            const float(&wu)[8] = weights(u, twice);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (there) dw[u][i] = __builtin_fmaf(g[i] * r, x[i], dw[u][i]);  // (r of no row may be infinite)
-                const float t = r * (g[i] * w[u][i] - x[i] * c);
+                const float t = r * (g[i] * wu[i] - x[i] * c);
                 d[i] = a.grad_sum ? d[i] + t : t;
             }
             if (a.grad_x && there && v < nvec) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
@@ -369,10 +375,18 @@ hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     return norm_rows<0, 4>(a, threads, stream);
 }
 
+// Each block writes a row of sums for the weight's gradient, so only as many as keep the
+// CUs busy: 1024 threads a CU, two blocks (16000 x 2048: 41 us with four blocks a CU, 49
+// with two, 46 with eight; 8000 x 4096: 39 with two, 42 with four), and one where a lane
+// has several vectors (2000 x 16384: 45 us, 50 with two). Rows for a few turns are shared
+// out evenly (300 x 16384: 15.3 us for 20.4).
 int64_t norm_grad_blocks(int64_t rows, int width) {
     const int per = width <= 128 ? 16 : width <= 256 ? 8 : width <= 1024 ? 4 : 1;  // rows at a time
-    const int64_t groups = (rows + per - 1) / per, most = width <= 1024 ? 1024 : 512;
-    return groups < most ? groups : most;
+    const int64_t groups = (rows + per - 1) / per;
+    const int v = gradient_vectors(width), threads = row_threads(width, v);
+    const int64_t most = width <= 1024 ? 1024 : 256 * (v > 1 ? 1 : threads > 512 ? 2 : 1024 / threads);
+    const int64_t turns = (groups + most - 1) / most;
+    return turns > 0 && turns <= 4 ? (groups + turns - 1) / turns : groups < most ? groups : most;
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t stream) {
