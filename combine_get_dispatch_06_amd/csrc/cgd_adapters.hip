@@ -751,6 +751,9 @@ struct AdapterWeightArgs {
     int a_blocks;           // column blocks of grad_a; those of grad_b follow
     uint16_t* grad_a;
     uint16_t* grad_b;
+    int shares;             // of an adapter's tokens, a block each
+    float* partial_a;       // several shares: their sums, [share] of grad_a's and of grad_b's elements
+    float* partial_b;
 };
 
 // A block has 128 columns (of x for grad_a, of grad for grad_b) and 16 * RT
@@ -773,7 +776,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
     const int64_t col = (int64_t)(is_a ? blockIdx.x : blockIdx.x - w.a_blocks) * 128 + n * 8;
     const uint16_t* wide = is_a ? w.x : w.grad;
     const float* thin = is_a ? w.scaled : w.hidden;
-    const int j = blockIdx.y, rank0 = blockIdx.z * 16 * RT;
+    const int j = blockIdx.y / w.shares, share = blockIdx.y - j * w.shares, rank0 = blockIdx.z * 16 * RT;
     if constexpr (FEW) {
         if (wave == 0) {
             const FewTokens t(w.index, w.tokens, w.adapters);
@@ -786,7 +789,12 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
         }
         __syncthreads();
     }
-    const int begin = FEW ? bounds[0] : w.offset[j], end = FEW ? bounds[1] : w.offset[j + 1];
+    int begin = FEW ? bounds[0] : w.offset[j], end = FEW ? bounds[1] : w.offset[j + 1];
+    if (!FEW && w.shares > 1) {  // whole steps of the waves
+        const int each = ((end - begin + w.shares - 1) / w.shares + NW * 32 - 1) / (NW * 32) * (NW * 32);
+        begin = begin + share * each < end ? begin + share * each : end;
+        end = begin + each < end ? begin + each : end;
+    }
     const int* const order = FEW ? own : w.order + begin;  // of the adapter's tokens
     const float scale = !is_a && w.scale ? w.scale[j] : 1.0f;
     float4_t acc[RT][8];
@@ -887,16 +895,44 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float v[8] = {acc[r][0][i], acc[r][1][i], acc[r][2][i], acc[r][3][i], acc[r][4][i], acc[r][5][i], acc[r][6][i], acc[r][7][i]};
-                store_run<8>(w.grad_a, ((int64_t)j * w.rank + k + i) * w.in + col, v, 8, false, true);
+                const int64_t at = ((int64_t)j * w.rank + k + i) * w.in + col;
+                if (!FEW && w.shares > 1)
+                    store_run<8>(w.partial_a, share * (w.adapters * w.rank * w.in) + at, v, 8, true, true);
+                else
+                    store_run<8>(w.grad_a, at, v, 8, false, true);
             }
         } else {  // [out][rank]: four ranks of eight columns
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const float v[4] = {acc[r][c][0], acc[r][c][1], acc[r][c][2], acc[r][c][3]};
-                store_run<4>(w.grad_b, ((int64_t)j * w.out + col + c) * w.rank + k, v, 4, false, true);
+                const int64_t at = ((int64_t)j * w.out + col + c) * w.rank + k;
+                if (!FEW && w.shares > 1)
+                    store_run<4>(w.partial_b, share * (w.adapters * w.rank * w.out) + at, v, 4, true, true);
+                else
+                    store_run<4>(w.grad_b, at, v, 4, false, true);
             }
         }
     }
+}
+
+// Adds the shares' sums, in order; four elements a thread, grad_a's and then grad_b's.
+__global__ __launch_bounds__(256) void adapter_join_kernel(const AdapterWeightArgs w) {
+    const int64_t na = w.grad_a ? w.adapters * w.rank * w.in / 4 : 0, nb = w.grad_b ? w.adapters * w.rank * w.out / 4 : 0;
+    const int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (v >= na + nb) return;
+    const bool is_a = v < na;
+    const int64_t i = is_a ? v : v - na, next = is_a ? na : nb;
+    const float4_t* from = reinterpret_cast<const float4_t*>(is_a ? w.partial_a : w.partial_b) + i;
+    float4_t sum = from[0];
+    for (int s = 1; s < w.shares; s += 4) {
+        float4_t part[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) part[u] = from[(s + u < w.shares ? s + u : 0) * next];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s + u < w.shares) sum += part[u];
+    }
+    reinterpret_cast<uint2*>(is_a ? w.grad_a : w.grad_b)[i] = make_uint2(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]));
 }
 
 // ---- host --------------------------------------------------------------------
@@ -904,7 +940,7 @@ __global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const Adapter
 size_t padded(size_t n) { return (n + 255) / 256 * 256; }
 
 struct Room {  // places in the workspace
-    size_t offset, order, counts, tiles, partial, scaled, bytes;
+    size_t offset, order, counts, tiles, partial, scaled, shares, bytes;
 };
 
 bool few(int64_t tokens) { return tokens <= kFewTokens; }
@@ -928,6 +964,20 @@ int64_t piece_count(int64_t tokens, int rank, int64_t in) {
 
 int64_t chunk_count(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
 
+// Shares of an adapter's tokens in its gradients, each with blocks of its own and sums
+// that another kernel adds: few adapters with many tokens would leave CUs idle. us of a
+// whole gradient without and with shares, 4096 -> 4096: 65536 tokens of one adapter, rank
+// 16 772 and 511, rank 64 955 and 814; 16384, rank 16 224 and 149. From a block for every
+// second CU on they cost more than they give (16384 tokens of two, rank 64: 207 and 237),
+// and below 1536 tokens of an adapter the launch does (1024 of one, rank 16: 25 and 26.5).
+int64_t weight_shares(int64_t tokens, int adapters, int rank, int64_t in, int64_t out) {
+    const int64_t blocks = ((in + 127) / 128 + (out + 127) / 128) * adapters * ((rank + 31) / 32);
+    if (blocks > 128 || tokens < int64_t(1536) * adapters) return 1;
+    int64_t shares = 1024 / blocks;
+    if (shares > tokens / (256 * adapters)) shares = tokens / (256 * adapters);
+    return shares > 16 ? 16 : shares;
+}
+
 Room room_for(int64_t tokens, int adapters, int rank, int64_t in, int64_t out, bool grad) {
     Room r;
     r.offset = 0;
@@ -936,7 +986,9 @@ Room room_for(int64_t tokens, int adapters, int rank, int64_t in, int64_t out, b
     r.tiles = r.counts + (tokens > kLongPlan ? padded((size_t)(chunk_count(tokens) + 1) * (adapters + 1) * 4) : 0);
     r.partial = r.tiles + padded((size_t)tile_slots(tokens, adapters) * sizeof(Tile));
     r.scaled = r.partial + padded((size_t)piece_count(tokens, rank, grad ? out : in) * tokens * rank * 4);
-    r.bytes = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
+    r.shares = r.scaled + (grad ? padded((size_t)tokens * rank * 4) : 0);
+    const int64_t shares = grad ? weight_shares(tokens, adapters, rank, in, out) : 1;
+    r.bytes = r.shares + (shares > 1 ? padded((size_t)shares * adapters * rank * (in + out) * 4) : 0);
     return r;
 }
 
@@ -1062,16 +1114,18 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
         if (err != hipSuccess) return err;
     }
     if (p.grad_a || p.grad_b) {
-        AdapterWeightArgs w{p.x, p.grad, scaled, p.hidden, p.scale, p.index, (int)p.tokens, offset, order, p.in, p.out_features, p.adapters, p.rank, 0, p.grad_a, p.grad_b};
+        AdapterWeightArgs w{p.x, p.grad, scaled, p.hidden, p.scale, p.index, (int)p.tokens, offset, order, p.in, p.out_features, p.adapters, p.rank, 0, p.grad_a, p.grad_b, (int)weight_shares(p.tokens, p.adapters, p.rank, p.in, p.out_features), nullptr, nullptr};
+        w.partial_a = reinterpret_cast<float*>(ws + room.shares);
+        w.partial_b = w.partial_a + (int64_t)w.shares * p.adapters * p.rank * p.in;
         w.a_blocks = p.grad_a ? (int)((p.in + 127) / 128) : 0;
         const int blocks = w.a_blocks + (p.grad_b ? (int)((p.out_features + 127) / 128) : 0);
 #define CGD_WEIGHTS(RT, NW, FEW)                                                                                                    \
-    hipLaunchKernelGGL((adapter_weight_kernel<RT, NW, FEW>), dim3((unsigned)blocks, (unsigned)p.adapters, (unsigned)((p.rank + 16 * RT - 1) / (16 * RT))), \
+    hipLaunchKernelGGL((adapter_weight_kernel<RT, NW, FEW>), dim3((unsigned)blocks, (unsigned)(p.adapters * w.shares), (unsigned)((p.rank + 16 * RT - 1) / (16 * RT))), \
                        dim3(NW* kWave), (size_t)NW / 2 * RT * 8 * kWave * 16, stream, w)
         // More waves where an adapter has many tokens. Rank 16, 4095 tokens, 4096 -> 7168, us with
-        // 4, 8 and 16 waves: 16 adapters 26 29 32, four 27 25 24, one 62 49 37; rank 64 with 4 and 8:
-        // 16 adapters 45 64, one 64 48.
-        const bool many = p.tokens >= int64_t(768) * p.adapters;
+        // 4, 8 and 16 waves: 16 adapters 26 29 32, four 27 25 24; rank 64 with 4 and 8: 16 adapters 45 64,
+        // one 64 48. (Shares are of 4 waves each.)
+        const bool many = p.tokens >= int64_t(768) * p.adapters && w.shares == 1;
         if (few(p.tokens) && p.rank <= 16)
             CGD_WEIGHTS(1, 4, true);
         else if (few(p.tokens))
@@ -1085,6 +1139,10 @@ hipError_t launch_adapters_grad(const AdapterGradArgs& p, void* workspace, hipSt
         else
             CGD_WEIGHTS(2, 4, false);
 #undef CGD_WEIGHTS
+        if (w.shares > 1) {
+            const int64_t vectors = (int64_t)p.adapters * p.rank * ((p.grad_a ? p.in : 0) + (p.grad_b ? p.out_features : 0)) / 4;
+            hipLaunchKernelGGL(adapter_join_kernel, dim3((unsigned)((vectors + 255) / 256)), dim3(256), 0, stream, w);
+        }
         err = hipGetLastError();
     }
     return err;

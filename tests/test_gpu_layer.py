@@ -314,7 +314,10 @@ def _adapters_grad64(c, hidden):
 
 @pytest.mark.parametrize("T,J,R,I,O,none,runs", [s for s in SHAPES if s[4] % 8 == 0] +
                          [(1, 1, 8, 8, 8, 0.0, 0), (40, 3, 16, 136, 264, 1.0, 0), (33, 2, 8, 64, 72, 0.0, 1),
-                          (700, 2, 64, 264, 136, 0.0, 2), (1025, 1, 16, 128, 128, 0.0, 1)])
+                          (700, 2, 64, 264, 136, 0.0, 2), (1025, 1, 16, 128, 128, 0.0, 1),
+                          # the tokens of few adapters in shares
+                          (1535, 1, 16, 128, 64, 0.0, 1), (1536, 1, 24, 136, 72, 0.2, 0), (3100, 2, 40, 264, 136, 0.1, 0),
+                          (4000, 2, 16, 72, 8, 1.0, 0), (5000, 3, 8, 24, 264, 0.0, 2)])
 @pytest.mark.parametrize("scaled", [True, False])
 def test_adapters_backward(T, J, R, I, O, none, runs, scaled):
     say(f"adapters backward T={T} J={J} R={R} I={I} O={O} none={none} runs={runs} scaled={scaled}")
