@@ -1,0 +1,79 @@
+"""The layer's operators at the edges of their number formats, against the definitions in
+64 bits: infinite operands of the adapters. What is finite is held to the tolerances of
+test_gpu_layer.py; what is infinite or NaN by the definition has to be so."""
+import math
+
+import pytest
+import torch
+
+import combine_get_dispatch_06_amd as cgd
+from gpu_util import say
+from test_gpu_layer import BF16, F32, _adapters64, _adapters_grad64, _dev, _gen, _near
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+def _as_defined(got, want, tol, dtype, what):
+    """Finite values by their tolerance, the others as they are."""
+    got, finite = got.cpu(), want.isfinite()
+    assert torch.equal(got.isnan(), want.isnan()), f"{what}: {int((got.isnan() != want.isnan()).sum())} of {got.numel()} wrongly NaN or not"
+    inf = want.isinf()
+    assert torch.equal(got[inf].double(), want[inf]), f"{what}: infinities"
+    _near(got[finite], want[finite], tol.expand(want.shape)[finite], dtype, what)
+
+
+def _positive(T, J, R, I, O, seed):
+    """Positive values: every sum's sign is known, so an infinity comes out as one."""
+    g = _gen(seed)
+    pos = lambda *shape: (torch.rand(shape, generator=g) + 0.5).to(BF16)  # noqa: E731
+    c = dict(x=pos(T, I), a=pos(J, R, I), b=pos(J, O, R), idx=torch.randint(J, (T,), generator=g), scale=torch.rand(J, generator=g) + 0.25,
+             res=pos(T, O), grad=pos(T, O))
+    c["idx"][T // 2], c["idx"][0] = -1, 0
+    c["x"][0], c["x"][0, 0] = 0, 1  # hidden values that bf16 holds: their second part is 0
+    c["grad"][0], c["grad"][0, 0] = 0, 1
+    c["scale"][0] = 1
+    return c
+
+
+@pytest.mark.parametrize("T,J,R,I,O", [(1, 1, 8, 64, 40), (70, 3, 16, 136, 72), (100, 2, 40, 72, 128), (300, 3, 24, 136, 72), (520, 2, 136, 64, 64),
+                                       (1100, 3, 8, 72, 136), (1500, 2, 64, 136, 72), (1100, 2, 72, 64, 136), (1200, 2, 200, 72, 72), (3300, 2, 16, 64, 72)])
+def test_adapters_infinite_operands(T, J, R, I, O):
+    """An infinity in b, a, x or grad_out: each is the other operand of values that go into
+    a product in two parts, the second of them 0 or of the other sign."""
+    say(f"adapters infinite operands T={T} J={J} R={R} I={I} O={O}")
+    clean = _positive(T, J, R, I, O, T + R)
+    if T == 1:
+        clean["idx"][0] = 0
+    hidden = _adapters64(clean, None)[0].to(F32)
+
+    def forward(c):
+        d = {k: _dev(v) for k, v in c.items()}
+        out, h = cgd.adapter_linear(d["x"], d["a"], d["b"], d["idx"], scale=d["scale"], residual=d["res"], return_hidden=True)
+        h64, y64, th, ty = _adapters64(c, c["res"])
+        _as_defined(h, h64, th, F32, "hidden")
+        _as_defined(out, y64, ty, BF16, "out")
+        return y64
+
+    def backward(c):
+        d = {k: _dev(v) for k, v in c.items()}
+        got = cgd.adapter_linear_backward(d["grad"], d["x"], d["a"], d["b"], d["idx"], _dev(hidden), scale=d["scale"])
+        want, tol = _adapters_grad64(c, hidden)
+        for name, v, w, t in zip(("grad_x", "grad_a", "grad_b"), got, want, tol):
+            _as_defined(v, w, t, BF16, name)
+        return want
+
+    def with_infinity(name, at, value):
+        c = dict(clean, **{name: clean[name].clone()})
+        c[name][at] = value
+        return c
+
+    assert forward(with_infinity("b", (0, O - 1, R - 1), -INF)).isinf().any()
+    both = with_infinity("b", (0, 3, 0), INF)
+    both["b"][0, 3, R // 2] = -INF  # of both signs: NaN
+    assert forward(both).isnan().any()
+    assert backward(with_infinity("a", (0, R - 1, 5), INF))[0].isinf().any()
+    if T > 1:
+        t = int((clean["idx"] == 0).nonzero()[-1])
+        assert backward(with_infinity("x", (t, I - 1), -INF))[1].isinf().any()
+        assert backward(with_infinity("grad", (t, O // 2), INF))[2].isinf().any()
