@@ -34,14 +34,14 @@ __device__ __forceinline__ float4_t mul16(const bf16x8_t& rows, const bf16x8_t& 
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, columns, sum, 0, 0, 0);
 }
 
-// v = hi + lo in bf16 pairs: of two values.
+// v = hi + lo in bf16 pairs: of two values. A finite value that would round to an
+// infinity has the largest bf16 number as its first part; an infinity or NaN has no second.
 __device__ __forceinline__ void halves2(float a, float b, uint32_t* hi, uint32_t* lo) {
-    const uint32_t h = pack_bf16x2(a, b);
-    // what is infinite or NaN already has no second part
-    const float da = fabsf(a) < __builtin_inff() ? a - bf16_lo(h) : 0.0f;
-    const float db = fabsf(b) < __builtin_inff() ? b - bf16_hi(h) : 0.0f;
+    const float most = __uint_as_float(0x7F7F0000u);
+    const bool fa = fabsf(a) < __builtin_inff(), fb = fabsf(b) < __builtin_inff();
+    const uint32_t h = pack_bf16x2(fa ? __builtin_amdgcn_fmed3f(a, -most, most) : a, fb ? __builtin_amdgcn_fmed3f(b, -most, most) : b);
     *hi = h;
-    *lo = pack_bf16x2(da, db);
+    *lo = pack_bf16x2(fa ? a - bf16_lo(h) : 0.0f, fb ? b - bf16_hi(h) : 0.0f);
 }
 
 // An infinite operand times a part of 0, or infinities of both signs from two parts of

@@ -1,5 +1,5 @@
 """The layer's operators at the edges of their number formats, against the definitions in
-64 bits: infinite operands of the adapters. What is finite is held to the tolerances of
+64 bits: infinite operands of the adapters, and values next to the largest number. What is finite is held to the tolerances of
 test_gpu_layer.py; what is infinite or NaN by the definition has to be so."""
 import math
 
@@ -77,3 +77,27 @@ def test_adapters_infinite_operands(T, J, R, I, O):
         t = int((clean["idx"] == 0).nonzero()[-1])
         assert backward(with_infinity("x", (t, I - 1), -INF))[1].isinf().any()
         assert backward(with_infinity("grad", (t, O // 2), INF))[2].isinf().any()
+
+
+@pytest.mark.parametrize("T,R", [(3, 8), (70, 24), (300, 64), (1100, 8), (1300, 72), (3300, 16)])
+def test_adapters_next_to_the_largest_number(T, R):
+    """Scaled hidden values of 3.4e38, which bf16 would round to an infinity: the results,
+    some 2^-10 of them and less, are finite."""
+    say(f"adapters next to the largest number T={T} R={R}")
+    J, I, O = 2, 72, 136
+    g = _gen(T + R)
+    small = lambda *shape: ((torch.rand(shape, generator=g) + 0.5) * 2.0 ** -30).to(BF16)  # noqa: E731
+    c = dict(x=small(T, I), a=small(J, R, I), b=small(J, O, R), idx=torch.randint(J, (T,), generator=g),
+             scale=torch.tensor([3.4e38, -3.4e38]), res=small(T, O), grad=small(T, O))
+    c["x"][:, 0], c["a"][:, :, 0], c["b"][:, 0], c["grad"][:, 0] = 2.0 ** 10, 2.0 ** -10, 2.0 ** -10, 2.0 ** 10
+    d = {k: _dev(v) for k, v in c.items()}
+    out, hidden = cgd.adapter_linear(d["x"], d["a"], d["b"], d["idx"], scale=d["scale"], return_hidden=True)
+    assert (hidden == 1).all()
+    _, y64, _, ty = _adapters64(c, None)
+    _near(out, y64, ty, BF16, "out")
+    gx, ga, gb = cgd.adapter_linear_backward(d["grad"], d["x"], d["a"], d["b"], d["idx"], hidden, scale=d["scale"])
+    want, tol = _adapters_grad64(c, hidden.cpu())
+    _near(gx, want[0], tol[0], BF16, "grad_x")
+    # (the first columns of x and grad are 2^10: their products are past the largest number)
+    _near(ga[:, :, 1:], want[1][:, :, 1:], tol[1][:, :, 1:], BF16, "grad_a")
+    _near(gb[:, 1:], want[2][:, 1:], tol[2][:, 1:], BF16, "grad_b")
