@@ -28,7 +28,8 @@ extern "C" {
  *   sum           bf16 [num_rows, hidden] out or NULL: s rounded (y is made from s before that)
  * At least one of y and codes. sum may be x or residual itself; the outputs share no other memory.
  * hidden: a multiple of 8 (FP8: of 128) up to 32768. A finite row whose squares add up to more than
- * fp32 holds gives zeros. All but scales 16-byte aligned. */
+ * fp32 holds gives zeros; one whose squares are too small for it is normed as any other, and only
+ * zeros without eps are 0 / 0. All but scales 16-byte aligned. */
 int cgd_rms_norm(const void* x, const void* residual, const void* weight, int weight_type, float eps, int64_t num_rows,
                  int hidden, void* y, void* codes, void* scales, int scale_format, void* sum, hipStream_t stream);
 

@@ -1,14 +1,13 @@
 """The layer's operators at the edges of their number formats, against the definitions in
-64 bits: infinite operands of the adapters, and values next to the largest number. What is finite is held to the tolerances of
+64 bits: infinite operands of the adapters, values next to the largest number, and rows
+whose squares are too small for fp32. What is finite is held to the tolerances of
 test_gpu_layer.py; what is infinite or NaN by the definition has to be so."""
-import math
-
 import pytest
 import torch
 
 import combine_get_dispatch_06_amd as cgd
 from gpu_util import say
-from test_gpu_layer import BF16, F32, _adapters64, _adapters_grad64, _dev, _gen, _near
+from test_gpu_layer import BF16, F32, F64, U, _adapters64, _adapters_grad64, _check_fp8, _dev, _gen, _near, _norm64
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
@@ -101,3 +100,60 @@ def test_adapters_next_to_the_largest_number(T, R):
     # (the first columns of x and grad are 2^10: their products are past the largest number)
     _near(ga[:, :, 1:], want[1][:, :, 1:], tol[1][:, :, 1:], BF16, "grad_a")
     _near(gb[:, 1:], want[2][:, 1:], tol[2][:, 1:], BF16, "grad_b")
+
+
+FAINT = [(5, 64), (7, 200), (9, 256), (3, 512), (5, 1024), (4, 1032), (3, 7168), (600, 4096), (515, 8200), (3, 20480), (65600, 64)]
+
+
+def _faint(T, H, scale, seed):
+    """Rows of `scale`, one in three of ordinary size among them; -> x, residual, weight."""
+    g = _gen(seed)
+    x, r = torch.randn(T, H, generator=g), torch.randn(T, H, generator=g)
+    size = torch.full((T, 1), scale)
+    size[2::3] = 1
+    return (x * size).to(BF16), (r * size).to(BF16), torch.rand(H, generator=g) + 0.5
+
+
+@pytest.mark.parametrize("T,H", FAINT)
+@pytest.mark.parametrize("scale", [1e-15, 1e-22, 1e-30, 2.0 ** -130])
+def test_norm_of_rows_whose_squares_vanish(T, H, scale):
+    """Without eps, or with one that is as small, a row's size does not matter."""
+    say(f"norm of faint rows T={T} H={H} scale={scale}")
+    x, r, w = _faint(T, H, scale, T + H)
+    for eps in (0.0, 1e-40) if T < 10000 else (0.0,):
+        eps64 = torch.tensor(eps, dtype=F32).to(F64).item()
+        y = cgd.rms_norm(_dev(x), _dev(w), eps=eps)
+        _, y64, _, ty = _norm64(x, None, w, eps64)
+        _near(y, y64, ty, BF16, "y alone")
+        fp8 = cgd.SCALE_F32 if H % 128 == 0 else None
+        got, total = cgd.rms_norm(_dev(x), _dev(w), eps=eps, residual=_dev(r), cast_fp8=fp8, return_bf16=fp8 is not None)
+        s64, y64, _, ty = _norm64(x, r, w, eps64)
+        y, q = got if fp8 is not None else (got, None)
+        _near(y, y64, ty, BF16, "y")
+        assert torch.equal(total.cpu(), (x.float() + r.float()).to(BF16))
+        if q:
+            _check_fp8(*q, y64, ty, fp8)
+
+
+@pytest.mark.parametrize("T,H", FAINT)
+@pytest.mark.parametrize("scale", [1e-15, 1e-22, 1e-30, 2.0 ** -130])
+def test_norm_backward_of_rows_whose_squares_vanish(T, H, scale):
+    say(f"norm backward of faint rows T={T} H={H} scale={scale}")
+    x, _, w = _faint(T, H, scale, T * 3 + H)
+    gy = (torch.randn(T, H, generator=_gen(1)) * 2.0 ** -20).to(BF16)  # (2^130 times 1 would be infinite)
+    gx, gw = cgd.rms_norm_backward(_dev(gy), _dev(x), _dev(w), eps=0.0)
+    x, gy, w64 = x.to(F64), gy.to(F64), w.to(F64)
+    r = 1 / torch.sqrt((x * x).mean(1, keepdim=True))
+    gwx = gy * w64 * x
+    want = r * (gy * w64 - x * r * r * gwx.mean(1, keepdim=True))
+    tol = (2 * H + 16) * U * r * ((gy * w64).abs() + x.abs() * r * r * gwx.abs().mean(1, keepdim=True))
+    _near(gx, want, tol, BF16, "grad_x")
+    _near(gw, (gy * x * r).sum(0), (T + H / 2 + 8) * U * (gy * x * r).abs().sum(0), F32, "grad_weight")
+
+
+def test_norm_of_zeros_without_eps():
+    """0 / 0."""
+    x, w = torch.zeros(2, 256, dtype=BF16), torch.ones(256)
+    x[1] = 1e-30
+    y = cgd.rms_norm(_dev(x), _dev(w), eps=0.0)
+    assert y[0].isnan().all() and (y[1] == 1).all()
