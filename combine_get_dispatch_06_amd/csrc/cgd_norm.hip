@@ -102,8 +102,8 @@ __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&o
 // all of them. It is taken again, kLift times as large: every bf16 value is a normal
 // number then, and so are the squares. That is done behind what every row goes through,
 // with its inputs loaded anew; where the sums are known it would keep apart what overlaps
-// otherwise (131040 x 128 1.3 us more). To look for such rows costs the gradient 0.3 to 2
-// us (8000 x 4096: 41.5 for 39.6).
+// otherwise (131040 x 128 1.3 us more, the gradient of 8000 x 4096 2). So to look for such
+// rows costs nothing that shows, but 2 us of the gradient of 10000 x 3200 (40).
 constexpr float kFaint = 0x1p-100f, kLift = 0x1p100f;
 
 // V 16-byte vectors a lane, R rows one after the other (their loads together).
@@ -249,6 +249,13 @@ hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Whether sums of a row have lost bits, or all of them, or are more than fp32 holds: then
+// its gradient is worked out by itself, from values that are some power of two larger or
+// smaller.
+__device__ __forceinline__ bool is_lost(float square, float dot) {
+    return !(square >= kFaint && square < __builtin_inff() && fabsf(dot) < __builtin_inff());
+}
+
 // Gradient. A block takes every gridDim.x-th group of rows and keeps the weight's gradient of its columns in registers: one row of sums a
 // block. Two blocks share a CU, so that one loads while the other adds up: 45 us for
 // 4095 x 7168 where one with its next row on the way took 52.
@@ -274,14 +281,13 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
         for (int i = 0; i < 8; ++i) dw[u][i] = 0.0f;
     }
     int turn = 0;
+    bool some = false;  // rows that are lost
     const float mean = 1.0f / (float)a.width;
     int64_t row0 = (int64_t)blockIdx.x * GROUPS;
     const int mine = LANES ? threadIdx.x / (LANES ? LANES : 1) : 0;
-    float lift = 1.0f;
-    bool again = false;  // the wave takes its rows a second time: those of lanes whose lift is not 1
-    while (row0 < a.rows) {
+    for (; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
         const int64_t row = row0 + mine;
-        const bool there = row < a.rows && (!again || lift != 1.0f);
+        const bool there = row < a.rows;
         const int64_t base = row * nvec;
         uint4 x4[V], g4[V], d4[V];
         const int first = KEPT ? l : afresh(l);
@@ -293,16 +299,6 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
                 x4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.x) + base + v);
                 g4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad) + base + v);
                 if (KEPT && a.grad_sum) d4[u] = take<FAR>(reinterpret_cast<const uint4*>(a.grad_sum) + base + v);
-            }
-        }
-        if (again) {
-#pragma unroll
-            for (int u = 0; u < V; ++u) {
-                float x[8];
-                unpack8(x4[u], x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= lift;
-                x4[u] = pack8(x);
             }
         }
         const int once = KEPT ? l : afresh(l);
@@ -322,11 +318,12 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
         // two sets of slots: a wave may be one sum ahead of another's reads, not two
         row_sums<LANES>(sums, threads, slot[turn]);
         turn ^= 1;
-        const float square = sums[0] * mean + a.eps * lift * lift;
-        const bool faint = square < kFaint && there && !again;
+        const float square = sums[0] * mean + a.eps;
+        const bool lost = is_lost(square, sums[1]) && there;
+        some |= lost;
         const float r = rsqrtf(square);
         const float c = sums[1] * r * r * mean;  // times s: h mean(g h)
-        const float kept = there && !faint ? r : 0.0f;  // (r of no row may be infinite)
+        const float kept = there && !lost ? r : 0.0f;  // (r of no row may be infinite)
         const int twice = KEPT ? l : afresh(l);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -340,14 +337,70 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[u][i] = __builtin_fmaf(g[i] * kept, x[i], dw[u][i]);
-                const float t = r * (g[i] * wu[i] - x[i] * c) * lift;
+                const float t = r * (g[i] * wu[i] - x[i] * c);
                 d[i] = a.grad_sum ? d[i] + t : t;
             }
-            if (a.grad_x && there && v < nvec && !faint) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
+            if (a.grad_x && there && v < nvec && !lost) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
         }
-        lift = faint ? kLift : 1.0f;  // (the same for all lanes of the row)
-        again = ballot(faint) != 0;
-        if (!again) row0 += (int64_t)gridDim.x * GROUPS;
+    }
+    // the lost rows, found by their sums once more
+    if (ballot(some) != 0) {
+        for (row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
+            const int64_t row = row0 + mine, base = row * nvec;
+            const bool there = row < a.rows;
+            auto vector = [&](const uint16_t* from, int v, float factor, float(&out)[8]) {
+                unpack8(from && there && v < nvec ? reinterpret_cast<const uint4*>(from)[base + v] : make_uint4(0, 0, 0, 0), out);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) out[i] *= factor;
+            };
+            auto add_up = [&](float lift, float(&sums)[2]) {
+                sums[0] = sums[1] = 0.0f;
+#pragma unroll
+                for (int u = 0; u < V; ++u) {
+                    const int from = afresh(l), v = from + u * step;
+                    float x[8], g[8];
+                    vector(a.x, v, lift, x);
+                    vector(a.grad, v, 1.0f, g);
+                    const float(&wu)[8] = weights(u, from);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        sums[0] = __builtin_fmaf(x[i], x[i], sums[0]);
+                        sums[1] = __builtin_fmaf(g[i] * wu[i], x[i], sums[1]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                row_sums<LANES>(sums, threads, slot[turn]);
+                turn ^= 1;
+            };
+            float sums[2];
+            add_up(1.0f, sums);
+            float square = sums[0] * mean + a.eps;
+            if (!is_lost(square, sums[1]) || !there) continue;  // (the same for all lanes of the row)
+            const float lift = square < kFaint ? kLift : square < __builtin_inff() ? 0x1p-40f : 0x1p-112f;
+            add_up(lift, sums);
+            square = sums[0] * mean + a.eps * lift * lift;
+            const float r = rsqrtf(square), c = sums[1] * r * mean;  // mean(g h)
+            // of the row as it is, r is r * lift: in two steps where that may be infinite
+            const float down = r * fminf(lift, 1.0f), up = fmaxf(lift, 1.0f);
+#pragma unroll
+            for (int u = 0; u < V; ++u) {
+                const int from = afresh(l), v = from + u * step;
+                float x[8], g[8], d[8];
+                vector(a.x, v, lift, x);
+                vector(a.grad, v, 1.0f, g);
+                vector(a.grad_sum, v, 1.0f, d);
+                const float(&wu)[8] = weights(u, from);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float h = x[i] * r;
+                    dw[u][i] = __builtin_fmaf(g[i], h, dw[u][i]);
+                    const float t = down * (g[i] * wu[i] - h * c) * up;
+                    d[i] = a.grad_sum ? d[i] + t : t;
+                }
+                if (a.grad_x && v < nvec) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
     if (!a.partial) return;
     float* const out = a.partial + (int64_t)blockIdx.x * a.width;

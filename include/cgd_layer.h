@@ -34,10 +34,10 @@ int cgd_rms_norm(const void* x, const void* residual, const void* weight, int we
                  int hidden, void* y, void* codes, void* scales, int scale_format, void* sum, hipStream_t stream);
 
 /* Its gradient at x, the values that were normed (with a residual: their sum, whose gradient is that
- * of both):
+ * of both), also of rows whose squares are more, or less, than fp32 holds:
  *   grad_y        bf16 [num_rows, hidden]
  *   grad_sum      bf16 [num_rows, hidden] or NULL: what reaches the sum on another way, added
- *   grad_x        bf16 [num_rows, hidden] out or NULL
+ *   grad_x        bf16 [num_rows, hidden] out or NULL; shares no memory with an input
  *   grad_weight   [hidden] of weight_type out or NULL, which needs the workspace */
 size_t cgd_rms_norm_backward_workspace_bytes(int64_t num_rows, int hidden);
 int cgd_rms_norm_backward(const void* grad_y, const void* x, const void* weight, int weight_type, float eps,

@@ -1,6 +1,6 @@
 """The layer's operators at the edges of their number formats, against the definitions in
 64 bits: infinite operands of the adapters, values next to the largest number, and rows
-whose squares are too small for fp32. What is finite is held to the tolerances of
+whose squares are too small or too large for fp32. What is finite is held to the tolerances of
 test_gpu_layer.py; what is infinite or NaN by the definition has to be so."""
 import pytest
 import torch
@@ -135,20 +135,38 @@ def test_norm_of_rows_whose_squares_vanish(T, H, scale):
             _check_fp8(*q, y64, ty, fp8)
 
 
+def _check_norm_backward(x, gy, w, eps):
+    T, H = x.shape
+    gx, gw = cgd.rms_norm_backward(_dev(gy), _dev(x), _dev(w), eps=eps)
+    x, gy, w64 = x.to(F64), gy.to(F64), w.to(F64)
+    r = 1 / torch.sqrt((x * x).mean(1, keepdim=True) + eps)
+    gwx = gy * w64 * x
+    want = r * (gy * w64 - x * r * r * gwx.mean(1, keepdim=True))
+    tol = (2 * H + 16) * U * r * ((gy * w64).abs() + x.abs() * r * r * gwx.abs().mean(1, keepdim=True))
+    _near(gx, want, tol, BF16, "grad_x")
+    _near(gw, (gy * x * r).sum(0), (T + H / 2 + 8) * U * (gy * x * r).abs().sum(0), F32, "grad_weight")
+
+
 @pytest.mark.parametrize("T,H", FAINT)
 @pytest.mark.parametrize("scale", [1e-15, 1e-22, 1e-30, 2.0 ** -130])
 def test_norm_backward_of_rows_whose_squares_vanish(T, H, scale):
     say(f"norm backward of faint rows T={T} H={H} scale={scale}")
     x, _, w = _faint(T, H, scale, T * 3 + H)
     gy = (torch.randn(T, H, generator=_gen(1)) * 2.0 ** -20).to(BF16)  # (2^130 times 1 would be infinite)
-    gx, gw = cgd.rms_norm_backward(_dev(gy), _dev(x), _dev(w), eps=0.0)
-    x, gy, w64 = x.to(F64), gy.to(F64), w.to(F64)
-    r = 1 / torch.sqrt((x * x).mean(1, keepdim=True))
-    gwx = gy * w64 * x
-    want = r * (gy * w64 - x * r * r * gwx.mean(1, keepdim=True))
-    tol = (2 * H + 16) * U * r * ((gy * w64).abs() + x.abs() * r * r * gwx.abs().mean(1, keepdim=True))
-    _near(gx, want, tol, BF16, "grad_x")
-    _near(gw, (gy * x * r).sum(0), (T + H / 2 + 8) * U * (gy * x * r).abs().sum(0), F32, "grad_weight")
+    _check_norm_backward(x, gy, w, 0.0)
+
+
+@pytest.mark.parametrize("T,H", FAINT)
+@pytest.mark.parametrize("scale", [1e18, 1e30, 3e37])
+def test_norm_backward_of_rows_whose_squares_overflow(T, H, scale):
+    """Rows that the norm gives zeros for, and ordinary ones: grad_y of 2^100 makes the
+    gradients large enough to see, and g x overflow as well."""
+    say(f"norm backward of large rows T={T} H={H} scale={scale}")
+    x, _, w = _faint(T, H, scale, T * 5 + H)
+    x = x.clamp(-3e38, 3e38)
+    gy = torch.randn(T, H, generator=_gen(2)).to(BF16)
+    gy[::2] *= 2.0 ** 100
+    _check_norm_backward(x, gy, w, 1e-6)
 
 
 def test_norm_of_zeros_without_eps():
