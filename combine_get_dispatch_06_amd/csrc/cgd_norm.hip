@@ -102,8 +102,8 @@ __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&o
 // all of them. It is taken again, kLift times as large: every bf16 value is a normal
 // number then, and so are the squares. That is done behind what every row goes through,
 // with its inputs loaded anew; where the sums are known it would keep apart what overlaps
-// otherwise (131040 x 128 1.3 us more, the gradient of 8000 x 4096 2). So to look for such
-// rows costs nothing that shows, but 2 us of the gradient of 10000 x 3200 (40).
+// otherwise (131040 x 128 1.3 us more, the gradient of 8000 x 4096 2). To look for such
+// rows shows in few widths: 1 us of the gradient of 10000 x 3200 (41) and 30000 x 1032 (51).
 constexpr float kFaint = 0x1p-100f, kLift = 0x1p100f;
 
 // V 16-byte vectors a lane, R rows one after the other (their loads together).
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
         some |= lost;
         const float r = rsqrtf(square);
         const float c = sums[1] * r * r * mean;  // times s: h mean(g h)
-        const float kept = there && !lost ? r : 0.0f;  // (r of no row may be infinite)
+        const bool kept = there && !lost;  // (r of no row may be infinite)
         const int twice = KEPT ? l : afresh(l);
 #pragma unroll
         for (int u = 0; u < V; ++u) {
@@ -336,11 +336,11 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
             const float(&wu)[8] = weights(u, twice);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                dw[u][i] = __builtin_fmaf(g[i] * kept, x[i], dw[u][i]);
+                if (kept) dw[u][i] = __builtin_fmaf(g[i] * r, x[i], dw[u][i]);
                 const float t = r * (g[i] * wu[i] - x[i] * c);
                 d[i] = a.grad_sum ? d[i] + t : t;
             }
-            if (a.grad_x && there && v < nvec && !lost) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
+            if (a.grad_x && kept && v < nvec) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
         }
     }
     // the lost rows, found by their sums once more

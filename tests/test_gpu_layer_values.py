@@ -175,3 +175,24 @@ def test_norm_of_zeros_without_eps():
     x[1] = 1e-30
     y = cgd.rms_norm(_dev(x), _dev(w), eps=0.0)
     assert y[0].isnan().all() and (y[1] == 1).all()
+
+
+@pytest.mark.parametrize("T,H", [(5, 64), (9, 256), (3, 512), (5, 1032), (600, 4096), (515, 8200), (3, 20480)])
+def test_norm_backward_of_an_infinite_gradient(T, H):
+    """It spoils its own row, and its own column of grad_weight, which is infinite. (That
+    row's other terms are added to grad_weight behind those of the other rows: an fp32
+    sum in another order, off by the same bound.)"""
+    say(f"norm backward of an infinite gradient T={T} H={H}")
+    g = _gen(T + H)
+    x, gy, w = torch.randn(T, H, generator=g).to(BF16), torch.randn(T, H, generator=g).to(BF16), torch.rand(H, generator=g) + 0.5
+    x[1, 3] = 1
+    clean = cgd.rms_norm_backward(_dev(gy), _dev(x), _dev(w))
+    gy[1, 3] = INF
+    size = x[:, 3:4].to(F64) ** 2
+    gx, gw = cgd.rms_norm_backward(_dev(gy), _dev(x), _dev(w))
+    rows, columns = torch.arange(T) != 1, torch.arange(H) != 3
+    assert not gx[1].isfinite().any() and torch.equal(gx[rows], clean[0][rows])
+    assert gw[3] == INF
+    x, gy = x[:, columns].to(F64), gy[:, columns].to(F64)
+    terms = gy * x / torch.sqrt(((x * x).sum(1, keepdim=True) + size) / H + 1e-6)
+    _near(gw.cpu()[columns], terms.sum(0), (T + H / 2 + 8) * U * terms.abs().sum(0), F32, "grad_weight")
