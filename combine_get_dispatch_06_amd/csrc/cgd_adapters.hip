@@ -1066,7 +1066,7 @@ hipError_t plan(const int64_t* index, int64_t tokens, int adapters, int32_t* off
     return hipGetLastError();
 }
 
-// own_plan: few tokens, and the kernel makes the tiles itself.
+// FEW: the kernel makes the tiles itself, and there is no plan.
 template <int MT, bool FEW, bool TURNED>
 void shrink_rank(const ShrinkArgs& s, hipStream_t stream) {
     const int nt = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : 4;

@@ -365,21 +365,6 @@ __device__ __forceinline__ void load_run(const uint16_t* p, int have, bool wide,
     }
 }
 
-// The sum of `splits` pieces, `slice` apart, in their order: four on their way at a time.
-__device__ __forceinline__ float4_t join_pieces(const float* p, int64_t slice, int splits) {
-    float4_t v = {0.f, 0.f, 0.f, 0.f};
-    int s = 0;
-    for (; s + 4 <= splits; s += 4) {
-        float4_t x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4_t*>(p + (s + u) * slice);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v += x[u];
-    }
-    for (; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(p + s * slice);
-    return v;
-}
-
 // The LDS rows (RB = 128 or 64 bytes) of a k-contiguous tile hold their 16-byte
 // pieces in an order that depends on the row: piece c of row r is at c ^ key(r),
 // so that the 16 rows a matrix instruction takes are spread over all banks (no

@@ -63,6 +63,20 @@ GemmPlan plan_forward(int64_t n, int glu, int64_t k, bool fp8, const Groups& g, 
 // and several are on their way at a time.
 constexpr int kJoinRows = 4;
 
+__device__ __forceinline__ float4_t join_pieces(const float* p, int64_t slice, int splits) {
+    float4_t v = {0.f, 0.f, 0.f, 0.f};
+    int s = 0;
+    for (; s + 4 <= splits; s += 4) {
+        float4_t x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = *reinterpret_cast<const float4_t*>(p + (s + u) * slice);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v += x[u];
+    }
+    for (; s < splits; ++s) v += *reinterpret_cast<const float4_t*>(p + s * slice);
+    return v;
+}
+
 __global__ __launch_bounds__(256) void join_kernel(const GemmArgs a) {
     const Piece pc = find_piece<true>(a.g, kJoinRows, (int)blockIdx.x);
     if (pc.group < 0) return;

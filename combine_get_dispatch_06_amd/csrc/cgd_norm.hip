@@ -8,7 +8,7 @@
 //   gradient, with g = dy w and h = s r:  ds = r (g - h mean(g h)) + d_sum,
 //   dw = sum over rows of dy h
 // Memory-bound: every input is read once into registers and every output written
-// once; a row's sums go over its lanes with shuffles and, where a row has more
+// once; a row's sums go over its lanes within the vector unit and, where a row has more
 // than a wave, over its waves through LDS.
 #include "cgd_gemm.h"
 #include "cgd_layer_launch.h"
