@@ -241,8 +241,9 @@ hipError_t norm_rows(const NormArgs& all, int threads, hipStream_t stream) {
             a.scales = static_cast<char*>(a.scales) + at / kFp8Block * (a.format == 2 ? 1 : 4);
         }
         const dim3 grid((unsigned)((a.rows + rows - 1) / rows)), block((unsigned)threads);
-        if (far)
-            hipLaunchKernelGGL((norm_kernel<LANES, V, R, true>), grid, block, 0, stream, a, threads);
+        // one vector a lane and one row at a time is for few rows, which are never far
+        if (far && (V > 1 || R > 1))
+            hipLaunchKernelGGL((norm_kernel<LANES, V, R, (V > 1 || R > 1)>), grid, block, 0, stream, a, threads);
         else
             hipLaunchKernelGGL((norm_kernel<LANES, V, R, false>), grid, block, 0, stream, a, threads);
     }
