@@ -34,42 +34,19 @@ __device__ __forceinline__ float4_t mul16(const bf16x8_t& rows, const bf16x8_t& 
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(rows, columns, sum, 0, 0, 0);
 }
 
-// v = hi + lo in bf16 pairs: of two values. A finite value that would round to an
-// infinity has the largest bf16 number as its first part; an infinity or NaN has no second.
+// v = hi + lo in bf16 pairs: of two values. Both parts have v's sign, and neither is 0 where
+// v is not (below 2^-103 the second may be): hi is what lies next below |v| in bf16, also
+// where v itself is a bf16 number, lo the rest, rounded (off by 2^-16 of v at most). So an
+// infinite operand gives infinities of one sign and no NaN, by 0 times it or by adding
+// two signs, and a value that would round to an infinity does not become one. Of an
+// infinity hi is the largest bf16 number and lo the infinity; of 0 (of either sign) both are 0.
 __device__ __forceinline__ void halves2(float a, float b, uint32_t* hi, uint32_t* lo) {
-    const float most = __uint_as_float(0x7F7F0000u);
-    const bool fa = fabsf(a) < __builtin_inff(), fb = fabsf(b) < __builtin_inff();
-    const uint32_t h = pack_bf16x2(fa ? __builtin_amdgcn_fmed3f(a, -most, most) : a, fb ? __builtin_amdgcn_fmed3f(b, -most, most) : b);
-    *hi = h;
-    *lo = pack_bf16x2(fa ? a - bf16_lo(h) : 0.0f, fb ? b - bf16_hi(h) : 0.0f);
+    a += 0.0f;  // -0 becomes 0
+    b += 0.0f;
+    const uint32_t ua = __builtin_elementwise_sub_sat(__float_as_uint(a), 1u), ub = __builtin_elementwise_sub_sat(__float_as_uint(b), 1u);
+    *hi = __builtin_amdgcn_perm(ub, ua, 0x07060302u);  // the upper halves
+    *lo = pack_bf16x2(a - __uint_as_float(ua & 0xFFFF0000u), b - __uint_as_float(ub & 0xFFFF0000u));
 }
-
-// An infinite operand times a part of 0, or infinities of both signs from two parts of
-// opposite sign, would be NaN where v times it is infinite. So the second parts take
-// infinities (and NaN, which the first parts pass on) as 0: where NaN is found among the
-// sums, they are added up afresh like that. Looking costs 0.3 us of the 26 and of the 16
-// that the second products of 4093 tokens of rank 64 and 4095 of rank 16 take.
-__device__ __forceinline__ bf16x8_t without_infinities(const bf16x8_t& v) {
-    uint4_t q = __builtin_bit_cast(uint4_t, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if ((q[i] & 0x7F80u) == 0x7F80u) q[i] &= 0xFFFF0000u;
-        if ((q[i] & 0x7F800000u) == 0x7F800000u) q[i] &= 0xFFFFu;
-    }
-    return __builtin_bit_cast(bf16x8_t, q);
-}
-template <int M, int N>
-__device__ __forceinline__ bool any_nan(const float4_t (&sums)[M][N]) {  // in the wave
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < M; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            found |= __builtin_isunordered(sums[i][j][0], sums[i][j][1]) | __builtin_isunordered(sums[i][j][2], sums[i][j][3]);
-    return ballot(found) != 0;
-}
-struct Quick { static constexpr bool careful = false; };
-struct Careful { static constexpr bool careful = true; };
 
 // ---- order of the tokens ---------------------------------------------------
 
@@ -686,39 +663,6 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
         for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int p = 0; p < FT; ++p) acc[t][p] = float4_t{0.f, 0.f, 0.f, 0.f};
-        auto multiply = [&](int k, auto way) {
-            const int piece = KS ? k * 4 + g : g & 1;
-            bf16x8_t wf[FT];
-#pragma unroll
-            for (int p = 0; p < FT; ++p) {
-                if constexpr (TURNED)
-                    wf[p] = turned((const CGD_LDS(char)*)(mine + place((piece * 8 + (n >> 2)) * PR + p * 2 + (n >> 1 & 1)) + (n & 1) * 8), 4 * F * 2);
-                else
-                    wf[p] = get16(mine + place((p * 16 + n) * PR + piece));
-            }
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                if constexpr (KS > 0) {
-                    const bf16x8_t hi = get16(&parts[0][t * 16 + n][k * 32 + g * 8]), lo = get16(&parts[1][t * 16 + n][k * 32 + g * 8]);
-#pragma unroll
-                    for (int p = 0; p < FT; ++p) {
-                        if constexpr (way.careful)
-                            acc[t][p] = mul16(without_infinities(wf[p]), lo, mul16(wf[p], hi, acc[t][p]));
-                        else
-                            acc[t][p] = mul16(wf[p], lo, mul16(wf[p], hi, acc[t][p]));
-                    }
-                } else {
-                    const bf16x8_t h = get16(&parts[g >> 1][t * 16 + n][(g & 1) * 8]);
-#pragma unroll
-                    for (int p = 0; p < FT; ++p) {
-                        if constexpr (way.careful)
-                            acc[t][p] = mul16(g >> 1 ? without_infinities(wf[p]) : wf[p], h, acc[t][p]);
-                        else
-                            acc[t][p] = mul16(wf[p], h, acc[t][p]);
-                    }
-                }
-            }
-        };
         if (!none) {
 #pragma unroll
             for (int i = 0; i < LOADS; ++i) put16(mine + place(i * 64 + lane), stage[i]);
@@ -726,14 +670,28 @@ __global__ __launch_bounds__(256, KS <= 2 ? 2 : 1) void adapter_expand_kernel(co
             if (o0 + 4 * F < end) load(o0 + 4 * F);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int k = 0; k < KN; ++k) multiply(k, Quick());
-            if (any_nan(acc)) {
+            for (int k = 0; k < KN; ++k) {
+                const int piece = KS ? k * 4 + g : g & 1;
+                bf16x8_t wf[FT];
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
+                for (int p = 0; p < FT; ++p) {
+                    if constexpr (TURNED)
+                        wf[p] = turned((const CGD_LDS(char)*)(mine + place((piece * 8 + (n >> 2)) * PR + p * 2 + (n >> 1 & 1)) + (n & 1) * 8), 4 * F * 2);
+                    else
+                        wf[p] = get16(mine + place((p * 16 + n) * PR + piece));
+                }
 #pragma unroll
-                    for (int p = 0; p < FT; ++p) acc[t][p] = float4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                for (int k = 0; k < KN; ++k) multiply(k, Careful());
+                for (int t = 0; t < MT; ++t) {
+                    if constexpr (KS > 0) {
+                        const bf16x8_t hi = get16(&parts[0][t * 16 + n][k * 32 + g * 8]), lo = get16(&parts[1][t * 16 + n][k * 32 + g * 8]);
+#pragma unroll
+                        for (int p = 0; p < FT; ++p) acc[t][p] = mul16(wf[p], lo, mul16(wf[p], hi, acc[t][p]));
+                    } else {
+                        const bf16x8_t h = get16(&parts[g >> 1][t * 16 + n][(g & 1) * 8]);
+#pragma unroll
+                        for (int p = 0; p < FT; ++p) acc[t][p] = mul16(wf[p], h, acc[t][p]);
+                    }
+                }
             }
         }
         // a lane has four consecutive features of one token; b's rows are in registers by now
@@ -813,7 +771,7 @@ struct AdapterWeightArgs {
 // join). The next tokens on their way, at half as many waves: 23.6; grad_b's blocks in
 // the first product's launch: 42 for both and grad_a, where they take 38 one by one.
 template <int RT, int NW, bool FEW>
-__global__ __launch_bounds__(NW* kWave, RT == 1 ? 4 : 1) void adapter_weight_kernel(const AdapterWeightArgs w) {
+__global__ __launch_bounds__(NW* kWave) void adapter_weight_kernel(const AdapterWeightArgs w) {
     extern __shared__ __attribute__((aligned(16))) float4_t joined[];  // [wave][RT * 8][lane]
     __shared__ int own[FEW ? kFewTokens : 1], bounds[2];
     const int lane = lane_id(), wave = threadIdx.x / kWave, n = lane & 15, g = lane >> 4;
@@ -875,7 +833,7 @@ __global__ __launch_bounds__(NW* kWave, RT == 1 ? 4 : 1) void adapter_weight_ker
             for (int r = 0; r < RT; ++r) s.v[r][i] = at[rank_at[r]];
         }
     };
-    auto multiply = [&](Step& s, int p0, auto way) {
+    auto multiply = [&](Step& s, int p0) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -907,28 +865,13 @@ __global__ __launch_bounds__(NW* kWave, RT == 1 ? 4 : 1) void adapter_weight_ker
             }
             const bf16x8_t f = __builtin_bit_cast(bf16x8_t, uint4_t{q[0], q[1], q[2], q[3]});
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                if constexpr (way.careful)
-                    acc[r][c] = mul16(lo[r], without_infinities(f), mul16(hi[r], f, acc[r][c]));
-                else
-                    acc[r][c] = mul16(lo[r], f, mul16(hi[r], f, acc[r][c]));
-            }
+            for (int r = 0; r < RT; ++r) acc[r][c] = mul16(lo[r], f, mul16(hi[r], f, acc[r][c]));
         }
     };
     Step s;
     for (int p0 = begin + wave * 32; p0 < end; p0 += NW * 32) {
         load(s, p0);
-        multiply(s, p0, Quick());
-    }
-    if (any_nan(acc)) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int c = 0; c < 8; ++c) acc[r][c] = float4_t{0.f, 0.f, 0.f, 0.f};
-        for (int p0 = begin + wave * 32; p0 < end; p0 += NW * 32) {
-            load(s, p0);
-            multiply(s, p0, Careful());
-        }
+        multiply(s, p0);
     }
     // the upper half of the waves that had tokens gives its sums to the lower, until one has them
     const int most = (end - begin + 31) / 32;
