@@ -948,11 +948,18 @@ struct Room {  // places in the workspace
 };
 
 bool few(int64_t tokens) { return tokens <= kFewTokens; }
+// Tiles of 32 tokens read an adapter's weights half as often, but there are half as many,
+// and one of an adapter with few tokens is padded more. us with 16 and 32 rows, 4096 -> 4096
+// with a residual unless said otherwise: 1024 tokens of 8 adapters, rank 16 18.4 and 18.6, rank
+// 64 27.1 and 28.2, of 64 adapters, rank 16 19.4 and 22.6; 2048 of 8, rank 64 33.3 and 35.6; 4093
+// of 8, rank 64, 7168 -> 4096 53.6 and 51.4, its gradient 93.5 and 87.6; 16384 of 16, rank 16 137 and 133.
 int tile_tokens(int64_t tokens) { return tokens >= 1024 ? kTallTile : kTile; }
 int64_t tile_slots(int64_t tokens, int adapters) { return tokens / tile_tokens(tokens) + adapters + 1; }
 
 // Pieces of the reduction: until there are some two blocks for a CU, of at least
-// 64 for each of a block's waves.
+// 64 for each of a block's waves. us with half as many blocks, these, and twice as many: 2048
+// tokens of 8 adapters, rank 64, 4096 -> 4096 33.8, 35.6, 37.9; 4093, rank 64, 7168 -> 4096 49.9, 51.4, 51.9;
+// 4095 of 16, rank 16, 4096 -> 7168 45.0, 43.5, 44.0, its gradient 57.1, 54.5, 55.9; 8192 of 8, rank 64 79.1, 74.6, 76.9.
 int64_t shrink_piece(int64_t tokens, int rank, int64_t in) {
     const int64_t tiles = (tokens + tile_tokens(tokens) - 1) / tile_tokens(tokens) * ((rank + 63) / 64);
     int64_t pieces = (rank > 32 ? 768 : 640) / (tiles > 0 ? tiles : 1);
@@ -974,6 +981,10 @@ int64_t chunk_count(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
 // 16 772 and 511, rank 64 955 and 814; 16384, rank 16 224 and 149. From a block for every
 // second CU on they cost more than they give (16384 tokens of two, rank 64: 207 and 237),
 // and below 1536 tokens of an adapter the launch does (1024 of one, rank 16: 25 and 26.5).
+// The host does not know how the tokens are spread and takes it for even. Where all are one
+// adapter's, that one's blocks have all the work: 16384 tokens, rank 16, of 8, 32 and 64
+// adapters 227, 325 and 324 (spread evenly 147, 152 and 161), 4096 79, 79 and 80 (45, 47 and 52);
+// rank 64, 16384 tokens of 32 387 (270).
 int64_t weight_shares(int64_t tokens, int adapters, int rank, int64_t in, int64_t out) {
     const int64_t blocks = ((in + 127) / 128 + (out + 127) / 128) * adapters * ((rank + 31) / 32);
     if (blocks > 128 || tokens < int64_t(1536) * adapters) return 1;
@@ -1044,6 +1055,10 @@ template <bool TURNED>
 void expand(ExpandArgs e, hipStream_t stream) {
     const int tile = tile_tokens(e.tokens), step = e.rank <= 128 ? 256 : 128;  // features of a block's waves at a time
     const int64_t tiles = (e.tokens + tile - 1) / tile, steps = e.out ? (e.width + step - 1) / step : 1;
+    // Every chunk's block joins the same pieces first, so more blocks are not always better. us with
+    // half as many, these, and twice as many: 1024 tokens of 8 adapters, rank 64, 4096 -> 4096 27.5, 28.2,
+    // 33.8; 2048 36.4, 35.6, 42.0; 4093, 7168 -> 4096 54.6, 51.4, 55.5; 4095 of 16, rank 16, 4096 -> 7168 44.1, 43.5,
+    // 43.8; 8192 of 8, rank 64 72.4, 74.6, 66.6; 16384 of 16, rank 16 134, 133, 125.
     int64_t chunks = ((e.rank > 32 ? 384 : 640) + tiles - 1) / tiles;
     if (chunks > steps) chunks = steps;
     e.chunk = (steps + chunks - 1) / chunks * step;

@@ -73,7 +73,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // FAR: what the call touches does not fit the Infinity Cache, so nothing of it is worth
 // keeping there: non-temporal accesses. 4096 x 7168 with residual and FP8 (265 MB)
 // 46.7 us against 54, its gradient (235 MB) 42.6 against 48.8; 131040 x 128 (67 MB) 13.6
-// against 11.8.
+// against 11.8. That is the call alone. With ordinary stores (and the same loads) it takes
+// 48.5 for 47.5, with 8192 rows 85.6 for 90.2, and what reads y next is faster: norm, gate and
+// dispatch of 4096 rows 142 for 152 (8192: 270 for 267), bf16 norm and gate of 8192 121 for 134.
 constexpr int64_t kFarBytes = int64_t(160) << 20;
 template <bool FAR>
 __device__ __forceinline__ uint4 take(const uint4* p) {
@@ -263,7 +265,7 @@ __device__ __forceinline__ bool is_lost(float square, float dot) {
 template <int LANES, int V, bool FAR>
 __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void norm_grad_kernel(const NormGradArgs a, int threads) {
     constexpr int GROUPS = LANES ? 256 / LANES : 1;
-    constexpr bool KEPT = V < 4;  // room for the weights in registers: four vectors spill (1000 x 32768: 104 us for 60)
+    constexpr bool KEPT = V < 4;  // room for the weights in registers: four vectors spill (1000 x 32768: 126 us for 62)
     __shared__ float slot[2][kMaxWaves][2];
     const int nvec = a.width / 8;
     const int step = LANES ? LANES : threads;
@@ -481,7 +483,10 @@ int gradient_vectors(int width) { return width <= 8192 ? 1 : width <= 16384 ? 2 
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream) {
     if (a.rows == 0) return hipSuccess;
     const int w = a.width;
-    if (w <= 512) {  // several rows a block; many rows: two at a time
+    // Several rows a block; many rows: two at a time. us with one and two: 66000 x 128 with a residual
+    // 12.3 and 11.1, 131040 x 128 13.2 and 13.0, with a residual 21.7 and 20.2, 33000 x 512 with one 22.0 and
+    // 20.6; but 262144 x 128 with a residual 39.6 and 43.3, and to FP8 33000 x 512 13.1 and 14.6.
+    if (w <= 512) {
         const int lanes = w <= 128 ? 16 : w <= 256 ? 32 : 64;
         const bool many = a.rows * lanes >= int64_t(256) * 2048 * kRowsTogether;
         if (lanes == 16) return many ? norm_rows<16, 1, kRowsTogether>(a, 256, stream) : norm_rows<16, 1>(a, 256, stream);
