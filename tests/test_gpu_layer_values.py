@@ -148,6 +148,16 @@ def _check_norm_backward(x, gy, w, eps):
 
 
 @pytest.mark.parametrize("T,H", FAINT)
+def test_norm_of_rows_whose_squares_vanish_in_place(T, H):
+    x, r, w = map(_dev, _faint(T, H, 1e-30, T - H))
+    y, total = cgd.rms_norm(x, w, eps=0.0, residual=r)
+    for over in (0, 1):
+        terms = [x.clone(), r.clone()]
+        y2, s2 = cgd.rms_norm(terms[0], w, eps=0.0, residual=terms[1], sum_out=terms[over])
+        assert s2 is terms[over] and torch.equal(s2, total) and torch.equal(y2, y)
+
+
+@pytest.mark.parametrize("T,H", FAINT)
 @pytest.mark.parametrize("scale", [1e-15, 1e-22, 1e-30, 2.0 ** -130])
 def test_norm_backward_of_rows_whose_squares_vanish(T, H, scale):
     say(f"norm backward of faint rows T={T} H={H} scale={scale}")
