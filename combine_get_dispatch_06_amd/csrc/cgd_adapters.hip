@@ -978,7 +978,7 @@ int64_t chunk_count(int64_t tokens) { return (tokens + kChunk - 1) / kChunk; }
 // Shares of an adapter's tokens in its gradients, each with blocks of its own and sums
 // that another kernel adds: few adapters with many tokens would leave CUs idle. us of a
 // whole gradient without and with shares, 4096 -> 4096: 65536 tokens of one adapter, rank
-// 16 772 and 511, rank 64 955 and 814; 16384, rank 16 224 and 149. From a block for every
+// 16 772 and 511, rank 64 955 and 773; 16384, rank 16 224 and 149. From a block for every
 // second CU on they cost more than they give (16384 tokens of two, rank 64: 207 and 237),
 // and below 1536 tokens of an adapter the launch does (1024 of one, rank 16: 25 and 26.5).
 // The host does not know how the tokens are spread and takes it for even. Where all are one

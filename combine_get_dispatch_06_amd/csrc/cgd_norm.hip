@@ -105,7 +105,7 @@ __device__ __forceinline__ void weight8(const void* w, int f32, int v, float (&o
 // number then, and so are the squares. That is done behind what every row goes through,
 // with its inputs loaded anew; where the sums are known it would keep apart what overlaps
 // otherwise (131040 x 128 1.3 us more, the gradient of 8000 x 4096 2). To look for such
-// rows shows in few widths: 1 us of the gradient of 10000 x 3200 (41) and 30000 x 1032 (51).
+// rows shows in few widths: 1 to 2 us of the gradient of 10000 x 3200 (42) and 30000 x 1032 (53).
 constexpr float kFaint = 0x1p-100f, kLift = 0x1p100f;
 
 // V 16-byte vectors a lane, R rows one after the other (their loads together).

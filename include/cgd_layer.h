@@ -53,7 +53,8 @@ int cgd_rms_norm_backward(const void* grad_y, const void* x, const void* weight,
  *   out           bf16 [num_tokens, out_features]; may be residual itself, no other input
  *   hidden        fp32 [num_tokens, rank] out or NULL: a[j] x[t] (0 without an adapter), as the
  *                 gradient takes it
- * a[j] x[t] is kept to 2^-16 of itself and out is rounded once. rank: a multiple of 8 up to 256 (pad
+ * a[j] x[t] is kept to 2^-16 of itself and out is rounded once. (Where it is a projection's residual,
+ * cgd_linear rounds the sum of both once more.) rank: a multiple of 8 up to 256 (pad
  * smaller ones with zeros); num_adapters in [1,512]; num_tokens up to 2^26; in_features a multiple of 8
  * up to 2^20. x, a, b, residual, out and hidden 16-byte aligned. */
 size_t cgd_adapter_linear_workspace_bytes(int64_t num_tokens, int num_adapters, int rank, int64_t in_features,
