@@ -183,3 +183,62 @@ def test_adapters_of_one_request(T, J, R):
     want, tol = _adapters_grad64(c, hidden.cpu())
     for name, v, x, t in zip(("grad_x", "grad_a", "grad_b"), got, want, tol):
         _near(v, x, t, BF16, name)
+
+
+# ---------------------------------------------------------------------------
+# The largest sizes that are documented
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,J,R,I,O", [(3, 2, 8, 1 << 20, 24), (70, 2, 8, 1 << 20, 72), (3, 2, 16, 72, 1 << 20), (300, 2, 8, 24, 1 << 20), (3, 512, 256, 64, 40),
+                                       (300, 512, 256, 40, 64)])
+def test_adapters_of_the_largest_sizes(T, J, R, I, O):
+    say(f"adapters of the largest sizes T={T} J={J} R={R} I={I} O={O}")
+    c = _case(T, J, R, I, O, 0.1, 0, T + R)
+    c["idx"][0] = J - 1
+    d = {k: _dev(v) for k, v in c.items()}
+    out, hidden = cgd.adapter_linear(d["x"], d["a"], d["b"], d["idx"], scale=d["scale"], residual=d["res"], return_hidden=True)
+    h, y, th, ty = _adapters64(c, c["res"])
+    _near(hidden, h, th, F32, "hidden")
+    _near(out, y, ty, BF16, "out")
+    got = cgd.adapter_linear_backward(d["grad"], d["x"], d["a"], d["b"], d["idx"], hidden, scale=d["scale"])
+    want, tol = _adapters_grad64(c, hidden.cpu())
+    for name, v, x, t in zip(("grad_x", "grad_a", "grad_b"), got, want, tol):
+        _near(v, x, t, BF16, name)
+
+
+def test_adapters_of_the_most_tokens():
+    """2^26 tokens whose sums are whole numbers below 2^24, so that fp32 holds them."""
+    T, J, R, I = 1 << 26, 5, 8, 8
+    say(f"adapters of the most tokens T={T}")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    idx = torch.randint(-1, J, (T,), generator=g, device=DEV)
+    place = torch.randint(I, (T,), generator=g, device=DEV)
+    x = torch.zeros(T, I, dtype=BF16, device=DEV)
+    x.scatter_(1, place[:, None], 1.0)  # one 1 a row
+    one = torch.eye(8, device=DEV)
+    a = torch.stack([one.roll(j, 0) for j in range(J)]).to(BF16)  # h = x rolled by j
+    b = torch.stack([one * (j + 1) for j in range(J)]).to(BF16)
+    out, hidden = cgd.adapter_linear(x, a, b, idx, return_hidden=True)
+    on = idx >= 0
+    for first in range(0, T, 1 << 22):
+        part = slice(first, first + (1 << 22))
+        j = idx[part].clamp_min(0)
+        want = torch.zeros(1 << 22, R, device=DEV).scatter_(1, ((place[part] + j) % R)[:, None], 1.0) * on[part][:, None]
+        assert torch.equal(hidden[part], want), first
+        assert torch.equal(out[part].float(), want * (j + 1)[:, None]), first
+    del out
+    gx, ga, gb = cgd.adapter_linear_backward(x, x, a, b, idx, hidden)
+    del hidden
+    for first in range(0, T, 1 << 22):
+        part = slice(first, first + (1 << 22))
+        j = idx[part].clamp_min(0)
+        want = torch.zeros(1 << 22, I, device=DEV).scatter_(1, ((place[part] - j) % R)[:, None], 1.0) * ((j + 1) * on[part])[:, None]
+        assert torch.equal(gx[part].float(), want), first
+    count = torch.zeros(J, I, dtype=torch.int64, device=DEV)  # tokens by adapter and place
+    count.view(-1).index_add_(0, (idx * I + place)[on], torch.ones(int(on.sum()), dtype=torch.int64, device=DEV))
+    assert int(count.max()) * J < 1 << 24
+    for j in range(J):
+        want_a = torch.diag(count[j].double() * (j + 1))
+        want_b = torch.zeros(I, R, dtype=F64, device=DEV)
+        want_b[torch.arange(I), (torch.arange(I) + j) % R] = count[j].double()
+        assert torch.equal(ga[j], want_a.to(F32).to(BF16)) and torch.equal(gb[j], want_b.to(F32).to(BF16)), j
