@@ -321,7 +321,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
         // two sets of slots: a wave may be one sum ahead of another's reads, not two
         row_sums<LANES>(sums, threads, slot[turn]);
         turn ^= 1;
-        const float square = sums[0] * mean + a.eps;
+        const float square = __builtin_fmaf(sums[0], mean, a.eps);
         const bool lost = is_lost(square, sums[1]) && there;
         some |= lost;
         const float r = rsqrtf(square);
@@ -346,7 +346,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
             if (a.grad_x && kept && v < nvec) reinterpret_cast<uint4*>(a.grad_x)[base + v] = pack8(d);
         }
     }
-    // the lost rows, found by their sums once more
+    // the lost rows, found by the same sums once more: the same operations, so the same rows
     if (ballot(some) != 0) {
         for (row0 = (int64_t)blockIdx.x * GROUPS; row0 < a.rows; row0 += (int64_t)gridDim.x * GROUPS) {
             const int64_t row = row0 + mine, base = row * nvec;
@@ -377,7 +377,7 @@ __global__ __launch_bounds__(LANES ? 256 : 1024, LANES ? 1 : V > 1 ? 4 : 8) void
             };
             float sums[2];
             add_up(1.0f, sums);
-            float square = sums[0] * mean + a.eps;
+            float square = __builtin_fmaf(sums[0], mean, a.eps);
             if (!is_lost(square, sums[1]) || !there) continue;  // (the same for all lanes of the row)
             const float lift = square < kFaint ? kLift : square < __builtin_inff() ? 0x1p-40f : 0x1p-112f;
             add_up(lift, sums);
